@@ -52,7 +52,9 @@ typedef enum attn_status {
     ATTN_ERR_UNSUPPORTED = 2,    /* valid for eq. (1) but outside what this build runs
                                     (e.g. a head size the bf16 kernel has no variant for) */
     ATTN_ERR_CUDA = 3,           /* a CUDA runtime/driver call failed; see attn_last_cuda_error() */
-    ATTN_ERR_DEVICE_TIMEOUT = 4  /* a kernel's bounded wait ran out (attn_get_device_status) */
+    ATTN_ERR_DEVICE_TIMEOUT = 4, /* a kernel's bounded wait ran out (attn_get_device_status) */
+    ATTN_ERR_DEVICE_INDEX = 5    /* a page index, or a new token's position, was out of range: its
+                                    row was left out (attn_get_device_status) */
 } attn_status;
 
 /* mask_kind bit flags */
@@ -468,10 +470,147 @@ attn_status attn_decode_host_async(const void *q_host, const void *k_cache,
                                    void *workspace, size_t workspace_bytes, tsd_stream_t stream);
 
 /*
+ * Paged key/value caches. The rows of B sequences live in a pool of pages
+ * that the caller hands out: row p of sequence b is slot p % page_size of
+ * page page_table[b * max_pages + p / page_size]. ("Attention Is All You Need
+ * 해부" (sj-techlog), section "KV cache는 추론의 같은 계산을 반복하지 않게
+ * 한다", gives the cache itself; pages, grouped heads, the rotation and the
+ * 4-bit form are this library's.)
+ *
+ *   page_table  device int32[B, max_pages]; entries past a sequence's last
+ *               row are never read
+ *   page_size   a power of two, 16..256 (other powers -> ATTN_ERR_UNSUPPORTED);
+ *               max_pages * page_size <= 2^30, else ATTN_ERR_UNSUPPORTED
+ *   cache_lens  device int32[B]: rows of each sequence, the new tokens included
+ *   new_lens    device int32[B]: how many of the call's n_new (n_q) tokens
+ *               sequence b really has, clamped to [0, n_new]; NULL: all.
+ *               Token t < new_lens[b] sits at position
+ *               cache_lens[b] - new_lens[b] + t; the tokens past them are padding.
+ *   h_kv        key/value heads, a divisor of h: query head i reads key head
+ *               i / (h / h_kv)
+ *   d           64 or 128 (else ATTN_ERR_UNSUPPORTED), of keys and values
+ *
+ * A bf16 cache is two pools [n_pages, h_kv, page_size, d] of bf16. A 4-bit
+ * cache holds each of keys and values as
+ *   codes   uint8 [n_pages, h_kv, page_size, d / 2]: two per byte, the even
+ *           column in the low half. A code is a sign bit, two exponent bits
+ *           and a mantissa bit (e2m1): 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives
+ *   scales  uint8 [n_pages, h_kv, page_size, d / 16]: an e4m3 number for each
+ *           16 columns
+ * and a factor f for the whole pool: value = code * scale * f. Values up to
+ * 6 * 448 * f can be held; 2^-100 <= f <= 2^100, else ATTN_ERR_INVALID. All
+ * pools are device memory, contiguous, 16-byte aligned.
+ *
+ * A page index outside [0, n_pages) where a row is needed: nothing is read
+ * or written through it, that row takes no part, and attn_get_device_status
+ * answers ATTN_ERR_DEVICE_INDEX once.
+ */
+enum {
+    ATTN_ROPE_NONE = 0,
+    ATTN_ROPE_HALVES = 1, /* columns i and i + rope_dim / 2 are a pair */
+    ATTN_ROPE_PAIRS = 2   /* columns 2 i and 2 i + 1 are a pair */
+};
+
+/*
+ * attn_cache_append -- writes the new tokens' keys and values into their
+ * pages, the keys rotated by their positions, and returns the queries rotated
+ * in the same way, in the layout that attn_decode_paged reads. Pair i of a
+ * query's or key's first rope_dim columns, (x, y), becomes
+ *   (x cos - y sin, y cos + x sin)
+ * with the cosine and sine of the token's position; columns past rope_dim
+ * and values are taken as they are. fp32, rounded once to bf16.
+ *
+ *   q   bf16, element (b, head, t, col) at b q_sb + head q_sh + t q_sr + col
+ *       (strides in elements, multiples of 8, >= 0): a projection's output
+ *       [B, n_new, h * d] has (n_new h d, d, h d). NULL (with q_out NULL): no queries
+ *   k, v  likewise with kv_sb, kv_sh, kv_sr, h_kv heads
+ *   q_out [B, h, n_new, d] bf16; may be q itself where q has that layout
+ *   k_out [B, h_kv, n_new, d] bf16: the rotated keys, for attn_forward over
+ *       a prompt; NULL: not wanted
+ *   rope  device fp32 [rope_rows, rope_dim], 16-byte aligned: row p holds
+ *       position p's rope_dim / 2 cosines, then their sines; ignored with
+ *       ATTN_ROPE_NONE. rope_dim: even, <= d (else ATTN_ERR_INVALID), and a
+ *       multiple of 32 (else ATTN_ERR_UNSUPPORTED)
+ * Nothing is written for padding tokens or for tokens at negative positions.
+ * A token whose position has no page table entry, no valid page or (when
+ * rotated) no row in `rope` is left out whole, as the section above says.
+ * Tokens of one call may not share a slot of a page. Errors as attn_forward.
+ * One launch.
+ */
+attn_status attn_cache_append(const void *q, int64_t q_sb, int64_t q_sh, int64_t q_sr,
+                              const void *k, const void *v,
+                              int64_t kv_sb, int64_t kv_sh, int64_t kv_sr,
+                              void *q_out, void *k_out, void *k_cache, void *v_cache,
+                              const int32_t *page_table, const int32_t *cache_lens,
+                              const int32_t *new_lens,
+                              const float *rope, int rope_rows, int rope_dim, int rope_kind,
+                              int B, int h, int h_kv, int n_new, int d,
+                              int n_pages, int page_size, int max_pages, tsd_stream_t stream);
+
+/*
+ * attn_cache_append_q4 -- attn_cache_append into a 4-bit cache. For each 16
+ * columns of a key (after the rotation, in fp32) or value x:
+ *   scale = max|x| / (6 f) rounded to e4m3, at most 448;
+ *   code  = x / (scale f) rounded to e2m1, at most 6 in magnitude
+ * both to nearest, ties to even. Columns holding an infinity or a NaN make
+ * their scale a NaN; a scale that rounds to 0 makes its codes 0. q_out and
+ * k_out are bf16 as above.
+ */
+attn_status attn_cache_append_q4(const void *q, int64_t q_sb, int64_t q_sh, int64_t q_sr,
+                                 const void *k, const void *v,
+                                 int64_t kv_sb, int64_t kv_sh, int64_t kv_sr,
+                                 void *q_out, void *k_out,
+                                 void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                                 float k_factor, float v_factor,
+                                 const int32_t *page_table, const int32_t *cache_lens,
+                                 const int32_t *new_lens,
+                                 const float *rope, int rope_rows, int rope_dim, int rope_kind,
+                                 int B, int h, int h_kv, int n_new, int d,
+                                 int n_pages, int page_size, int max_pages, tsd_stream_t stream);
+
+/*
+ * attn_decode_paged -- attn_decode over a paged cache with grouped heads.
+ *   q, out  [B, h, n_q, d] bf16; 1 <= n_q <= 8 (more -> ATTN_ERR_UNSUPPORTED)
+ *   cache_lens  as above, clamped to [0, max_pages * page_size]; NULL: that many
+ *   mask_kind   ATTN_MASK_CAUSAL: query t sees the rows at positions <=
+ *       cache_lens[b] - new_lens[b] + t, its own (the new tokens' keys are in
+ *       the cache already). ATTN_MASK_NONE: every query sees all cache_lens[b]
+ *       rows (cross-attention to encoder states kept in a cache). Others ->
+ *       ATTN_ERR_INVALID
+ *   scale       0 -> 1/sqrt(d)
+ *   workspace   device, 16-byte aligned, >= attn_decode_paged_workspace_bytes(...)
+ *       bytes of scratch (0 for sizes that the call refuses)
+ * Rows of `out` that see no row, padding tokens' among them, are 0. Rows at
+ * or past cache_lens[b] are never used, whatever they hold. Errors as
+ * attn_decode.
+ */
+size_t attn_decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
+                                         int max_pages);
+attn_status attn_decode_paged(const void *q, const void *k_cache, const void *v_cache, void *out,
+                              const int32_t *page_table, const int32_t *cache_lens,
+                              const int32_t *new_lens,
+                              int B, int h, int h_kv, int n_q, int d,
+                              int n_pages, int page_size, int max_pages,
+                              int mask_kind, float scale,
+                              void *workspace, size_t workspace_bytes, tsd_stream_t stream);
+
+/* attn_decode_paged_q4 -- attn_decode_paged over a 4-bit cache. */
+attn_status attn_decode_paged_q4(const void *q, const void *k_codes, const void *k_scales,
+                                 const void *v_codes, const void *v_scales,
+                                 float k_factor, float v_factor, void *out,
+                                 const int32_t *page_table, const int32_t *cache_lens,
+                                 const int32_t *new_lens,
+                                 int B, int h, int h_kv, int n_q, int d,
+                                 int n_pages, int page_size, int max_pages,
+                                 int mask_kind, float scale,
+                                 void *workspace, size_t workspace_bytes, tsd_stream_t stream);
+
+/*
  * attn_get_device_status -- synchronises `stream`, then reads and clears the
- * device error word the kernels set when a bounded wait runs out.
- * Returns ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT, or ATTN_ERR_CUDA if the
- * synchronisation itself failed.
+ * device error words the kernels set when a bounded wait runs out or a page
+ * index or position is out of range. Returns ATTN_OK,
+ * ATTN_ERR_DEVICE_TIMEOUT (also where both happened), ATTN_ERR_DEVICE_INDEX,
+ * or ATTN_ERR_CUDA if the synchronisation itself failed.
  */
 attn_status attn_get_device_status(tsd_stream_t stream);
 

@@ -18,7 +18,7 @@ from . import build as _build
 
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_CUDA",
-    "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_MASK_NONE", "ATTN_MASK_CAUSAL", "ATTN_MASK_KEY_PADDING",
+    "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_ERR_DEVICE_INDEX", "ATTN_MASK_NONE", "ATTN_MASK_CAUSAL", "ATTN_MASK_KEY_PADDING",
     "AttnError", "library", "library_path", "EXPORTED_SYMBOLS",
     "attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_workspace_bytes",
     "mha_forward", "attn_get_device_status", "attn_last_cuda_error", "attn_status_string",
@@ -30,10 +30,15 @@ __all__ = [
     "encoder_layer_forward_host", "attn_decode_host_workspace_bytes", "attn_decode_host",
     "attn_forward_window_host", "mha_forward_host_async", "attn_host_join",
     "attn_decode_host_async", "encoder_layer_forward_host_async",
+    "ATTN_ROPE_NONE", "ATTN_ROPE_HALVES", "ATTN_ROPE_PAIRS", "attn_cache_append",
+    "attn_cache_append_q4", "attn_decode_paged_workspace_bytes", "attn_decode_paged",
+    "attn_decode_paged_q4",
 ]
 
-ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DEVICE_TIMEOUT = range(5)
+ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DEVICE_TIMEOUT, \
+    ATTN_ERR_DEVICE_INDEX = range(6)
 ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_KEY_PADDING = 0, 1, 2
+ATTN_ROPE_NONE, ATTN_ROPE_HALVES, ATTN_ROPE_PAIRS = 0, 1, 2
 
 EXPORTED_SYMBOLS = (
     "attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_workspace_bytes",
@@ -45,7 +50,8 @@ EXPORTED_SYMBOLS = (
     "mha_forward_host", "encoder_layer_host_workspace_bytes", "encoder_layer_forward_host",
     "attn_decode_host_workspace_bytes", "attn_decode_host", "attn_forward_window_host",
     "mha_forward_host_async", "attn_host_join", "attn_decode_host_async",
-    "encoder_layer_forward_host_async",
+    "encoder_layer_forward_host_async", "attn_cache_append", "attn_cache_append_q4",
+    "attn_decode_paged_workspace_bytes", "attn_decode_paged", "attn_decode_paged_q4",
 )
 
 # TSD_MHA_NOALLOC_SCRATCH_BYTES of the header: the fixed scratch of mha_forward_noalloc
@@ -122,8 +128,17 @@ def library():
     lib.encoder_layer_forward_host_async.argtypes = lib.encoder_layer_forward_host.argtypes
     lib.attn_decode_host.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp, f, vp, sz, st]
     lib.attn_decode_host_async.argtypes = [vp, vp, vp, vp, i, i, i, i, i, i, vp, f, vp, sz, st]
+    lib.attn_cache_append.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, i64] + [vp] * 8 + \
+        [i] * 11 + [st]
+    lib.attn_cache_append_q4.argtypes = [vp, i64, i64, i64, vp, vp, i64, i64, i64] + [vp] * 6 + \
+        [f, f] + [vp] * 4 + [i] * 11 + [st]
+    lib.attn_decode_paged_workspace_bytes.argtypes = [i] * 7
+    lib.attn_decode_paged_workspace_bytes.restype = sz
+    lib.attn_decode_paged.argtypes = [vp] * 7 + [i] * 9 + [f, vp, sz, st]
+    lib.attn_decode_paged_q4.argtypes = [vp] * 5 + [f, f] + [vp] * 4 + [i] * 9 + [f, vp, sz, st]
     for name in ("attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_forward",
-                 "attn_get_device_status", "attn_last_cuda_error", "attn_selftest_wait_timeout",
+                 "attn_cache_append", "attn_cache_append_q4", "attn_decode_paged",
+                 "attn_decode_paged_q4", "attn_get_device_status", "attn_last_cuda_error", "attn_selftest_wait_timeout",
                  "mha_project_qkv", "mha_project_out", "mha_forward_noalloc", "mha_concat_heads",
                  "mha_forward_launches", "attn_forward_window", "attn_decode",
                  "encoder_layer_forward", "attn_forward_host", "mha_forward_host",
@@ -187,6 +202,60 @@ def attn_decode(q, k_cache, v_cache, out, B, h, n_q, n_max, d_k, d_v, cache_lens
     _check(library().attn_decode(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), B, h, n_q,
                                  n_max, d_k, d_v, _ptr(cache_lens), scale, _ptr(workspace),
                                  workspace_bytes, _stream(stream)), "attn_decode")
+
+
+def attn_cache_append(q, q_sb, q_sh, q_sr, k, v, kv_sb, kv_sh, kv_sr, q_out, k_out, k_cache,
+                      v_cache, page_table, cache_lens, new_lens, rope, rope_rows, rope_dim,
+                      rope_kind, B, h, h_kv, n_new, d, n_pages, page_size, max_pages, stream=None):
+    """Writes the new tokens' keys (rotated by their positions) and values into a paged
+    bf16 cache [n_pages, h_kv, page_size, d], and the rotated queries into q_out."""
+    _check(library().attn_cache_append(
+        _ptr(q), q_sb, q_sh, q_sr, _ptr(k), _ptr(v), kv_sb, kv_sh, kv_sr, _ptr(q_out), _ptr(k_out),
+        _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(cache_lens), _ptr(new_lens),
+        _ptr(rope), rope_rows, rope_dim, rope_kind, B, h, h_kv, n_new, d, n_pages, page_size,
+        max_pages, _stream(stream)), "attn_cache_append")
+
+
+def attn_cache_append_q4(q, q_sb, q_sh, q_sr, k, v, kv_sb, kv_sh, kv_sr, q_out, k_out, k_codes,
+                         k_scales, v_codes, v_scales, k_factor, v_factor, page_table, cache_lens,
+                         new_lens, rope, rope_rows, rope_dim, rope_kind, B, h, h_kv, n_new, d,
+                         n_pages, page_size, max_pages, stream=None):
+    """attn_cache_append into a paged cache of 4-bit codes [.., d / 2] with a scale per 16
+    columns [.., d / 16]."""
+    _check(library().attn_cache_append_q4(
+        _ptr(q), q_sb, q_sh, q_sr, _ptr(k), _ptr(v), kv_sb, kv_sh, kv_sr, _ptr(q_out), _ptr(k_out),
+        _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), k_factor, v_factor,
+        _ptr(page_table), _ptr(cache_lens), _ptr(new_lens), _ptr(rope), rope_rows, rope_dim,
+        rope_kind, B, h, h_kv, n_new, d, n_pages, page_size, max_pages, _stream(stream)),
+        "attn_cache_append_q4")
+
+
+def attn_decode_paged_workspace_bytes(B, h, h_kv, n_q, d, page_size, max_pages) -> int:
+    return int(library().attn_decode_paged_workspace_bytes(B, h, h_kv, n_q, d, page_size,
+                                                           max_pages))
+
+
+def attn_decode_paged(q, k_cache, v_cache, out, page_table, cache_lens, new_lens, B, h, h_kv, n_q,
+                      d, n_pages, page_size, max_pages, mask_kind=ATTN_MASK_CAUSAL, scale=0.0,
+                      workspace=None, workspace_bytes=0, stream=None):
+    """One decoding step over a paged bf16 cache: n_q queries per sequence, h / h_kv query
+    heads to a key head, causal from the end of the cache or without a mask."""
+    _check(library().attn_decode_paged(
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(out), _ptr(page_table), _ptr(cache_lens),
+        _ptr(new_lens), B, h, h_kv, n_q, d, n_pages, page_size, max_pages, mask_kind, scale,
+        _ptr(workspace), workspace_bytes, _stream(stream)), "attn_decode_paged")
+
+
+def attn_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, k_factor, v_factor, out,
+                         page_table, cache_lens, new_lens, B, h, h_kv, n_q, d, n_pages, page_size,
+                         max_pages, mask_kind=ATTN_MASK_CAUSAL, scale=0.0, workspace=None,
+                         workspace_bytes=0, stream=None):
+    """attn_decode_paged over a paged cache of 4-bit codes and their scales."""
+    _check(library().attn_decode_paged_q4(
+        _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), k_factor, v_factor,
+        _ptr(out), _ptr(page_table), _ptr(cache_lens), _ptr(new_lens), B, h, h_kv, n_q, d, n_pages,
+        page_size, max_pages, mask_kind, scale, _ptr(workspace), workspace_bytes,
+        _stream(stream)), "attn_decode_paged_q4")
 
 
 def encoder_layer_workspace_bytes(B, n, d_model, h, d_k, d_ff) -> int:

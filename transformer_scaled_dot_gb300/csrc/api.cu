@@ -590,6 +590,140 @@ attn_status decode_check(const void* q, const void* k_cache, const void* v_cache
   return ATTN_OK;
 }
 
+// Sizes shared by the paged cache's entry points.
+attn_status paged_check(int B, int h, int h_kv, int n, int d, int n_pages, int page_size,
+                        int max_pages, const int32_t* table, const int32_t* lens,
+                        const int32_t* new_lens) {
+  if (B < 0 || h < 0 || h_kv < 1 || n < 0 || n_pages < 1 || max_pages < 1) return ATTN_ERR_INVALID;
+  if (B > 65535 || h > 65535 || h_kv > 65535 || h % h_kv != 0) return ATTN_ERR_INVALID;
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_INVALID;
+  if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
+  if (page_size < 16 || page_size > 256) return ATTN_ERR_UNSUPPORTED;
+  if (int64_t(max_pages) * page_size > tsd::kPagedMaxRows) return ATTN_ERR_UNSUPPORTED;
+  if (table == nullptr) return ATTN_ERR_INVALID;
+  for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(lens),
+                        static_cast<const void*>(new_lens)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return ATTN_ERR_INVALID;
+  return ATTN_OK;
+}
+
+// The pools' pointers: bf16 rows, or codes with their scales and factors.
+attn_status pool_check(const void* k, const void* v, const void* k_scales, const void* v_scales,
+                       bool q4, float k_factor, float v_factor) {
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return ATTN_ERR_INVALID;
+  if (!q4) return ATTN_OK;
+  if (!k_scales || !v_scales || !aligned16(k_scales) || !aligned16(v_scales))
+    return ATTN_ERR_INVALID;
+  // 6 * factor and the product of a factor with any scale have to be finite
+  // and not denormal
+  for (float f : {k_factor, v_factor})
+    if (!(f >= 0x1p-100f && f <= 0x1p100f)) return ATTN_ERR_INVALID;
+  return ATTN_OK;
+}
+
+int log2_int(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+attn_status run_cache_append(const void* q, int64_t q_sb, int64_t q_sh, int64_t q_sr,
+                             const void* k, const void* v, int64_t kv_sb, int64_t kv_sh,
+                             int64_t kv_sr, void* q_out, void* k_out, void* k_cache,
+                             void* k_scales, void* v_cache, void* v_scales, bool q4,
+                             float k_factor, float v_factor, const int32_t* page_table,
+                             const int32_t* cache_lens, const int32_t* new_lens,
+                             const float* rope, int rope_rows, int rope_dim, int rope_kind, int B,
+                             int h, int h_kv, int n_new, int d, int n_pages, int page_size,
+                             int max_pages, cudaStream_t stream) {
+  attn_status s = paged_check(B, h, h_kv, n_new, d, n_pages, page_size, max_pages, page_table,
+                              cache_lens, new_lens);
+  if (s != ATTN_OK) return s;
+  if (cache_lens == nullptr) return ATTN_ERR_INVALID;
+  if ((q == nullptr) != (q_out == nullptr)) return ATTN_ERR_INVALID;
+  if (!k || !v) return ATTN_ERR_INVALID;
+  for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out),
+                        static_cast<const void*>(rope)})
+    if (!aligned16(p)) return ATTN_ERR_INVALID;
+  for (int64_t st : {q_sb, q_sh, q_sr, kv_sb, kv_sh, kv_sr})
+    if (st < 0 || st % 8 != 0) return ATTN_ERR_INVALID;
+  if (rope_kind != ATTN_ROPE_NONE && rope_kind != ATTN_ROPE_HALVES && rope_kind != ATTN_ROPE_PAIRS)
+    return ATTN_ERR_INVALID;
+  if (rope_kind != ATTN_ROPE_NONE) {
+    if (rope == nullptr || rope_rows < 1 || rope_dim < 2 || rope_dim > d || rope_dim % 2 != 0)
+      return ATTN_ERR_INVALID;
+    if (rope_dim % 32 != 0) return ATTN_ERR_UNSUPPORTED;
+  }
+  s = pool_check(k_cache, v_cache, k_scales, v_scales, q4, k_factor, v_factor);
+  if (s != ATTN_OK) return s;
+  if (int64_t(B) * n_new > INT32_MAX) return ATTN_ERR_INVALID;
+  if (B == 0 || n_new == 0) return ATTN_OK;
+  tsd::AppendProblem p;
+  std::memset(&p, 0, sizeof(p));
+  p.cache = {k_cache, v_cache, static_cast<uint8_t*>(k_scales), static_cast<uint8_t*>(v_scales),
+             k_factor, v_factor, page_table, cache_lens, new_lens, h_kv, d, n_pages,
+             log2_int(page_size), max_pages};
+  p.q = static_cast<const uint16_t*>(q);
+  p.k = static_cast<const uint16_t*>(k);
+  p.v = static_cast<const uint16_t*>(v);
+  p.q_sb = q_sb;
+  p.q_sh = q_sh;
+  p.q_sr = q_sr;
+  p.kv_sb = kv_sb;
+  p.kv_sh = kv_sh;
+  p.kv_sr = kv_sr;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.rope = rope;
+  p.rope_rows = rope_rows;
+  p.rope_dim = rope_kind == ATTN_ROPE_NONE ? 0 : rope_dim;
+  p.rope_kind = rope_kind;
+  p.B = B;
+  p.h = h;
+  p.n_new = n_new;
+  cudaError_t e = tsd::launch_cache_append(p, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status run_decode_paged(const void* q, const void* k_cache, const void* k_scales,
+                             const void* v_cache, const void* v_scales, bool q4, float k_factor,
+                             float v_factor, void* out, const int32_t* page_table,
+                             const int32_t* cache_lens, const int32_t* new_lens, int B, int h,
+                             int h_kv, int n_q, int d, int n_pages, int page_size, int max_pages,
+                             int mask_kind, float scale, void* workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+  if (n_q < 1) return ATTN_ERR_INVALID;
+  if (n_q > tsd::kDecodeMaxQueries) return ATTN_ERR_UNSUPPORTED;
+  attn_status s = paged_check(B, h, h_kv, n_q, d, n_pages, page_size, max_pages, page_table,
+                              cache_lens, new_lens);
+  if (s != ATTN_OK) return s;
+  if (mask_kind != ATTN_MASK_NONE && mask_kind != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID;
+  if (!valid_scale(scale)) return ATTN_ERR_INVALID;
+  for (const void* p : {q, static_cast<const void*>(out), static_cast<const void*>(workspace)})
+    if (p == nullptr || !aligned16(p)) return ATTN_ERR_INVALID;
+  s = pool_check(k_cache, v_cache, k_scales, v_scales, q4, k_factor, v_factor);
+  if (s != ATTN_OK) return s;
+  if (workspace_bytes < tsd::decode_paged_workspace_bytes(B, h, h_kv, n_q, d, page_size, max_pages))
+    return ATTN_ERR_INVALID;
+  if (B == 0 || h == 0) return ATTN_OK;
+  tsd::PagedDecodeProblem p;
+  std::memset(&p, 0, sizeof(p));
+  p.cache = {const_cast<void*>(k_cache), const_cast<void*>(v_cache),
+             static_cast<uint8_t*>(const_cast<void*>(k_scales)),
+             static_cast<uint8_t*>(const_cast<void*>(v_scales)), k_factor, v_factor, page_table,
+             cache_lens, new_lens, h_kv, d, n_pages, log2_int(page_size), max_pages};
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.workspace = workspace;
+  p.B = B;
+  p.h = h;
+  p.n_q = n_q;
+  p.causal = mask_kind == ATTN_MASK_CAUSAL;
+  p.scale = resolve_scale(scale, d);
+  cudaError_t e = tsd::launch_decode_paged(p, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
 // Staging regions of the host-buffer entry points, 256-byte aligned, in
 // order; the device entry point's own workspace follows them.
 struct StageLayout {
@@ -946,6 +1080,70 @@ attn_status mha_project_out(const void* concat, const void* w_o, void* out, int 
                          reinterpret_cast<cudaStream_t>(stream));
 }
 
+attn_status attn_cache_append(const void* q, int64_t q_sb, int64_t q_sh, int64_t q_sr,
+                              const void* k, const void* v, int64_t kv_sb, int64_t kv_sh,
+                              int64_t kv_sr, void* q_out, void* k_out, void* k_cache,
+                              void* v_cache, const int32_t* page_table, const int32_t* cache_lens,
+                              const int32_t* new_lens, const float* rope, int rope_rows,
+                              int rope_dim, int rope_kind, int B, int h, int h_kv, int n_new,
+                              int d, int n_pages, int page_size, int max_pages,
+                              tsd_stream_t stream) {
+  return run_cache_append(q, q_sb, q_sh, q_sr, k, v, kv_sb, kv_sh, kv_sr, q_out, k_out, k_cache,
+                          nullptr, v_cache, nullptr, false, 1.f, 1.f, page_table, cache_lens,
+                          new_lens, rope, rope_rows, rope_dim, rope_kind, B, h, h_kv, n_new, d,
+                          n_pages, page_size, max_pages, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_append_q4(const void* q, int64_t q_sb, int64_t q_sh, int64_t q_sr,
+                                 const void* k, const void* v, int64_t kv_sb, int64_t kv_sh,
+                                 int64_t kv_sr, void* q_out, void* k_out, void* k_codes,
+                                 void* k_scales, void* v_codes, void* v_scales, float k_factor,
+                                 float v_factor, const int32_t* page_table,
+                                 const int32_t* cache_lens, const int32_t* new_lens,
+                                 const float* rope, int rope_rows, int rope_dim, int rope_kind,
+                                 int B, int h, int h_kv, int n_new, int d, int n_pages,
+                                 int page_size, int max_pages, tsd_stream_t stream) {
+  return run_cache_append(q, q_sb, q_sh, q_sr, k, v, kv_sb, kv_sh, kv_sr, q_out, k_out, k_codes,
+                          k_scales, v_codes, v_scales, true, k_factor, v_factor, page_table,
+                          cache_lens, new_lens, rope, rope_rows, rope_dim, rope_kind, B, h, h_kv,
+                          n_new, d, n_pages, page_size, max_pages,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t attn_decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
+                                         int max_pages) {
+  static const int32_t table = 0;
+  if (n_q < 1 || n_q > tsd::kDecodeMaxQueries ||
+      paged_check(B, h, h_kv, n_q, d, 1, page_size, max_pages, &table, nullptr, nullptr) != ATTN_OK)
+    return 0;
+  return tsd::decode_paged_workspace_bytes(B, h, h_kv, n_q, d, page_size, max_pages);
+}
+
+attn_status attn_decode_paged(const void* q, const void* k_cache, const void* v_cache, void* out,
+                              const int32_t* page_table, const int32_t* cache_lens,
+                              const int32_t* new_lens, int B, int h, int h_kv, int n_q, int d,
+                              int n_pages, int page_size, int max_pages, int mask_kind,
+                              float scale, void* workspace, size_t workspace_bytes,
+                              tsd_stream_t stream) {
+  return run_decode_paged(q, k_cache, nullptr, v_cache, nullptr, false, 1.f, 1.f, out, page_table,
+                          cache_lens, new_lens, B, h, h_kv, n_q, d, n_pages, page_size, max_pages,
+                          mask_kind, scale, workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_decode_paged_q4(const void* q, const void* k_codes, const void* k_scales,
+                                 const void* v_codes, const void* v_scales, float k_factor,
+                                 float v_factor, void* out, const int32_t* page_table,
+                                 const int32_t* cache_lens, const int32_t* new_lens, int B, int h,
+                                 int h_kv, int n_q, int d, int n_pages, int page_size,
+                                 int max_pages, int mask_kind, float scale, void* workspace,
+                                 size_t workspace_bytes, tsd_stream_t stream) {
+  return run_decode_paged(q, k_codes, k_scales, v_codes, v_scales, true, k_factor, v_factor, out,
+                          page_table, cache_lens, new_lens, B, h, h_kv, n_q, d, n_pages, page_size,
+                          max_pages, mask_kind, scale, workspace, workspace_bytes,
+                          reinterpret_cast<cudaStream_t>(stream));
+}
+
 attn_status attn_get_device_status(tsd_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
@@ -960,8 +1158,15 @@ attn_status attn_get_device_status(tsd_stream_t stream) {
   unsigned int dec = 0;
   if (e == cudaSuccess) e = tsd::take_device_error_decode(&dec);
   m |= dec;
+  for (auto take : {tsd::take_device_error_append, tsd::take_device_error_paged}) {
+    unsigned int w = 0;
+    if (e == cudaSuccess) e = take(&w);
+    m |= w;
+  }
   if (e != cudaSuccess) return cuda_fail(e);
-  return (a | g | f | m) ? ATTN_ERR_DEVICE_TIMEOUT : ATTN_OK;
+  m |= a | g | f;
+  if (m & ~tsd::kDeviceErrIndex) return ATTN_ERR_DEVICE_TIMEOUT;
+  return m ? ATTN_ERR_DEVICE_INDEX : ATTN_OK;
 }
 
 int attn_last_cuda_error(void) { return g_last_cuda_error; }
@@ -973,6 +1178,7 @@ const char* attn_status_string(attn_status s) {
     case ATTN_ERR_UNSUPPORTED: return "ATTN_ERR_UNSUPPORTED";
     case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
     case ATTN_ERR_DEVICE_TIMEOUT: return "ATTN_ERR_DEVICE_TIMEOUT";
+    case ATTN_ERR_DEVICE_INDEX: return "ATTN_ERR_DEVICE_INDEX";
   }
   return "ATTN_STATUS_UNKNOWN";
 }

@@ -168,7 +168,6 @@ int mha_fused_out_clusters(int h, bool self);
 cudaError_t launch_mha_cross(const MhaFusedProblem& p, cudaStream_t stream);
 int mha_cross_out_clusters(int h);
 
-// Per-file device error words (read and cleared; see sm103.cuh).
 // One decoding step against a key/value cache: the n_q (<= 8) newest tokens'
 // queries, at positions L - n_q .. L - 1 of an L-row cache, each against the
 // keys at or before its position. Split over 128-key chunks (partials in a
@@ -188,6 +187,58 @@ struct DecodeProblem {
 int decode_chunks(int n_max);
 cudaError_t launch_decode(const DecodeProblem& p, cudaStream_t stream);
 
+// A paged key/value cache: row p of sequence b lies in page
+// table[b * max_pages + p / page_size], slot p % page_size (a power of two).
+// bf16 pools [n_pages, h_kv, page_size, d]; 4-bit pools hold e2m1 codes
+// [.., d / 2] (two per byte, the even column in the low half) and one e4m3
+// scale per 16 columns [.., d / 16], a value being code * scale * factor.
+struct PagedCache {
+  void* k;            // bf16 rows, or codes
+  void* v;
+  uint8_t* k_scales;  // null: a bf16 cache
+  uint8_t* v_scales;
+  float k_factor, v_factor;
+  const int32_t* table;  // [B, max_pages]
+  const int32_t* lens;   // [B] rows, the new tokens included; null (decode only): max_pages * page_size
+  const int32_t* new_lens;  // [B] new tokens, or null: all
+  int h_kv, d, n_pages, page_shift, max_pages;
+};
+
+constexpr int kRopeHalves = 1;  // columns i and i + dim / 2 are a pair
+constexpr int kRopePairs = 2;   // columns 2 i and 2 i + 1 are a pair
+
+// Rotates the new tokens' queries and keys by their positions' angles and
+// writes keys and values into the cache (quantised there when it is 4-bit).
+struct AppendProblem {
+  PagedCache cache;
+  const uint16_t* q;  // may be null
+  const uint16_t* k;
+  const uint16_t* v;
+  int64_t q_sb, q_sh, q_sr, kv_sb, kv_sh, kv_sr;  // elements
+  uint16_t* q_out;    // [B, h, n_new, d], with q
+  uint16_t* k_out;    // [B, h_kv, n_new, d] or null
+  const float* rope;  // [rope_rows, rope_dim]: cosines, then sines
+  int rope_rows, rope_dim, rope_kind;
+  int B, h, n_new;
+};
+cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream);
+
+// One decoding step against a paged cache: the n_q (<= 8) newest tokens'
+// queries of h = group * h_kv heads, end-aligned causal or without a mask.
+constexpr int64_t kPagedMaxRows = 1ll << 30;  // rows of one sequence's pages
+struct PagedDecodeProblem {
+  PagedCache cache;
+  const uint16_t* q;  // [B, h, n_q, d]
+  uint16_t* out;      // [B, h, n_q, d]
+  void* workspace;    // decode_paged_workspace_bytes(...)
+  int B, h, n_q;
+  bool causal;
+  float scale;        // logit factor (resolved: never 0)
+};
+size_t decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
+                                    int max_pages);
+cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream);
+
 // out = LayerNorm(x + r) over rows of d_model (256, 512, 1024 or 2048)
 // features: x bf16 (or fp32 when x_f32), r bf16 or null, gamma/beta bf16,
 // out bf16 and, when out32 is not null, the same values in fp32 as well.
@@ -196,12 +247,17 @@ cudaError_t launch_add_layernorm(const void* x, bool x_f32, const uint16_t* r,
                                  float* out32, int rows, int d_model, float eps,
                                  cudaStream_t stream);
 
+// Per-file device error words (read and cleared; see sm103.cuh). kDeviceErrIndex
+// is the bit of an index out of range; any other bit is a wait that ran out.
+constexpr unsigned int kDeviceErrIndex = 2u;
 cudaError_t take_device_error_attn(unsigned int* value);
 cudaError_t take_device_error_decode(unsigned int* value);
 cudaError_t take_device_error_gemm(unsigned int* value);
 cudaError_t take_device_error_f32(unsigned int* value);
 cudaError_t take_device_error_fused(unsigned int* value);
 cudaError_t take_device_error_cross(unsigned int* value);
+cudaError_t take_device_error_append(unsigned int* value);
+cudaError_t take_device_error_paged(unsigned int* value);
 
 // Failure-detection self test: a bounded wait on a barrier nobody arrives on.
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, cudaStream_t stream);

@@ -10,6 +10,8 @@
 #include <cstdint>
 #include <cuda.h>
 
+#include "kernels.h"
+
 namespace tsd {
 
 // ------------------------------------------------------------------ errors
@@ -21,7 +23,9 @@ static __device__ unsigned int g_device_error = 0u;
 
 enum : unsigned int {
   kErrWaitTimeout = 1u,
+  kErrIndex = 2u,  // a page index or a position outside its table; the row was left out
 };
+static_assert(kErrIndex == kDeviceErrIndex, "the word's bit that the API layer tells apart");
 
 // A wait that has not completed after this long is treated as a hang.
 // Legitimate waits in these kernels last microseconds.
