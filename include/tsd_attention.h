@@ -570,7 +570,8 @@ attn_status attn_cache_append_q4(const void *q, int64_t q_sb, int64_t q_sh, int6
 
 /*
  * attn_decode_paged -- attn_decode over a paged cache with grouped heads.
- *   q, out  [B, h, n_q, d] bf16; 1 <= n_q <= 8 (more -> ATTN_ERR_UNSUPPORTED)
+ *   q, out  [B, h, n_q, d] bf16; 1 <= n_q <= 8 (more -> ATTN_ERR_UNSUPPORTED);
+ *       B h n_q < 2^31, else ATTN_ERR_INVALID
  *   cache_lens  as above, clamped to [0, max_pages * page_size]; NULL: that many
  *   mask_kind   ATTN_MASK_CAUSAL: query t sees the rows at positions <=
  *       cache_lens[b] - new_lens[b] + t, its own (the new tokens' keys are in

@@ -685,6 +685,14 @@ attn_status run_cache_append(const void* q, int64_t q_sb, int64_t q_sh, int64_t 
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
+attn_status decode_paged_size_check(int B, int h, int h_kv, int n_q, int d, int page_size,
+                                    int max_pages) {
+  if (int64_t(B) * h * n_q > INT32_MAX) return ATTN_ERR_INVALID;
+  if (tsd::decode_paged_units(B, h, h_kv, n_q, d, page_size, max_pages) > tsd::kPagedMaxUnits)
+    return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
 attn_status run_decode_paged(const void* q, const void* k_cache, const void* k_scales,
                              const void* v_cache, const void* v_scales, bool q4, float k_factor,
                              float v_factor, void* out, const int32_t* page_table,
@@ -696,6 +704,8 @@ attn_status run_decode_paged(const void* q, const void* k_cache, const void* k_s
   if (n_q > tsd::kDecodeMaxQueries) return ATTN_ERR_UNSUPPORTED;
   attn_status s = paged_check(B, h, h_kv, n_q, d, n_pages, page_size, max_pages, page_table,
                               cache_lens, new_lens);
+  if (s != ATTN_OK) return s;
+  s = decode_paged_size_check(B, h, h_kv, n_q, d, page_size, max_pages);
   if (s != ATTN_OK) return s;
   if (mask_kind != ATTN_MASK_NONE && mask_kind != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID;
   if (!valid_scale(scale)) return ATTN_ERR_INVALID;
@@ -1114,7 +1124,8 @@ size_t attn_decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d,
                                          int max_pages) {
   static const int32_t table = 0;
   if (n_q < 1 || n_q > tsd::kDecodeMaxQueries ||
-      paged_check(B, h, h_kv, n_q, d, 1, page_size, max_pages, &table, nullptr, nullptr) != ATTN_OK)
+      paged_check(B, h, h_kv, n_q, d, 1, page_size, max_pages, &table, nullptr, nullptr) != ATTN_OK ||
+      decode_paged_size_check(B, h, h_kv, n_q, d, page_size, max_pages) != ATTN_OK)
     return 0;
   return tsd::decode_paged_workspace_bytes(B, h, h_kv, n_q, d, page_size, max_pages);
 }

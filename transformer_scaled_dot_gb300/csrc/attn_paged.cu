@@ -1,8 +1,41 @@
 // attn_paged.cu -- one decoding step against a paged key/value cache, bf16
-// or 4-bit: softmax(scale q K^T) V of each query row over the rows it sees.
+// or 4-bit, with grouped query heads:
+//   out_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = 2^(x_rj - m_r),
+//   x_rj = scale log2(e) q_r . k_j,  m_r the largest x_rj that row r sees.
+// The R = (h / h_kv) n_q query rows of one sequence and key head share every
+// cached row, so that each is read once for all of them.
 //
-// A warp per query row walks the cache row by row, the running maximum and
-// sum of the softmax in fp32; d / 32 columns per lane.
+// The step is bound by reading the cache, and is laid out around that:
+//
+//  * Work. A unit is 64 cached rows of one (sequence, key head, tile of query
+//    rows). The units of the batch, in that order, are cut into as many equal
+//    ranges as blocks fit on the device, from the lengths that the device
+//    holds: sequences of uneven lengths keep all SMs reading to the end, and
+//    pages that a sequence does not have cost nothing. A range's first and
+//    last sequence may be shared with the neighbouring blocks; those leave
+//    partial results (m, l = sum p, O = sum p v, in fp32) in the workspace
+//    and the merge kernel joins them.
+//  * Loads. A warp takes 16 rows at a time (they lie within one page) and
+//    copies them asynchronously into a ring of its own in shared memory, a
+//    few 16-row tiles ahead, so no warp waits for another within a range.
+//  * Products. A handful of query rows is far too few for a tcgen05 tile of
+//    128 rows, and the warp-wide m16n8k16 product reaches the cache's rate
+//    with room to spare: S^T = K Q^T with the 16 cached rows as its M and 8
+//    query rows as its N, then O^T += V^T P^T. The fragments of both come
+//    straight from the ring: a product's sum does not care about the order
+//    of its terms, so each thread's K columns are the ones it loaded with 16
+//    bytes, Q being laid out to match, and V's columns are numbered the same
+//    way. S^T's accumulators become P^T's operand through an 8 x 8 transpose
+//    within the warp (movmatrix).
+//
+// Numbers: S, the softmax and O in fp32. With a bf16 cache P is split into
+// two bf16 parts, p = hi + lo (16 bits), at the cost of a second product
+// that the tensor cores have time for. With a 4-bit cache code * scale has
+// 6 significant bits and is formed in f16 without rounding; q is brought to
+// f16 by a power of two per row, which keeps every bf16 value within 2^-33
+// of the row's largest, and P, taken times 2^15, is rounded to f16: to 11
+// bits, well below the output's 8, where it is at least 2^-29 of the row's
+// largest in its warp, and to 2^-40 of that below.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -12,107 +45,896 @@ namespace tsd {
 
 namespace {
 
-__device__ __forceinline__ float bf16_f32(uint16_t w) {
-  return __uint_as_float(static_cast<uint32_t>(w) << 16);
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 16;                // cached rows of a warp's step
+constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
+constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
+constexpr int kMergeThreads = 256;
+
+// Query rows of a block's tile: 8 per column block of the products.
+int column_blocks(int rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+
+struct PagedArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  const uint8_t* k;
+  const uint8_t* v;
+  const uint8_t* k_scales;
+  const uint8_t* v_scales;
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* new_lens;
+  int2* split;     // [blocks] (pair that block i begins and others finish, or -1; last block)
+  float* part_o;   // [blocks][2][rows of a tile][d]
+  float2* part_ml; // [blocks][2][rows of a tile]
+  int B, h_kv, n_q, rows, row_tiles, n_pages, page_shift, max_pages;
+  bool causal;
+  float scale_log2;  // scale log2(e), with the keys' factor
+  float v_factor;
+};
+
+template <int D, int NT, bool Q4>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
+  static constexpr int kScaleBytes = Q4 ? D / 16 : 0;
+  static constexpr int kStageBytes = 2 * kTile * (kRowBytes + kScaleBytes);
+  static constexpr int kStages = Q4 ? 4 : (D == 64 ? 4 : 3);
+  static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+  static constexpr int kPitch = D + 2;  // floats of a row of O in shared memory
+  static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
+  static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+};
+
+// ------------------------------------------------------------------ instructions
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? 16 : 0;  // 0: nothing is read, zeros are written
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ float e2m1_f32(uint32_t code) {
-  const uint32_t m = code & 7u;
-  const float v = m < 4 ? 0.5f * m : (m == 4 ? 2.f : (m == 5 ? 3.f : (m == 6 ? 4.f : 6.f)));
-  return (code & 8u) ? -v : v;
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 r;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t r;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
+  return r;
 }
 
-__device__ __forceinline__ float e4m3_f32(uint8_t s) {
-  uint32_t f2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(f2) : "h"(static_cast<uint16_t>(s)));
-  float x;
-  asm("{.reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.f32.f16 %0, lo;}" : "=f"(x) : "r"(f2));
-  return x;
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                    uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// four bytes of two e2m1 codes each -> four pairs of f16
+__device__ __forceinline__ void codes_f16x2(uint32_t w, uint32_t (&x)[4]) {
+  asm("{.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;}"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(w));
+}
+// two e4m3 bytes -> a pair of f16 (exact)
+__device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
+  return r;
+}
+__device__ __forceinline__ float bf16_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
+
+// ------------------------------------------------------------------ the ring
+
+// Where the 4-bit tile's rows lie in shared memory, so that a warp's loads of
+// K (rows by g, 16 or 8 bytes by t) and of V (rows by t, 8 or 4 bytes by g)
+// touch every bank once. Row r of the products is cached row cached_row(r):
+// the rows that one thread's V operand spans (2t, 2t+1, 2t+8, 2t+9) are t,
+// t+4, t+8 and t+12.
+__device__ __forceinline__ constexpr int cached_row(int r) {
+  return (r & 8) | ((r & 1) << 2) | ((r & 7) >> 1);
+}
+template <int D>
+__device__ __forceinline__ uint32_t k_code_offset(int row, int byte) {
+  if constexpr (D == 128) return static_cast<uint32_t>((row ^ ((row >> 2) & 1)) * 64 + byte);
+  return static_cast<uint32_t>((row ^ ((row >> 1) & 2)) * 32 + byte);
+}
+template <int D>
+__device__ __forceinline__ uint32_t v_code_offset(int row, int byte) {
+  if constexpr (D == 128) return static_cast<uint32_t>(row * 64 + (byte ^ ((row & 2) << 4)));
+  return static_cast<uint32_t>(row * 32 + byte);
+}
+
+// Copies the `valid` first of the 16 rows that start at row `at` of the pools
+// into a stage (the rest become zeros). bf16: each thread copies the very
+// 16-byte pieces that it will use, piece i of thread l at (i * 32 + l) * 16;
+// 4-bit: the tile as it is, the rows moved as above.
+template <int D, bool Q4>
+__device__ __forceinline__ void load_tile(uint32_t stage, const PagedArgs& a, int64_t at,
+                                          int valid, int lane) {
+  if constexpr (!Q4) {
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t* k = a.k + at * (2 * D);
+    const uint8_t* v = a.v + at * (2 * D);
+    uint32_t dst = stage + lane * 16;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+      for (int j = 0; j < D / 32; ++j) {
+        const int row = g + 8 * half;
+        cp_async_16(dst, k + row * (2 * D) + (t + 4 * j) * 16, row < valid);
+        dst += 512;
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const int row = 2 * t + (i & 1) + 4 * (i & 2);
+        cp_async_16(dst, v + row * (2 * D) + (g + 8 * j) * 16, row < valid);
+        dst += 512;
+      }
+  } else {
+    constexpr int kPieces = D / 32;  // 16-byte pieces of a row of codes
+    const uint8_t* k = a.k + at * (D / 2);
+    const uint8_t* v = a.v + at * (D / 2);
+#pragma unroll
+    for (int i = 0; i < kTile * kPieces / 32; ++i) {
+      const int piece = lane + 32 * i, row = piece / kPieces, byte = piece % kPieces * 16;
+      cp_async_16(stage + k_code_offset<D>(row, byte), k + piece * 16, row < valid);
+      cp_async_16(stage + kTile * (D / 2) + v_code_offset<D>(row, byte), v + piece * 16,
+                  row < valid);
+    }
+    // the scales of 16 rows: D bytes for keys, D for values; 16 bytes hold
+    // several rows' scales, those past `valid` meet codes of zero
+    constexpr int kRowsIn16 = 256 / D;
+    const int piece = lane % (D / 16);
+    if (lane < D / 8) {
+      const uint8_t* s = (lane < D / 16 ? a.k_scales : a.v_scales) + at * (D / 16);
+      cp_async_16(stage + kTile * D + lane * 16, s + piece * 16, piece * kRowsIn16 < valid);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ the work's order
+
+// Sequence b's rows that count, and its units.
+struct Sequence {
+  int len, fresh;  // cached rows, new tokens
+  int units;       // at least one: its output has to be written
+};
+__device__ __forceinline__ Sequence sequence(const PagedArgs& a, int b) {
+  Sequence s;
+  const int capacity = a.max_pages << a.page_shift;
+  s.len = a.lens ? min(max(__ldcg(a.lens + b), 0), capacity) : capacity;
+  s.fresh = a.new_lens ? min(max(__ldcg(a.new_lens + b), 0), a.n_q) : a.n_q;
+  s.units = s.fresh > 0 ? max((s.len + kUnit - 1) / kUnit, 1) : 1;
+  return s;
+}
+
+// Floor of x / y, in 32 bits where they suffice.
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
+  if (((x | y) >> 32) == 0) return static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+  return x / y;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, int NT, bool Q4>
+__global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs a) {
+  using S = Shape<D, NT, Q4>;
+  constexpr int kSteps = D / 16;  // products of S, and blocks of 16 columns of O
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kWarps][S::kRows];
+  const int tid = static_cast<int>(threadIdx.x);
+  const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  griddep_wait();  // the cache, queries, lengths and tables may come from the previous kernel
+  griddep_launch_dependents();
+
+  // this block's range of units: each warp by itself sums the sequences' units
+  const int pairs = a.h_kv * a.row_tiles;  // (key head, row tile) of a sequence
+  int64_t total = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    int u = b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) u += __shfl_xor_sync(0xffffffffu, u, s);
+    total += u;
+  }
+  total *= pairs;
+  const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);
+  const int64_t me = blockIdx.x;
+  if (me >= blocks) {
+    if (tid == 0) a.split[me] = make_int2(-1, 0);
+    return;
+  }
+  const int64_t each = quotient(total, blocks), left = total - each * blocks;
+  int64_t unit = me * each + quotient(me * left, blocks);
+  const int64_t end = (me + 1) * each + quotient((me + 1) * left, blocks);
+  int b = 0;
+  int64_t base = 0;  // units of one pair of all sequences before b
+  {
+    const int64_t want = quotient(unit, pairs);
+    for (int b0 = 0;; b0 += 32) {
+      const int u = b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+      int upto = u;
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, s);
+        if (lane >= s) upto += v;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, base + upto > want);
+      if (past != 0u || b0 + 32 >= a.B) {  // the second: for certain to end
+        const int first = past != 0u ? __ffs(past) - 1 : 31;
+        b = min(b0 + first, a.B - 1);
+        base += __shfl_sync(0xffffffffu, upto - u, first);
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+  }
+
+  const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
+  int begun = -1, begun_last = 0;  // the pair that this block begins and does not finish
+
+  while (unit < end) {
+    const Sequence seq = sequence(a, b);
+    const int64_t local = unit - base * pairs;
+    const int pair = static_cast<int>(quotient(local, seq.units));
+    const int chunk = static_cast<int>(local - static_cast<int64_t>(pair) * seq.units);
+    const int take = static_cast<int>(min(end - unit, static_cast<int64_t>(seq.units - chunk)));
+    const int head = pair / a.row_tiles, row0 = pair % a.row_tiles * S::kRows;
+    const int rows = min(S::kRows, a.rows - row0);
+    // rows [key0, key1) of the cache; none if every token is padding
+    const int key0 = chunk * kUnit;
+    const int key1 = seq.fresh > 0 ? min(seq.len, (chunk + take) * kUnit) : 0;
+    const int64_t q_row0 = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0;
+
+    // ---- queries as the products' operand: b0 and b1 of step s hold the
+    // columns that the threads' K registers of that step hold
+    uint32_t qf[NT][kSteps][2];
+    float mult[NT][2];  // the factor from S to x of this thread's two rows
+    int limit[NT][2];   // they see the cached rows before these
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const bool live = nt * 8 + g < rows;
+      const uint16_t* qp = a.q + (q_row0 + nt * 8 + g) * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int col = Q4 ? t * (D / 4) + 4 * s : 8 * (t + 4 * (s >> 1)) + 4 * (s & 1);
+        const uint2 w = live ? __ldcg(reinterpret_cast<const uint2*>(qp + col)) : make_uint2(0, 0);
+        qf[nt][s][0] = w.x;
+        qf[nt][s][1] = w.y;
+      }
+      mult[nt][0] = mult[nt][1] = a.scale_log2;
+      if constexpr (Q4) {
+        // the row's largest magnitude decides a power of two that brings it
+        // below 2^9; what was 2^-33 of it or less may lose bits
+        uint32_t top = 0;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            top = max(top, max(qf[nt][s][i] & 0x7fffu, (qf[nt][s][i] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // exponent field e of the largest: times 2^(135 - e) in two factors,
+        // since 135 - e may pass a float's exponents by itself
+        const int e = min(max(static_cast<int>(top >> 7), 1), 254);
+        const int up = 135 - e, up0 = up / 2, up1 = up - up0;
+        const float f0 = __int_as_float((127 + up0) << 23), f1 = __int_as_float((127 + up1) << 23);
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w = qf[nt][s][i];
+            qf[nt][s][i] = pack_f16x2(bf16_f32(w & 0xffffu) * f0 * f1, bf16_f32(w >> 16) * f0 * f1);
+          }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int e_col = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4) - 135;
+          const int d0 = e_col / 2, d1 = e_col - d0;
+          mult[nt][i] = a.scale_log2 * __int_as_float((127 + d0) << 23) *
+                        __int_as_float((127 + d1) << 23);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = nt * 8 + 2 * t + i;
+        const int token = (row0 + r) % a.n_q;
+        limit[nt][i] = 0x7fffffff;  // columns that nobody reads: no mask needed
+        if (r < rows && token < seq.fresh && a.causal) limit[nt][i] = seq.len - seq.fresh + token + 1;
+        if (r < rows && token < seq.fresh) limit[nt][i] = min(limit[nt][i], seq.len);
+      }
+    }
+    // cached rows from here on are hidden from some row of the tile
+    const int hidden = a.causal ? min(seq.len, seq.len - seq.fresh + 1) : seq.len;
+
+    float o[NT][kSteps][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+
+    // ---- this warp's tiles: key0 + (warp + 4 i) * 16, i < tiles
+    const int span = key1 - key0 - warp * kTile;
+    const int tiles = span > 0 ? (span + kUnit - 1) / kUnit : 0;
+    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
+    const int first_key = key0 + warp * kTile;
+    // the page of tile i: 32 at a time, one per lane, the next 32 on their way
+    auto page_of = [&](int i) {
+      return i < tiles ? __ldcg(table + ((first_key + i * kUnit) >> a.page_shift)) : 0;
+    };
+    int pages = page_of(lane), pages_next = page_of(32 + lane);
+    uint32_t skipped = 0;  // bit s: the tile in stage s has no page
+    auto issue = [&](int i) {  // tile i into stage i % kStages
+      if (i < tiles) {
+        if ((i & 31) == 0 && i > 0) {
+          pages = pages_next;
+          pages_next = page_of(i + 32 + lane);
+        }
+        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+        const int stage = i % S::kStages;
+        const int key = first_key + i * kUnit;
+        if (page < 0 || page >= a.n_pages) {
+          skipped |= 1u << stage;
+          if (lane == 0) atomicOr(&g_device_error, kErrIndex);
+        } else {
+          skipped &= ~(1u << stage);
+          const int64_t at = ((static_cast<int64_t>(page) * a.h_kv + head) << a.page_shift) +
+                             (key & ((1 << a.page_shift) - 1));
+          load_tile<D, Q4>(ring + stage * S::kStageBytes, a, at, key1 - key, lane);
+        }
+      }
+      cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+
+    for (int i = 0; i < tiles; ++i) {
+      cp_async_wait<S::kStages - 2>();
+      __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
+      issue(i + S::kStages - 1);
+      const int stage = i % S::kStages;
+      if (skipped & (1u << stage)) continue;
+      const uint32_t at = ring + stage * S::kStageBytes;
+      const int key = first_key + i * kUnit;
+
+      // ---- S^T = K Q^T
+      float x[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+      if constexpr (!Q4) {
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+          const uint4 lo = lds128(at + j * 512 + lane * 16);
+          const uint4 hi = lds128(at + (D / 32 + j) * 512 + lane * 16);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<false>(x[nt], lo.x, hi.x, lo.y, hi.y, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+            mma<false>(x[nt], lo.z, hi.z, lo.w, hi.w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+          }
+        }
+      } else {
+        constexpr int kWords = D / 32;  // of this thread's codes of one row
+        uint32_t w[2][kWords], sc[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int row = cached_row(g + 8 * half);
+          if constexpr (D == 128) {
+            const uint4 v = lds128(at + k_code_offset<D>(row, t * 16));
+            w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
+            sc[half] = scales_f16x2(lds16(at + kTile * D + row * 8 + t * 2));
+          } else {
+            const uint2 v = lds64(at + k_code_offset<D>(row, t * 8));
+            w[half][0] = v.x, w[half][1] = v.y;
+            sc[half] = scales_f16x2(lds8(at + kTile * D + row * 4 + t) * 0x0101u);
+          }
+        }
+#pragma unroll
+        for (int i4 = 0; i4 < kWords; ++i4) {
+          uint32_t lo[4], hi[4];
+          codes_f16x2(w[0][i4], lo);
+          codes_f16x2(w[1][i4], hi);
+          // d = 128: words 0, 1 are of the thread's first group, 2, 3 of its second
+          const uint32_t s0 = D == 128 ? __byte_perm(sc[0], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[0];
+          const uint32_t s1 = D == 128 ? __byte_perm(sc[1], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[1];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            lo[c] = mul_f16x2(lo[c], s0);
+            hi[c] = mul_f16x2(hi[c], s1);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<true>(x[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][2 * i4][0], qf[nt][2 * i4][1]);
+            mma<true>(x[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][2 * i4 + 1][0],
+                      qf[nt][2 * i4 + 1][1]);
+          }
+        }
+      }
+
+      // ---- x, masks, the running maximum
+      const int row_lo = Q4 ? cached_row(g) : g, row_hi = row_lo + 8;
+      const bool masked = key + kTile > hidden;
+      bool grew = false;
+      float next[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          x[nt][c] *= mult[nt][c];
+          x[nt][2 + c] *= mult[nt][c];
+          if (masked) {
+            if (key + row_lo >= limit[nt][c]) x[nt][c] = -INFINITY;
+            if (key + row_hi >= limit[nt][c]) x[nt][2 + c] = -INFINITY;
+          }
+          float top = fmaxf(x[nt][c], x[nt][2 + c]);
+#pragma unroll
+          for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+          next[nt][c] = fmaxf(m[nt][c], top);
+          grew |= next[nt][c] > m[nt][c];
+        }
+      }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float f = next[nt][c] > m[nt][c] ? ex2(m[nt][c] - next[nt][c]) : 1.f;
+            m[nt][c] = next[nt][c];
+            l[nt][c] *= f;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              o[nt][s][c] *= f;
+              o[nt][s][2 + c] *= f;
+            }
+          }
+      }
+
+      // ---- p, its sum, and P^T as the second product's operand
+      uint32_t p_hi[NT][2], p_lo[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // 4-bit: P, and with it l and O, carry a factor 2^15
+          const float m_use = (m[nt][c] == -INFINITY ? 0.f : m[nt][c]) - (Q4 ? 15.f : 0.f);
+          p[c] = ex2(x[nt][c] - m_use);
+          p[2 + c] = ex2(x[nt][2 + c] - m_use);
+          l[nt][c] += p[c] + p[2 + c];
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const float p0 = p[2 * half], p1 = p[2 * half + 1];
+          if constexpr (Q4) {
+            p_hi[nt][half] = transpose8x8(pack_f16x2(p0, p1));
+          } else {
+            const uint32_t hi = pack_bf16x2(p0, p1);
+            p_hi[nt][half] = transpose8x8(hi);
+            p_lo[nt][half] = transpose8x8(
+                pack_bf16x2(p0 - bf16_f32(hi & 0xffffu), p1 - bf16_f32(hi >> 16)));
+          }
+        }
+      }
+
+      // ---- O^T += V^T P^T. V's operand: registers 0 and 1 of block s are
+      // columns d and d + 1 of rows 2t, 2t+1; registers 2 and 3 of rows 2t+8, 2t+9
+      uint32_t va[kSteps][4];
+      bool odd = false;  // a value that is not finite in a row that some query does not see
+      if constexpr (!Q4) {
+        const uint32_t vat = at + (D / 16) * 512 + lane * 16;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) {
+          uint4 w[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) w[r] = lds128(vat + (r * (D / 64) + j) * 512);
+          if (masked) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                odd |= (u[e] & 0x7f80u) == 0x7f80u || (u[e] & 0x7f800000u) == 0x7f800000u;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; r += 2) {
+            const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+            const uint32_t v[4] = {w[r + 1].x, w[r + 1].y, w[r + 1].z, w[r + 1].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              va[4 * j + e][r] = __byte_perm(u[e], v[e], 0x5410);
+              va[4 * j + e][r + 1] = __byte_perm(u[e], v[e], 0x7632);
+            }
+          }
+        }
+      } else {
+        constexpr int kWords = D / 64;
+        const uint32_t vat = at + kTile * (D / 2);
+        const uint32_t sat = at + kTile * D + D;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {  // rows t, t + 4; then t + 8, t + 12
+          uint32_t u[kWords], v[kWords];
+          if constexpr (D == 128) {
+            const uint2 x0 = lds64(vat + v_code_offset<D>(t + 8 * r, g * 8));
+            const uint2 x1 = lds64(vat + v_code_offset<D>(t + 8 * r + 4, g * 8));
+            u[0] = x0.x, u[1] = x0.y, v[0] = x1.x, v[1] = x1.y;
+          } else {
+            u[0] = lds32(vat + v_code_offset<D>(t + 8 * r, g * 4));
+            v[0] = lds32(vat + v_code_offset<D>(t + 8 * r + 4, g * 4));
+          }
+          const int group = D == 128 ? g : g >> 1;
+          const uint32_t b0 = lds8(sat + (t + 8 * r) * (D / 16) + group);
+          const uint32_t b1 = lds8(sat + (t + 8 * r + 4) * (D / 16) + group);
+          odd |= (b0 & 0x7fu) == 0x7fu || (b1 & 0x7fu) == 0x7fu;
+          const uint32_t sc = scales_f16x2(b0 | (b1 << 8));
+#pragma unroll
+          for (int i4 = 0; i4 < kWords; ++i4) {
+            uint32_t even[4], uneven[4];
+            codes_f16x2((u[i4] & 0x0f0f0f0fu) | ((v[i4] & 0x0f0f0f0fu) << 4), even);
+            codes_f16x2(((u[i4] >> 4) & 0x0f0f0f0fu) | (v[i4] & 0xf0f0f0f0u), uneven);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              va[4 * i4 + e][2 * r] = mul_f16x2(even[e], sc);
+              va[4 * i4 + e][2 * r + 1] = mul_f16x2(uneven[e], sc);
+            }
+          }
+        }
+      }
+      if (masked && __any_sync(0xffffffffu, odd)) {
+        // 0 times an infinity is no number: the products once for each new
+        // token, with the rows that it does not see cleared, and only the
+        // token's own columns of O taken from them
+        const int r0 = Q4 ? t : 2 * t, r1 = Q4 ? t + 4 : 2 * t + 1;  // and 8 further
+        for (int token = 0; token < seq.fresh; ++token) {
+          const int seen = a.causal ? seq.len - seq.fresh + token + 1 : seq.len;
+          uint32_t keep[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            keep[r] = (key + r0 + 8 * r < seen ? 0xffffu : 0u) |
+                      (key + r1 + 8 * r < seen ? 0xffff0000u : 0u);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const bool mine0 = (row0 + nt * 8 + 2 * t) % a.n_q == token;
+            const bool mine1 = (row0 + nt * 8 + 2 * t + 1) % a.n_q == token;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+              const uint32_t a0 = va[s][0] & keep[0], a1 = va[s][1] & keep[0];
+              const uint32_t a2 = va[s][2] & keep[1], a3 = va[s][3] & keep[1];
+              float y[4] = {o[nt][s][0], o[nt][s][1], o[nt][s][2], o[nt][s][3]};
+              mma<Q4>(y, a0, a1, a2, a3, p_hi[nt][0], p_hi[nt][1]);
+              if constexpr (!Q4) mma<Q4>(y, a0, a1, a2, a3, p_lo[nt][0], p_lo[nt][1]);
+              if (mine0) o[nt][s][0] = y[0], o[nt][s][2] = y[2];
+              if (mine1) o[nt][s][1] = y[1], o[nt][s][3] = y[3];
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma<Q4>(o[nt][s], va[s][0], va[s][1], va[s][2], va[s][3], p_hi[nt][0], p_hi[nt][1]);
+            if constexpr (!Q4)
+              mma<Q4>(o[nt][s], va[s][0], va[s][1], va[s][2], va[s][3], p_lo[nt][0], p_lo[nt][1]);
+          }
+      }
+    }
+    cp_async_wait<0>();
+
+    // ---- the four warps' results of these units, joined in shared memory
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int s = 4; s < 32; s <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], s);
+        if (g == 0) s_ml[warp][nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
+      }
+    __syncthreads();  // also: no warp uses its ring any more
+    float* o_smem = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = nt * 8 + 2 * t + c;
+        float top = s_ml[0][r].x;
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
+        const float f = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - top);
+        float* dst = o_smem + (warp * S::kRows + r) * S::kPitch;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          // block s of this thread: columns d, d + 1
+          const int d = Q4 ? g * (D / 8) + 8 * (s >> 2) + 2 * (s & 3)
+                           : 8 * (g + 8 * (s >> 2)) + 2 * (s & 3);
+          // a warp without a tile adds nothing, whatever f would multiply
+          *reinterpret_cast<float2*>(dst + d) =
+              make_float2(f == 0.f ? 0.f : o[nt][s][c] * f, f == 0.f ? 0.f : o[nt][s][2 + c] * f);
+        }
+      }
+    __syncthreads();
+    const bool whole = chunk == 0 && take == seq.units;
+    const int64_t slot = 2 * me + (chunk == 0 ? 1 : 0);
+    for (int i = tid; i < rows * (D / 2); i += kThreads) {
+      const int r = i / (D / 2), d = i % (D / 2) * 2;
+      float top = s_ml[0][r].x;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
+      float sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = s_ml[w][r];
+        sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);  // no row: 0, or no number
+        const float2 y = *reinterpret_cast<const float2*>(o_smem + (w * S::kRows + r) * S::kPitch + d);
+        y0 += y.x;
+        y1 += y.y;
+      }
+      if (whole) {
+        const bool real = (row0 + r) % a.n_q < seq.fresh;
+        // no row seen (sum 0), or padding: 0; a sum that is no number stays one
+        const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
+        *reinterpret_cast<uint32_t*>(a.out + (q_row0 + r) * D + d) =
+            inv == 0.f ? 0u : pack_bf16x2(y0 * inv, y1 * inv);
+      } else {
+        *reinterpret_cast<float2*>(a.part_o + (slot * S::kRows + r) * D + d) = make_float2(y0, y1);
+        if (d == 0) a.part_ml[slot * S::kRows + r] = make_float2(top, sum);
+      }
+    }
+    __syncthreads();  // shared memory is free for the next sequence
+    if (!whole && chunk == 0) {
+      // who finishes this pair: the block of its last unit
+      begun = b * pairs + pair;
+      const int64_t last = base * pairs + static_cast<int64_t>(pair + 1) * seq.units;
+      begun_last = static_cast<int>((last * blocks - 1) / total);
+    }
+    unit += take;
+    if (unit == (base + seq.units) * pairs) {
+      base += seq.units;
+      ++b;
+    }
+  }
+  if (tid == 0) a.split[me] = make_int2(begun, begun_last);
+}
+
+// Joins the partial results of the pair that block blockIdx.x of the first
+// kernel began and the blocks after it went on with: one query row per block
+// here, the columns over the threads and the contributions over groups of them.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const PagedArgs a,
+                                                                          int tile_rows) {
+  constexpr int kGroups = kMergeThreads / D;
+  __shared__ float weight[kMaxBlocks];
+  __shared__ float part[kGroups][D];
+  __shared__ float red[kMergeThreads / 32], red_l[kMergeThreads / 32];
+  const int tid = static_cast<int>(threadIdx.x);
+  griddep_wait();  // the partials are complete
+  griddep_launch_dependents();
+  const int2 split = a.split[blockIdx.x];
+  if (split.x < 0) return;
+  const int pairs = a.h_kv * a.row_tiles;
+  const int b = split.x / pairs, pair = split.x % pairs;
+  const int head = pair / a.row_tiles, row0 = pair % a.row_tiles * tile_rows;
+  const int r = static_cast<int>(blockIdx.y);
+  if (row0 + r >= a.rows) return;
+  const int first = static_cast<int>(blockIdx.x), n = split.y - first + 1;
+  // contribution i: the first block's second slot, then the others' first
+  auto slot = [&](int i) {
+    return (static_cast<int64_t>(2 * (first + i)) + (i == 0 ? 1 : 0)) * tile_rows + r;
+  };
+  float top = -INFINITY;
+  for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, a.part_ml[slot(i)].x);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+  if ((tid & 31) == 0) red[tid >> 5] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) top = fmaxf(top, red[w]);
+  float sum = 0.f;
+  for (int i = tid; i < n; i += kMergeThreads) {
+    const float2 ml = a.part_ml[slot(i)];
+    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    weight[i] = w;
+    sum += ml.x == -INFINITY ? ml.y : w * ml.y;  // no row: 0, or no number
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+  if ((tid & 31) == 0) red_l[tid >> 5] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < kMergeThreads / 32; ++w) sum += red_l[w];
+  const int d = tid % D, grp = tid / D;
+  float y = 0.f;
+#pragma unroll 8
+  for (int i = grp; i < n; i += kGroups) {
+    const float o = a.part_o[slot(i) * D + d];
+    y += weight[i] == 0.f ? 0.f : weight[i] * o;
+  }
+  part[grp][d] = y;
+  __syncthreads();
+  if (grp == 0) {
+#pragma unroll
+    for (int i = 1; i < kGroups; ++i) y += part[i][d];
+    const Sequence seq = sequence(a, b);
+    const bool real = (row0 + r) % a.n_q < seq.fresh;
+    const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
+    const int64_t row = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0 + r;
+    reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + d] =
+        __float2bfloat16_rn(inv == 0.f ? 0.f : y * inv);
+  }
+}
+
+// ------------------------------------------------------------------ launch
+
+struct Layout {
+  int row_tiles, tile_rows;
+  int64_t units;          // at most
+  int blocks;             // at most
+  size_t ml_off, o_off, total;
+};
+
+Layout layout(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pages) {
+  Layout w;
+  const int rows = h / h_kv * n_q;
+  w.tile_rows = 8 * column_blocks(rows);
+  w.row_tiles = (rows + w.tile_rows - 1) / w.tile_rows;
+  const int64_t per_pair = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
+  w.units = int64_t(B) * h_kv * w.row_tiles * per_pair;
+  w.blocks = static_cast<int>(w.units < kMaxBlocks ? w.units : kMaxBlocks);
+  auto align = [](size_t x) { return (x + 255u) & ~size_t(255u); };
+  w.ml_off = align(size_t(w.blocks) * sizeof(int2));
+  w.o_off = w.ml_off + align(size_t(w.blocks) * 2 * w.tile_rows * sizeof(float2));
+  w.total = w.o_off + align(size_t(w.blocks) * 2 * w.tile_rows * d * sizeof(float));
+  if (w.total < 256) w.total = 256;
+  return w;
+}
+
+// Blocks of this instance that fit on the current device at once (cached per device).
+template <typename Kernel>
+cudaError_t resident_blocks(Kernel kernel, int smem, int* cache, int* out) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  int n = dev >= 0 && dev < 64 ? __atomic_load_n(&cache[dev], __ATOMIC_ACQUIRE) : 0;
+  if (n == 0) {
+    int sms = 0, per_sm = 0;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+    if (e != cudaSuccess) return e;
+    if (sms < 1 || per_sm < 1) return cudaErrorInvalidConfiguration;
+    n = sms * per_sm;
+    if (dev >= 0 && dev < 64) __atomic_store_n(&cache[dev], n, __ATOMIC_RELEASE);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+template <int D, int NT, bool Q4>
+cudaError_t launch_instance(const PagedArgs& a, const Layout& w, cudaStream_t stream) {
+  auto kernel = decode_paged_kernel<D, NT, Q4>;
+  constexpr int smem = Shape<D, NT, Q4>::kSmem;
+  static unsigned long long configured = 0;
+  static int resident[64] = {};
+  cudaError_t e = set_smem_once(kernel, smem, &configured);
+  int fit = 0;
+  if (e == cudaSuccess) e = resident_blocks(kernel, smem, resident, &fit);
+  if (e != cudaSuccess) return e;
+  const unsigned blocks = static_cast<unsigned>(fit < w.blocks ? fit : w.blocks);
+  e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, a);
+  if (e != cudaSuccess) return e;
+  const unsigned rows = static_cast<unsigned>(a.rows < w.tile_rows ? a.rows : w.tile_rows);
+  return launch_pdl(decode_paged_merge_kernel<D>, dim3(blocks, rows), dim3(kMergeThreads), 0,
+                    stream, a, w.tile_rows);
 }
 
 template <int D, bool Q4>
-__global__ void __launch_bounds__(128) decode_paged_kernel(const PagedDecodeProblem p) {
-  constexpr int kCols = D / 32;
-  griddep_wait();
-  griddep_launch_dependents();
-  const PagedCache& c = p.cache;
-  const int lane = static_cast<int>(threadIdx.x) & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<int64_t>(p.B) * p.h * p.n_q) return;
-  const int t = static_cast<int>(row % p.n_q);
-  const int head = static_cast<int>(row / p.n_q % p.h);
-  const int b = static_cast<int>(row / p.n_q / p.h);
-  const int g = head / (p.h / c.h_kv);
-  const int capacity = c.max_pages << c.page_shift;
-  const int L = c.lens ? min(max(c.lens[b], 0), capacity) : capacity;
-  const int m = c.new_lens ? min(max(c.new_lens[b], 0), p.n_q) : p.n_q;
-  const int seen = t >= m ? 0 : (p.causal ? L - m + t + 1 : L);  // rows 0 .. seen - 1
-  float q[kCols], o[kCols];
-#pragma unroll
-  for (int i = 0; i < kCols; ++i) {
-    q[i] = bf16_f32(p.q[row * D + lane * kCols + i]) * p.scale;
-    o[i] = 0.f;
-  }
-  float top = -INFINITY, sum = 0.f;
-  for (int j = 0; j < seen; ++j) {
-    const int page = c.table[static_cast<int64_t>(b) * c.max_pages + (j >> c.page_shift)];
-    if (page < 0 || page >= c.n_pages) {
-      if (lane == 0) atomicOr(&g_device_error, kErrIndex);
-      continue;
-    }
-    const int64_t at = (((static_cast<int64_t>(page) * c.h_kv + g) << c.page_shift) +
-                        (j & ((1 << c.page_shift) - 1)));
-    float k[kCols], v[kCols];
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) {
-      const int col = lane * kCols + i;
-      if constexpr (Q4) {
-        const uint8_t kc = static_cast<const uint8_t*>(c.k)[at * (D / 2) + col / 2];
-        const uint8_t vc = static_cast<const uint8_t*>(c.v)[at * (D / 2) + col / 2];
-        k[i] = e2m1_f32(kc >> (4 * (col & 1))) * e4m3_f32(c.k_scales[at * (D / 16) + col / 16]) *
-               c.k_factor;
-        v[i] = e2m1_f32(vc >> (4 * (col & 1))) * e4m3_f32(c.v_scales[at * (D / 16) + col / 16]) *
-               c.v_factor;
-      } else {
-        k[i] = bf16_f32(static_cast<const uint16_t*>(c.k)[at * D + col]);
-        v[i] = bf16_f32(static_cast<const uint16_t*>(c.v)[at * D + col]);
-      }
-    }
-    float x = 0.f;
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) x = fmaf(q[i], k[i], x);
-#pragma unroll
-    for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    const float next = fmaxf(top, x);
-    const float keep = top == -INFINITY ? 0.f : __expf(top - next);
-    const float w = x == -INFINITY ? 0.f : __expf(x - next);
-    sum = sum * keep + w;
-#pragma unroll
-    for (int i = 0; i < kCols; ++i) o[i] = fmaf(w, v[i], o[i] * keep);
-    top = next;
-  }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
-#pragma unroll
-  for (int i = 0; i < kCols; ++i)
-    reinterpret_cast<__nv_bfloat16*>(p.out)[row * D + lane * kCols + i] =
-        __float2bfloat16_rn(o[i] * inv);
+cudaError_t launch_rows(const PagedArgs& a, const Layout& w, cudaStream_t stream) {
+  if (w.tile_rows == 8) return launch_instance<D, 1, Q4>(a, w, stream);
+  if (w.tile_rows == 16) return launch_instance<D, 2, Q4>(a, w, stream);
+  return launch_instance<D, 4, Q4>(a, w, stream);
 }
 
 }  // namespace
 
-size_t decode_paged_workspace_bytes(int, int, int, int, int, int, int) { return 256; }
+size_t decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
+                                    int max_pages) {
+  return layout(B, h, h_kv, n_q, d, page_size, max_pages).total;
+}
+
+int64_t decode_paged_units(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pages) {
+  return layout(B, h, h_kv, n_q, d, page_size, max_pages).units;
+}
 
 cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream) {
-  const int64_t rows = static_cast<int64_t>(p.B) * p.h * p.n_q;
-  if (rows < 1 || (rows + 3) / 4 > INT32_MAX) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>((rows + 3) / 4)), block(128);
-  const bool q4 = p.cache.k_scales != nullptr;
-  if (p.cache.d == 64)
-    return launch_pdl(q4 ? decode_paged_kernel<64, true> : decode_paged_kernel<64, false>, grid,
-                      block, 0, stream, p);
-  if (p.cache.d == 128)
-    return launch_pdl(q4 ? decode_paged_kernel<128, true> : decode_paged_kernel<128, false>, grid,
-                      block, 0, stream, p);
+  const PagedCache& c = p.cache;
+  const Layout w = layout(p.B, p.h, c.h_kv, p.n_q, c.d, 1 << c.page_shift, c.max_pages);
+  if (p.B < 1 || p.h < 1 || p.n_q < 1 || w.units > kPagedMaxUnits) return cudaErrorInvalidValue;
+  const bool q4 = c.k_scales != nullptr;
+  PagedArgs a;
+  a.q = p.q;
+  a.out = p.out;
+  a.k = static_cast<const uint8_t*>(c.k);
+  a.v = static_cast<const uint8_t*>(c.v);
+  a.k_scales = c.k_scales;
+  a.v_scales = c.v_scales;
+  a.table = c.table;
+  a.lens = c.lens;
+  a.new_lens = c.new_lens;
+  uint8_t* ws = static_cast<uint8_t*>(p.workspace);
+  a.split = reinterpret_cast<int2*>(ws);
+  a.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+  a.part_o = reinterpret_cast<float*>(ws + w.o_off);
+  a.B = p.B;
+  a.h_kv = c.h_kv;
+  a.n_q = p.n_q;
+  a.rows = p.h / c.h_kv * p.n_q;
+  a.row_tiles = w.row_tiles;
+  a.n_pages = c.n_pages;
+  a.page_shift = c.page_shift;
+  a.max_pages = c.max_pages;
+  a.causal = p.causal;
+  a.scale_log2 = p.scale * 1.4426950408889634f * (q4 ? c.k_factor : 1.f);
+  a.v_factor = q4 ? c.v_factor : 1.f;
+  if (c.d == 64) return q4 ? launch_rows<64, true>(a, w, stream) : launch_rows<64, false>(a, w, stream);
+  if (c.d == 128)
+    return q4 ? launch_rows<128, true>(a, w, stream) : launch_rows<128, false>(a, w, stream);
   return cudaErrorInvalidValue;
 }
 

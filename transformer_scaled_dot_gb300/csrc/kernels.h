@@ -235,6 +235,8 @@ struct PagedDecodeProblem {
   bool causal;
   float scale;        // logit factor (resolved: never 0)
 };
+constexpr int64_t kPagedMaxUnits = 1ll << 50;
+int64_t decode_paged_units(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pages);
 size_t decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
                                     int max_pages);
 cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream);
