@@ -61,7 +61,7 @@ def dequantise(codes, scales, factor):
 
 def decode(q, k_rows, v_rows, lens, new_lens, causal, scale):
     """q [B, h, n_q, d]; k_rows, v_rows: per sequence [h_kv, L, d]. Returns the output,
-    sum p |v| (what an error of the weights is relative to) with 2^-29 sum |v| added to it (below
+    sum p |v| (what an error of the weights is relative to) with 2^-25 sum |v| added to it (below
     which a weight's error is absolute), and the largest sum |q k| scale."""
     B, h, n_q, d = q.shape
     out, mass, size = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape[:3])
@@ -78,7 +78,7 @@ def decode(q, k_rows, v_rows, lens, new_lens, causal, scale):
                 w = np.exp(x - x.max())
                 w /= w.sum()
                 out[b, i, t] = w @ v
-                mass[b, i, t] = w @ np.abs(v) + 2.0 ** -29 * np.abs(v).sum(0)
+                mass[b, i, t] = w @ np.abs(v) + 2.0 ** -25 * np.abs(v).sum(0)
                 size[b, i, t] = (np.abs(k) @ np.abs(q[b, i, t])).max() * scale
     return out, mass, size
 
@@ -86,9 +86,9 @@ def decode(q, k_rows, v_rows, lens, new_lens, causal, scale):
 def decode_tolerance(ref, mass, size, n, d):
     """Largest |error| of an output element. The output's rounding to bf16: 2^-8 of the value.
     The weights: rounded to 11 bits or more (2^-11 each, and their sum is taken before the
-    rounding); the 4-bit cache's are numbers of f16 taken times 2^15, so that those under
-    2^-29 (2^-14, the least with 11 bits, over 2^15) of the largest are off by up to half of
-    f16's least step, 2^-25 / 2^15 = 2^-40 = 2^-11 2^-29; their exponents' error, twice the logit's (2 (d + 4) 2^-24 of sum |q k|, in 32
+    rounding); the 4-bit cache's are numbers of f16 taken times 2^11 or more, so that
+    those under 2^-25 (2^-14, the least with 11 bits, over 2^11) of the largest are off by up to
+    half of f16's least step, 2^-25 / 2^11 = 2^-36 = 2^-11 2^-25; their exponents' error, twice the logit's (2 (d + 4) 2^-24 of sum |q k|, in 32
     bits), and 2^-21 of the exponential itself; sums of n terms in 32 bits, n 2^-24."""
     weights = 2.0 ** -11 + 2 * (d + 4) * 2.0 ** -24 * size[..., None] + 2.0 ** -21 + n * 2.0 ** -24
     return 2.0 ** -8 * np.abs(ref) + 1.01 * weights * mass + 1e-30

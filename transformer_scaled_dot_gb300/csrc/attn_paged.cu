@@ -21,21 +21,25 @@
 //  * Products. A handful of query rows is far too few for a tcgen05 tile of
 //    128 rows, and the warp-wide m16n8k16 product reaches the cache's rate
 //    with room to spare: S^T = K Q^T with the 16 cached rows as its M and 8
-//    query rows as its N, then O^T += V^T P^T. The fragments of both come
-//    straight from the ring: a product's sum does not care about the order
-//    of its terms, so each thread's K columns are the ones it loaded with 16
-//    bytes, Q being laid out to match, and V's columns are numbered the same
-//    way. S^T's accumulators become P^T's operand through an 8 x 8 transpose
-//    within the warp (movmatrix).
+//    query rows as its N, then O^T += V^T P^T. S^T's accumulators become
+//    P^T's operand through an 8 x 8 transpose within the warp (movmatrix).
+//    bf16 fragments come from the ring by ldmatrix, V's transposed by it;
+//    4-bit codes are turned into f16 in registers, and since a product's sum
+//    does not care about the order of its terms, a thread's K columns are
+//    the ones that its 16 bytes hold, Q being laid out to match, and the two
+//    rows that share a register of V are interleaved before the conversion.
+//  * Softmax. The exponents' reference m follows the running maximum only
+//    when a value exceeds it by 2^kSlack: the common tile then needs no
+//    maximum over the warp, only a vote.
 //
 // Numbers: S, the softmax and O in fp32. With a bf16 cache P is split into
 // two bf16 parts, p = hi + lo (16 bits), at the cost of a second product
 // that the tensor cores have time for. With a 4-bit cache code * scale has
 // 6 significant bits and is formed in f16 without rounding; q is brought to
 // f16 by a power of two per row, which keeps every bf16 value within 2^-33
-// of the row's largest, and P, taken times 2^15, is rounded to f16: to 11
-// bits, well below the output's 8, where it is at least 2^-29 of the row's
-// largest in its warp, and to 2^-40 of that below.
+// of the row's largest; and P is rounded to f16: to 11 bits, well below the
+// output's 8, where it is at least 2^-25 of the row's largest in its warp
+// (m is 2^kShift below that), and to 2^-36 of that below.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -51,6 +55,7 @@ constexpr int kTile = 16;                // cached rows of a warp's step
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
 constexpr int kMergeThreads = 256;
+constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
 // Query rows of a block's tile: 8 per column block of the products.
 int column_blocks(int rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
@@ -82,17 +87,25 @@ struct Shape {
   static constexpr int kStageBytes = 2 * kTile * (kRowBytes + kScaleBytes);
   static constexpr int kStages = Q4 ? 4 : (D == 64 ? 4 : 3);
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-  static constexpr int kPitch = D + 2;  // floats of a row of O in shared memory
+  static constexpr int kPitch = D + 4;  // floats of a row of O in shared memory
+  // p = 2^(x - m) is at most 2^(kShift + kSlack); f16 holds up to 2^15.99
+  static constexpr float kShift = Q4 ? 11.f : 0.f, kSlack = Q4 ? 4.f : 8.f;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
   static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
 };
 
 // ------------------------------------------------------------------ instructions
 
+// FULL: 16 bytes; else `valid` decides whether they are read or zeros written.
+template <bool FULL>
 __device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;  // 0: nothing is read, zeros are written
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
+  if constexpr (FULL) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  } else {
+    const int n = valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                 : "memory");
+  }
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -125,6 +138,16 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   uint32_t r;
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
+}
+
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  if constexpr (TRANS)
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+  else
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
 }
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -198,51 +221,42 @@ __device__ __forceinline__ uint32_t v_code_offset(int row, int byte) {
 }
 
 // Copies the `valid` first of the 16 rows that start at row `at` of the pools
-// into a stage (the rest become zeros). bf16: each thread copies the very
-// 16-byte pieces that it will use, piece i of thread l at (i * 32 + l) * 16;
-// 4-bit: the tile as it is, the rows moved as above.
-template <int D, bool Q4>
+// into a stage; the rest become zeros. bf16: rows of 2 D bytes, keys then
+// values, 16-byte piece c of row r at c ^ (r & 7), which ldmatrix reads from
+// all banks; 4-bit: both sides' codes, rows moved as above, then their scales.
+template <int D, bool Q4, bool FULL>
 __device__ __forceinline__ void load_tile(uint32_t stage, const PagedArgs& a, int64_t at,
                                           int valid, int lane) {
-  if constexpr (!Q4) {
-    const int g = lane >> 2, t = lane & 3;
-    const uint8_t* k = a.k + at * (2 * D);
-    const uint8_t* v = a.v + at * (2 * D);
-    uint32_t dst = stage + lane * 16;
+  constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
+  constexpr int kPieces = kRowBytes / 16;              // of a row
+  constexpr int kRounds = kTile * kPieces / 32;        // a lane's pieces of each side
+  const uint8_t* k = a.k + at * kRowBytes + lane * 16;
+  const uint8_t* v = a.v + at * kRowBytes + lane * 16;
+  const int row0 = lane / kPieces, piece = lane % kPieces;
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-      for (int j = 0; j < D / 32; ++j) {
-        const int row = g + 8 * half;
-        cp_async_16(dst, k + row * (2 * D) + (t + 4 * j) * 16, row < valid);
-        dst += 512;
-      }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        const int row = 2 * t + (i & 1) + 4 * (i & 2);
-        cp_async_16(dst, v + row * (2 * D) + (g + 8 * j) * 16, row < valid);
-        dst += 512;
-      }
-  } else {
-    constexpr int kPieces = D / 32;  // 16-byte pieces of a row of codes
-    const uint8_t* k = a.k + at * (D / 2);
-    const uint8_t* v = a.v + at * (D / 2);
-#pragma unroll
-    for (int i = 0; i < kTile * kPieces / 32; ++i) {
-      const int piece = lane + 32 * i, row = piece / kPieces, byte = piece % kPieces * 16;
-      cp_async_16(stage + k_code_offset<D>(row, byte), k + piece * 16, row < valid);
-      cp_async_16(stage + kTile * (D / 2) + v_code_offset<D>(row, byte), v + piece * 16,
-                  row < valid);
+  for (int i = 0; i < kRounds; ++i) {
+    const int row = row0 + i * (32 / kPieces);
+    uint32_t k_off, v_off;
+    if constexpr (Q4) {
+      k_off = k_code_offset<D>(row, piece * 16);
+      v_off = v_code_offset<D>(row, piece * 16);
+    } else {
+      // row & 7 is row0 | the rounds' part, so the second is a constant
+      const uint32_t first = row0 * kRowBytes + ((piece ^ row0) << 4);
+      k_off = i * 512 + (first ^ (((i * (32 / kPieces)) & 7) << 4));
+      v_off = k_off;
     }
+    cp_async_16<FULL>(stage + k_off, k + i * 512, row < valid);
+    cp_async_16<FULL>(stage + kTile * kRowBytes + v_off, v + i * 512, row < valid);
+  }
+  if constexpr (Q4) {
     // the scales of 16 rows: D bytes for keys, D for values; 16 bytes hold
     // several rows' scales, those past `valid` meet codes of zero
     constexpr int kRowsIn16 = 256 / D;
-    const int piece = lane % (D / 16);
+    const int part = lane % (D / 16);
     if (lane < D / 8) {
       const uint8_t* s = (lane < D / 16 ? a.k_scales : a.v_scales) + at * (D / 16);
-      cp_async_16(stage + kTile * D + lane * 16, s + piece * 16, piece * kRowsIn16 < valid);
+      cp_async_16<FULL>(stage + kTile * D + lane * 16, s + part * 16, part * kRowsIn16 < valid);
     }
   }
 }
@@ -351,10 +365,16 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       const uint16_t* qp = a.q + (q_row0 + nt * 8 + g) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        const int col = Q4 ? t * (D / 4) + 4 * s : 8 * (t + 4 * (s >> 1)) + 4 * (s & 1);
-        const uint2 w = live ? __ldcg(reinterpret_cast<const uint2*>(qp + col)) : make_uint2(0, 0);
-        qf[nt][s][0] = w.x;
-        qf[nt][s][1] = w.y;
+        if constexpr (Q4) {
+          const uint2 w = live ? __ldcg(reinterpret_cast<const uint2*>(qp + t * (D / 4) + 4 * s))
+                               : make_uint2(0, 0);
+          qf[nt][s][0] = w.x;
+          qf[nt][s][1] = w.y;
+        } else {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * t);
+          qf[nt][s][0] = live ? __ldcg(w) : 0u;
+          qf[nt][s][1] = live ? __ldcg(w + 4) : 0u;
+        }
       }
       mult[nt][0] = mult[nt][1] = a.scale_log2;
       if constexpr (Q4) {
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // exponent field e of the largest: times 2^(135 - e) in two factors,
         // since 135 - e may pass a float's exponents by itself
-        const int e = min(max(static_cast<int>(top >> 7), 1), 254);
+        const int e = top == 0 ? 127 : min(max(static_cast<int>(top >> 7), 1), 254);
         const int up = 135 - e, up0 = up / 2, up1 = up - up0;
         const float f0 = __int_as_float((127 + up0) << 23), f1 = __int_as_float((127 + up1) << 23);
 #pragma unroll
@@ -384,8 +404,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         for (int i = 0; i < 2; ++i) {
           const int e_col = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4) - 135;
           const int d0 = e_col / 2, d1 = e_col - d0;
-          mult[nt][i] = a.scale_log2 * __int_as_float((127 + d0) << 23) *
-                        __int_as_float((127 + d1) << 23);
+          // not 0, which would make the masks' -inf no number
+          mult[nt][i] = fmaxf(a.scale_log2 * __int_as_float((127 + d0) << 23) *
+                                  __int_as_float((127 + d1) << 23), 1.2e-38f);
         }
       }
 #pragma unroll
@@ -406,7 +427,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) o[nt][s][0] = o[nt][s][1] = o[nt][s][2] = o[nt][s][3] = 0.f;
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kLowest;
       l[nt][0] = l[nt][1] = 0.f;
     }
 
@@ -421,53 +442,60 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
     };
     int pages = page_of(lane), pages_next = page_of(32 + lane);
     uint32_t skipped = 0;  // bit s: the tile in stage s has no page
-    auto issue = [&](int i) {  // tile i into stage i % kStages
+    int fill = 0;          // the stage that is filled next
+    auto issue = [&](int i) {  // tile i into the next stage
       if (i < tiles) {
         if ((i & 31) == 0 && i > 0) {
           pages = pages_next;
           pages_next = page_of(i + 32 + lane);
         }
         const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        const int stage = i % S::kStages;
         const int key = first_key + i * kUnit;
         if (page < 0 || page >= a.n_pages) {
-          skipped |= 1u << stage;
+          skipped |= 1u << fill;
           if (lane == 0) atomicOr(&g_device_error, kErrIndex);
         } else {
-          skipped &= ~(1u << stage);
+          skipped &= ~(1u << fill);
           const int64_t at = ((static_cast<int64_t>(page) * a.h_kv + head) << a.page_shift) +
                              (key & ((1 << a.page_shift) - 1));
-          load_tile<D, Q4>(ring + stage * S::kStageBytes, a, at, key1 - key, lane);
+          const uint32_t stage = ring + fill * S::kStageBytes;
+          if (key1 - key >= kTile) load_tile<D, Q4, true>(stage, a, at, kTile, lane);
+          else load_tile<D, Q4, false>(stage, a, at, key1 - key, lane);
         }
       }
       cp_async_commit();
+      fill = fill == S::kStages - 1 ? 0 : fill + 1;
     };
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
+    int stage = 0;
     for (int i = 0; i < tiles; ++i) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
       issue(i + S::kStages - 1);
-      const int stage = i % S::kStages;
-      if (skipped & (1u << stage)) continue;
       const uint32_t at = ring + stage * S::kStageBytes;
+      const bool skip = skipped & (1u << stage);
+      stage = stage == S::kStages - 1 ? 0 : stage + 1;
+      if (skip) continue;
       const int key = first_key + i * kUnit;
 
-      // ---- S^T = K Q^T
-      float x[NT][4];
+      // ---- S^T = K Q^T, even and odd steps apart: shorter chains of products
+      float x[NT][4], x2[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[nt][c] = x2[nt][c] = 0.f;
       if constexpr (!Q4) {
+        const uint32_t kat = at + (lane & 15) * (2 * D);
+        const uint32_t swz = (lane >> 4) ^ (lane & 7);
 #pragma unroll
-        for (int j = 0; j < D / 32; ++j) {
-          const uint4 lo = lds128(at + j * 512 + lane * 16);
-          const uint4 hi = lds128(at + (D / 32 + j) * 512 + lane * 16);
+        for (int s = 0; s < kSteps; ++s) {
+          uint32_t w[4];
+          ldmatrix4<false>(w, kat + ((swz ^ (2 * s)) << 4));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<false>(x[nt], lo.x, hi.x, lo.y, hi.y, qf[nt][2 * j][0], qf[nt][2 * j][1]);
-            mma<false>(x[nt], lo.z, hi.z, lo.w, hi.w, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
-          }
+          for (int nt = 0; nt < NT; ++nt)
+            mma<false>(s & 1 ? x2[nt] : x[nt], w[0], w[1], w[2], w[3], qf[nt][s][0], qf[nt][s][1]);
         }
       } else {
         constexpr int kWords = D / 32;  // of this thread's codes of one row
@@ -501,47 +529,45 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma<true>(x[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][2 * i4][0], qf[nt][2 * i4][1]);
-            mma<true>(x[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][2 * i4 + 1][0],
+            mma<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][2 * i4 + 1][0],
                       qf[nt][2 * i4 + 1][1]);
           }
         }
       }
 
-      // ---- x, masks, the running maximum
+      // ---- masks; x - m, and whether any passes what P may be
       const int row_lo = Q4 ? cached_row(g) : g, row_hi = row_lo + 8;
       const bool masked = key + kTile > hidden;
-      bool grew = false;
-      float next[NT][2];
+      bool over = false;
+      float y[NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          x[nt][c] *= mult[nt][c];
-          x[nt][2 + c] *= mult[nt][c];
-          if (masked) {
-            if (key + row_lo >= limit[nt][c]) x[nt][c] = -INFINITY;
-            if (key + row_hi >= limit[nt][c]) x[nt][2 + c] = -INFINITY;
-          }
-          float top = fmaxf(x[nt][c], x[nt][2 + c]);
-#pragma unroll
-          for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-          next[nt][c] = fmaxf(m[nt][c], top);
-          grew |= next[nt][c] > m[nt][c];
+        for (int c = 0; c < 4; ++c) {
+          x[nt][c] += x2[nt][c];
+          if (masked && key + (c < 2 ? row_lo : row_hi) >= limit[nt][c & 1]) x[nt][c] = -INFINITY;
+          y[nt][c] = fmaf(x[nt][c], mult[nt][c & 1], -m[nt][c & 1]);
+          over |= y[nt][c] > S::kShift + S::kSlack;
         }
-      }
-      if (__any_sync(0xffffffffu, grew)) {
+      if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float f = next[nt][c] > m[nt][c] ? ex2(m[nt][c] - next[nt][c]) : 1.f;
-            m[nt][c] = next[nt][c];
+            float top = fmaxf(x[nt][c], x[nt][2 + c]) * mult[nt][c];
+#pragma unroll
+            for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            const float next = fmaxf(m[nt][c], top - S::kShift);
+            const float f = ex2(m[nt][c] - next);
+            m[nt][c] = next;
             l[nt][c] *= f;
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
               o[nt][s][c] *= f;
               o[nt][s][2 + c] *= f;
             }
+            y[nt][c] = fmaf(x[nt][c], mult[nt][c], -next);
+            y[nt][2 + c] = fmaf(x[nt][2 + c], mult[nt][c], -next);
           }
       }
 
@@ -551,13 +577,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       for (int nt = 0; nt < NT; ++nt) {
         float p[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          // 4-bit: P, and with it l and O, carry a factor 2^15
-          const float m_use = (m[nt][c] == -INFINITY ? 0.f : m[nt][c]) - (Q4 ? 15.f : 0.f);
-          p[c] = ex2(x[nt][c] - m_use);
-          p[2 + c] = ex2(x[nt][2 + c] - m_use);
-          l[nt][c] += p[c] + p[2 + c];
-        }
+        for (int c = 0; c < 4; ++c) p[c] = ex2(y[nt][c]);
+        l[nt][0] += p[0] + p[2];
+        l[nt][1] += p[1] + p[3];
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           const float p0 = p[2 * half], p1 = p[2 * half + 1];
@@ -572,67 +594,63 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         }
       }
 
-      // ---- O^T += V^T P^T. V's operand: registers 0 and 1 of block s are
-      // columns d and d + 1 of rows 2t, 2t+1; registers 2 and 3 of rows 2t+8, 2t+9
-      uint32_t va[kSteps][4];
-      bool odd = false;  // a value that is not finite in a row that some query does not see
-      if constexpr (!Q4) {
-        const uint32_t vat = at + (D / 16) * 512 + lane * 16;
+      // ---- O^T += V^T P^T. Registers 0 and 1 of V's operand are two columns
+      // of cached rows r0 and r1, registers 2 and 3 of the rows 8 further
+      const uint32_t vat = at + kTile * S::kRowBytes;
+      uint32_t v_codes[2][2][D / 64], v_scale[2];  // 4-bit: [rows' half][r0, r1][word]
+      bool odd = false;  // a value that is not finite
+      if constexpr (Q4) {
+        const uint32_t sat = at + kTile * D + D;
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          uint4 w[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) w[r] = lds128(vat + (r * (D / 64) + j) * 512);
-          if (masked) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                odd |= (u[e] & 0x7f80u) == 0x7f80u || (u[e] & 0x7f800000u) == 0x7f800000u;
-            }
+        for (int r = 0; r < 2; ++r) {
+          const int a0 = t + 8 * r, a1 = a0 + 4;
+          if constexpr (D == 128) {
+            const uint2 w0 = lds64(vat + v_code_offset<D>(a0, g * 8));
+            const uint2 w1 = lds64(vat + v_code_offset<D>(a1, g * 8));
+            v_codes[r][0][0] = w0.x, v_codes[r][0][1] = w0.y;
+            v_codes[r][1][0] = w1.x, v_codes[r][1][1] = w1.y;
+          } else {
+            v_codes[r][0][0] = lds32(vat + v_code_offset<D>(a0, g * 4));
+            v_codes[r][1][0] = lds32(vat + v_code_offset<D>(a1, g * 4));
           }
+          const int group = D == 128 ? g : g >> 1;
+          const uint32_t two = lds8(sat + a0 * (D / 16) + group) |
+                               (lds8(sat + a1 * (D / 16) + group) << 8);
+          if (masked) odd |= (two & 0x7fu) == 0x7fu || (two & 0x7f00u) == 0x7f00u;
+          v_scale[r] = scales_f16x2(two);
+        }
+      }
+      // the operand of kBlock blocks of 16 columns from block s0 on
+      constexpr int kBlock = Q4 ? 4 : 1;
+      auto v_operand = [&](int s0, uint32_t (&va)[kBlock][4]) {
+        if constexpr (!Q4) {
+          const uint32_t row = (lane & 7) + ((lane >> 4) << 3);
+          ldmatrix4<true>(va[0], vat + row * (2 * D) +
+                                     (((2 * s0) ^ ((lane >> 3) & 1) ^ (lane & 7)) << 4));
+        } else {
 #pragma unroll
-          for (int r = 0; r < 4; r += 2) {
-            const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
-            const uint32_t v[4] = {w[r + 1].x, w[r + 1].y, w[r + 1].z, w[r + 1].w};
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t u = v_codes[r][0][s0 / 4], v = v_codes[r][1][s0 / 4];
+            uint32_t even[4], uneven[4];
+            codes_f16x2((u & 0x0f0f0f0fu) | ((v & 0x0f0f0f0fu) << 4), even);
+            codes_f16x2(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), uneven);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              va[4 * j + e][r] = __byte_perm(u[e], v[e], 0x5410);
-              va[4 * j + e][r + 1] = __byte_perm(u[e], v[e], 0x7632);
+              va[e][2 * r] = mul_f16x2(even[e], v_scale[r]);
+              va[e][2 * r + 1] = mul_f16x2(uneven[e], v_scale[r]);
             }
           }
         }
-      } else {
-        constexpr int kWords = D / 64;
-        const uint32_t vat = at + kTile * (D / 2);
-        const uint32_t sat = at + kTile * D + D;
+      };
+      if constexpr (!Q4) {
+        if (masked) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {  // rows t, t + 4; then t + 8, t + 12
-          uint32_t u[kWords], v[kWords];
-          if constexpr (D == 128) {
-            const uint2 x0 = lds64(vat + v_code_offset<D>(t + 8 * r, g * 8));
-            const uint2 x1 = lds64(vat + v_code_offset<D>(t + 8 * r + 4, g * 8));
-            u[0] = x0.x, u[1] = x0.y, v[0] = x1.x, v[1] = x1.y;
-          } else {
-            u[0] = lds32(vat + v_code_offset<D>(t + 8 * r, g * 4));
-            v[0] = lds32(vat + v_code_offset<D>(t + 8 * r + 4, g * 4));
-          }
-          const int group = D == 128 ? g : g >> 1;
-          const uint32_t b0 = lds8(sat + (t + 8 * r) * (D / 16) + group);
-          const uint32_t b1 = lds8(sat + (t + 8 * r + 4) * (D / 16) + group);
-          odd |= (b0 & 0x7fu) == 0x7fu || (b1 & 0x7fu) == 0x7fu;
-          const uint32_t sc = scales_f16x2(b0 | (b1 << 8));
+          for (int s = 0; s < kSteps; ++s) {
+            uint32_t va[1][4];
+            v_operand(s, va);
 #pragma unroll
-          for (int i4 = 0; i4 < kWords; ++i4) {
-            uint32_t even[4], uneven[4];
-            codes_f16x2((u[i4] & 0x0f0f0f0fu) | ((v[i4] & 0x0f0f0f0fu) << 4), even);
-            codes_f16x2(((u[i4] >> 4) & 0x0f0f0f0fu) | (v[i4] & 0xf0f0f0f0u), uneven);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              va[4 * i4 + e][2 * r] = mul_f16x2(even[e], sc);
-              va[4 * i4 + e][2 * r + 1] = mul_f16x2(uneven[e], sc);
-            }
+            for (int e = 0; e < 4; ++e)
+              odd |= (va[0][e] & 0x7f80u) == 0x7f80u || (va[0][e] & 0x7f800000u) == 0x7f800000u;
           }
         }
       }
@@ -640,7 +658,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         // 0 times an infinity is no number: the products once for each new
         // token, with the rows that it does not see cleared, and only the
         // token's own columns of O taken from them
-        const int r0 = Q4 ? t : 2 * t, r1 = Q4 ? t + 4 : 2 * t + 1;  // and 8 further
+        const int r0 = Q4 ? t : 2 * t, r1 = Q4 ? t + 4 : 2 * t + 1;
         for (int token = 0; token < seq.fresh; ++token) {
           const int seen = a.causal ? seq.len - seq.fresh + token + 1 : seq.len;
           uint32_t keep[2];
@@ -649,30 +667,40 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
             keep[r] = (key + r0 + 8 * r < seen ? 0xffffu : 0u) |
                       (key + r1 + 8 * r < seen ? 0xffff0000u : 0u);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const bool mine0 = (row0 + nt * 8 + 2 * t) % a.n_q == token;
-            const bool mine1 = (row0 + nt * 8 + 2 * t + 1) % a.n_q == token;
+          for (int s = 0; s < kSteps; s += kBlock) {
+            uint32_t va[kBlock][4];
+            v_operand(s, va);
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-              const uint32_t a0 = va[s][0] & keep[0], a1 = va[s][1] & keep[0];
-              const uint32_t a2 = va[s][2] & keep[1], a3 = va[s][3] & keep[1];
-              float y[4] = {o[nt][s][0], o[nt][s][1], o[nt][s][2], o[nt][s][3]};
-              mma<Q4>(y, a0, a1, a2, a3, p_hi[nt][0], p_hi[nt][1]);
-              if constexpr (!Q4) mma<Q4>(y, a0, a1, a2, a3, p_lo[nt][0], p_lo[nt][1]);
-              if (mine0) o[nt][s][0] = y[0], o[nt][s][2] = y[2];
-              if (mine1) o[nt][s][1] = y[1], o[nt][s][3] = y[3];
-            }
+            for (int e = 0; e < kBlock; ++e)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const uint32_t a0 = va[e][0] & keep[0], a1 = va[e][1] & keep[0];
+                const uint32_t a2 = va[e][2] & keep[1], a3 = va[e][3] & keep[1];
+                float (&acc)[4] = o[nt][s + e];
+                float z[4] = {acc[0], acc[1], acc[2], acc[3]};
+                mma<Q4>(z, a0, a1, a2, a3, p_hi[nt][0], p_hi[nt][1]);
+                if constexpr (!Q4) mma<Q4>(z, a0, a1, a2, a3, p_lo[nt][0], p_lo[nt][1]);
+                if ((row0 + nt * 8 + 2 * t) % a.n_q == token) acc[0] = z[0], acc[2] = z[2];
+                if ((row0 + nt * 8 + 2 * t + 1) % a.n_q == token) acc[1] = z[1], acc[3] = z[3];
+              }
           }
         }
       } else {
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s)
+        for (int s = 0; s < kSteps; s += kBlock) {
+          uint32_t va[kBlock][4];
+          v_operand(s, va);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma<Q4>(o[nt][s], va[s][0], va[s][1], va[s][2], va[s][3], p_hi[nt][0], p_hi[nt][1]);
-            if constexpr (!Q4)
-              mma<Q4>(o[nt][s], va[s][0], va[s][1], va[s][2], va[s][3], p_lo[nt][0], p_lo[nt][1]);
-          }
+          for (int e = 0; e < kBlock; ++e)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_hi[nt][0],
+                      p_hi[nt][1]);
+              if constexpr (!Q4)
+                mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_lo[nt][0],
+                        p_lo[nt][1]);
+            }
+        }
       }
     }
     cp_async_wait<0>();
@@ -696,16 +724,14 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         float top = s_ml[0][r].x;
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
-        const float f = m[nt][c] == -INFINITY ? 0.f : ex2(m[nt][c] - top);
+        const float f = ex2(m[nt][c] - top);  // a warp without a row has O = l = 0
         float* dst = o_smem + (warp * S::kRows + r) * S::kPitch;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
-          // block s of this thread: columns d, d + 1
-          const int d = Q4 ? g * (D / 8) + 8 * (s >> 2) + 2 * (s & 3)
-                           : 8 * (g + 8 * (s >> 2)) + 2 * (s & 3);
-          // a warp without a tile adds nothing, whatever f would multiply
-          *reinterpret_cast<float2*>(dst + d) =
-              make_float2(f == 0.f ? 0.f : o[nt][s][c] * f, f == 0.f ? 0.f : o[nt][s][2 + c] * f);
+          // the two columns of block s that this thread has
+          const int d0 = Q4 ? g * (D / 8) + 8 * (s >> 2) + 2 * (s & 3) : 16 * s + g;
+          dst[d0] = o[nt][s][c] * f;
+          dst[d0 + (Q4 ? 1 : 8)] = o[nt][s][2 + c] * f;
         }
       }
     __syncthreads();
@@ -720,7 +746,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w][r];
-        sum += ml.x == -INFINITY ? ml.y : ml.y * ex2(ml.x - top);  // no row: 0, or no number
+        sum += ml.y * ex2(ml.x - top);
         const float2 y = *reinterpret_cast<const float2*>(o_smem + (w * S::kRows + r) * S::kPitch + d);
         y0 += y.x;
         y1 += y.y;
@@ -777,7 +803,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   auto slot = [&](int i) {
     return (static_cast<int64_t>(2 * (first + i)) + (i == 0 ? 1 : 0)) * tile_rows + r;
   };
-  float top = -INFINITY;
+  float top = kLowest;
   for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, a.part_ml[slot(i)].x);
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
@@ -788,9 +814,9 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   float sum = 0.f;
   for (int i = tid; i < n; i += kMergeThreads) {
     const float2 ml = a.part_ml[slot(i)];
-    const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+    const float w = ex2(ml.x - top);
     weight[i] = w;
-    sum += ml.x == -INFINITY ? ml.y : w * ml.y;  // no row: 0, or no number
+    sum += w * ml.y;
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
@@ -804,7 +830,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
 #pragma unroll 8
   for (int i = grp; i < n; i += kGroups) {
     const float o = a.part_o[slot(i) * D + d];
-    y += weight[i] == 0.f ? 0.f : weight[i] * o;
+    y += weight[i] * o;
   }
   part[grp][d] = y;
   __syncthreads();
