@@ -54,7 +54,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                // cached rows of a warp's step
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
 // Query rows of a block's tile: 8 per column block of the products.
@@ -70,7 +70,11 @@ struct PagedArgs {
   const int32_t* table;
   const int32_t* lens;
   const int32_t* new_lens;
-  int2* split;     // [blocks] (pair that block i begins and others finish, or -1; last block)
+  // what the merge has to join: by_pair, entry p is pair p's (first block, last
+  // block), first -1 if one block did it all; else entry i is the pair that
+  // block i begins and others finish (or -1), and its last block
+  int2* split;
+  bool by_pair;
   float* part_o;   // [blocks][2][rows of a tile][d]
   float2* part_ml; // [blocks][2][rows of a tile]
   int B, h_kv, n_q, rows, row_tiles, n_pages, page_shift, max_pages;
@@ -88,6 +92,7 @@ struct Shape {
   static constexpr int kStages = Q4 ? 4 : (D == 64 ? 4 : 3);
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kPitch = D + 4;  // floats of a row of O in shared memory
+  static constexpr bool kQInSmem = NT * D > 128;
   // p = 2^(x - m) is at most 2^(kShift + kSlack); f16 holds up to 2^15.99
   static constexpr float kShift = Q4 ? 11.f : 0.f, kSlack = Q4 ? 4.f : 8.f;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
@@ -291,6 +296,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
   constexpr int kSteps = D / 16;  // products of S, and blocks of 16 columns of O
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps][S::kRows];
+  __shared__ float s_mult[S::kRows];
+  __shared__ int s_limit[S::kRows];
+  __shared__ uint2 s_q[S::kQInSmem ? kSteps * NT : 1][32];
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   griddep_wait();  // the cache, queries, lengths and tables may come from the previous kernel
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);
   const int64_t me = blockIdx.x;
   if (me >= blocks) {
-    if (tid == 0) a.split[me] = make_int2(-1, 0);
+    if (tid == 0 && !a.by_pair) a.split[me] = make_int2(-1, 0);
     return;
   }
   const int64_t each = quotient(total, blocks), left = total - each * blocks;
@@ -354,38 +362,38 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
     const int key1 = seq.fresh > 0 ? min(seq.len, (chunk + take) * kUnit) : 0;
     const int64_t q_row0 = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0;
 
-    // ---- queries as the products' operand: b0 and b1 of step s hold the
-    // columns that the threads' K registers of that step hold
-    uint32_t qf[NT][kSteps][2];
-    float mult[NT][2];  // the factor from S to x of this thread's two rows
-    int limit[NT][2];   // they see the cached rows before these
+    // ---- queries as the products' operand: registers 0 and 1 of step s hold
+    // the columns that the threads' K registers of that step hold. In shared
+    // memory where they would take too many registers.
+    uint32_t qf[S::kQInSmem ? 1 : NT][S::kQInSmem ? 1 : kSteps][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
+      if (S::kQInSmem && nt != warp) continue;  // a warp for each
+      uint32_t w[kSteps][2];
       const bool live = nt * 8 + g < rows;
       const uint16_t* qp = a.q + (q_row0 + nt * 8 + g) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         if constexpr (Q4) {
-          const uint2 w = live ? __ldcg(reinterpret_cast<const uint2*>(qp + t * (D / 4) + 4 * s))
-                               : make_uint2(0, 0);
-          qf[nt][s][0] = w.x;
-          qf[nt][s][1] = w.y;
+          const uint2 two = live ? __ldcg(reinterpret_cast<const uint2*>(qp + t * (D / 4) + 4 * s))
+                                 : make_uint2(0, 0);
+          w[s][0] = two.x;
+          w[s][1] = two.y;
         } else {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * t);
-          qf[nt][s][0] = live ? __ldcg(w) : 0u;
-          qf[nt][s][1] = live ? __ldcg(w + 4) : 0u;
+          const uint32_t* src = reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * t);
+          w[s][0] = live ? __ldcg(src) : 0u;
+          w[s][1] = live ? __ldcg(src + 4) : 0u;
         }
       }
-      mult[nt][0] = mult[nt][1] = a.scale_log2;
       if constexpr (Q4) {
         // the row's largest magnitude decides a power of two that brings it
-        // below 2^9; what was 2^-33 of it or less may lose bits
+        // below 2^9; what is 2^-33 of it or less may lose bits
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            top = max(top, max(qf[nt][s][i] & 0x7fffu, (qf[nt][s][i] >> 16) & 0x7fffu));
+            top = max(top, max(w[s][i] & 0x7fffu, (w[s][i] >> 16) & 0x7fffu));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // exponent field e of the largest: times 2^(135 - e) in two factors,
@@ -396,27 +404,30 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t w = qf[nt][s][i];
-            qf[nt][s][i] = pack_f16x2(bf16_f32(w & 0xffffu) * f0 * f1, bf16_f32(w >> 16) * f0 * f1);
-          }
+          for (int i = 0; i < 2; ++i)
+            w[s][i] = pack_f16x2(bf16_f32(w[s][i] & 0xffffu) * f0 * f1, bf16_f32(w[s][i] >> 16) * f0 * f1);
+        // the factor from S to x; not 0, which would make the masks' -inf no number
+        const float d0 = __int_as_float((127 - up0) << 23), d1 = __int_as_float((127 - up1) << 23);
+        if (t == 0) s_mult[nt * 8 + g] = fmaxf(a.scale_log2 * d0 * d1, 1.2e-38f);
+      }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int e_col = __shfl_sync(0xffffffffu, e, (2 * t + i) * 4) - 135;
-          const int d0 = e_col / 2, d1 = e_col - d0;
-          // not 0, which would make the masks' -inf no number
-          mult[nt][i] = fmaxf(a.scale_log2 * __int_as_float((127 + d0) << 23) *
-                                  __int_as_float((127 + d1) << 23), 1.2e-38f);
+      for (int s = 0; s < kSteps; ++s) {
+        if constexpr (S::kQInSmem) {
+          s_q[s * NT + nt][lane] = make_uint2(w[s][0], w[s][1]);
+        } else {
+          qf[nt][s][0] = w[s][0];
+          qf[nt][s][1] = w[s][1];
         }
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = nt * 8 + 2 * t + i;
-        const int token = (row0 + r) % a.n_q;
-        limit[nt][i] = 0x7fffffff;  // columns that nobody reads: no mask needed
-        if (r < rows && token < seq.fresh && a.causal) limit[nt][i] = seq.len - seq.fresh + token + 1;
-        if (r < rows && token < seq.fresh) limit[nt][i] = min(limit[nt][i], seq.len);
+    }
+    if (tid < S::kRows) {  // row tid of the tile sees the cached rows before its limit
+      const int token = (row0 + tid) % a.n_q;
+      int limit = 0x7fffffff;  // rows that nobody reads need no mask
+      if (tid < rows && token < seq.fresh) {
+        limit = seq.len;
+        if (a.causal) limit = min(limit, seq.len - seq.fresh + token + 1);
       }
+      s_limit[tid] = limit;
     }
     // cached rows from here on are hidden from some row of the tile
     const int hidden = a.causal ? min(seq.len, seq.len - seq.fresh + 1) : seq.len;
@@ -469,6 +480,16 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) issue(i);
 
+    __syncthreads();  // s_limit, s_mult, s_q
+    float mult[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) mult[nt][c] = Q4 ? s_mult[nt * 8 + 2 * t + c] : a.scale_log2;
+    auto query = [&](int nt, int s) {
+      if constexpr (S::kQInSmem) return s_q[s * NT + nt][lane];
+      else return make_uint2(qf[nt][s][0], qf[nt][s][1]);
+    };
     int stage = 0;
     for (int i = 0; i < tiles; ++i) {
       cp_async_wait<S::kStages - 2>();
@@ -480,7 +501,8 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       if (skip) continue;
       const int key = first_key + i * kUnit;
 
-      // ---- S^T = K Q^T, even and odd steps apart: shorter chains of products
+      // ---- S^T = K Q^T; for one column block even and odd steps apart, as
+      // one chain of dependent products would be waited for
       float x[NT][4], x2[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -495,7 +517,10 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
           ldmatrix4<false>(w, kat + ((swz ^ (2 * s)) << 4));
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma<false>(s & 1 ? x2[nt] : x[nt], w[0], w[1], w[2], w[3], qf[nt][s][0], qf[nt][s][1]);
+          {
+            const uint2 q = query(nt, s);
+            mma<false>(NT == 1 && (s & 1) ? x2[nt] : x[nt], w[0], w[1], w[2], w[3], q.x, q.y);
+          }
         }
       } else {
         constexpr int kWords = D / 32;  // of this thread's codes of one row
@@ -528,9 +553,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma<true>(x[nt], lo[0], hi[0], lo[1], hi[1], qf[nt][2 * i4][0], qf[nt][2 * i4][1]);
-            mma<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], qf[nt][2 * i4 + 1][0],
-                      qf[nt][2 * i4 + 1][1]);
+            const uint2 q0 = query(nt, 2 * i4), q1 = query(nt, 2 * i4 + 1);
+            mma<true>(x[nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
+            mma<true>(NT == 1 ? x2[nt] : x[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
           }
         }
       }
@@ -544,8 +569,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          x[nt][c] += x2[nt][c];
-          if (masked && key + (c < 2 ? row_lo : row_hi) >= limit[nt][c & 1]) x[nt][c] = -INFINITY;
+          if (NT == 1) x[nt][c] += x2[nt][c];
+          if (masked && key + (c < 2 ? row_lo : row_hi) >= s_limit[nt * 8 + 2 * t + (c & 1)])
+            x[nt][c] = -INFINITY;
           y[nt][c] = fmaf(x[nt][c], mult[nt][c & 1], -m[nt][c & 1]);
           over |= y[nt][c] > S::kShift + S::kSlack;
         }
@@ -763,11 +789,16 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       }
     }
     __syncthreads();  // shared memory is free for the next sequence
-    if (!whole && chunk == 0) {
-      // who finishes this pair: the block of its last unit
-      begun = b * pairs + pair;
+    if (chunk == 0) {
+      // the block of this pair's last unit
       const int64_t last = base * pairs + static_cast<int64_t>(pair + 1) * seq.units;
-      begun_last = static_cast<int>((last * blocks - 1) / total);
+      const int last_block = static_cast<int>(quotient(last * blocks - 1, total));
+      if (a.by_pair) {
+        if (tid == 0) a.split[b * pairs + pair] = make_int2(whole ? -1 : static_cast<int>(me), last_block);
+      } else if (!whole) {
+        begun = b * pairs + pair;
+        begun_last = last_block;
+      }
     }
     unit += take;
     if (unit == (base + seq.units) * pairs) {
@@ -775,42 +806,51 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       ++b;
     }
   }
-  if (tid == 0) a.split[me] = make_int2(begun, begun_last);
+  if (tid == 0 && !a.by_pair) a.split[me] = make_int2(begun, begun_last);
 }
 
-// Joins the partial results of the pair that block blockIdx.x of the first
-// kernel began and the blocks after it went on with: one query row per block
-// here, the columns over the threads and the contributions over groups of them.
+// Joins the partial results of one query row of a pair that several blocks
+// worked on: a warp takes every fourth contribution, its lanes the columns.
+// It is a chain of three reads (who, m and l, O); a warp's first O is read
+// along with the second.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const PagedArgs a,
                                                                           int tile_rows) {
-  constexpr int kGroups = kMergeThreads / D;
+  constexpr int kMergeWarps = kMergeThreads / 32;
+  constexpr int kCols = D / 32;
   __shared__ float weight[kMaxBlocks];
-  __shared__ float part[kGroups][D];
-  __shared__ float red[kMergeThreads / 32], red_l[kMergeThreads / 32];
-  const int tid = static_cast<int>(threadIdx.x);
+  __shared__ float part[kMergeWarps][D];
+  __shared__ float red[kMergeWarps], red_l[kMergeWarps];
+  const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   griddep_wait();  // the partials are complete
   griddep_launch_dependents();
   const int2 split = a.split[blockIdx.x];
   if (split.x < 0) return;
   const int pairs = a.h_kv * a.row_tiles;
-  const int b = split.x / pairs, pair = split.x % pairs;
+  const int whole_pair = a.by_pair ? static_cast<int>(blockIdx.x) : split.x;
+  const int first = a.by_pair ? split.x : static_cast<int>(blockIdx.x), n = split.y - first + 1;
+  const int b = whole_pair / pairs, pair = whole_pair % pairs;
   const int head = pair / a.row_tiles, row0 = pair % a.row_tiles * tile_rows;
   const int r = static_cast<int>(blockIdx.y);
   if (row0 + r >= a.rows) return;
-  const int first = static_cast<int>(blockIdx.x), n = split.y - first + 1;
   // contribution i: the first block's second slot, then the others' first
   auto slot = [&](int i) {
     return (static_cast<int64_t>(2 * (first + i)) + (i == 0 ? 1 : 0)) * tile_rows + r;
   };
+  float o0[kCols], y[kCols];
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) {
+    o0[c] = warp < n ? a.part_o[slot(warp) * D + c * 32 + lane] : 0.f;
+    y[c] = 0.f;
+  }
   float top = kLowest;
   for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, a.part_ml[slot(i)].x);
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-  if ((tid & 31) == 0) red[tid >> 5] = top;
+  if (lane == 0) red[warp] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) top = fmaxf(top, red[w]);
+  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, red[w]);
   float sum = 0.f;
   for (int i = tid; i < n; i += kMergeThreads) {
     const float2 ml = a.part_ml[slot(i)];
@@ -820,31 +860,38 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   }
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
-  if ((tid & 31) == 0) red_l[tid >> 5] = sum;
+  if (lane == 0) red_l[warp] = sum;
   __syncthreads();
   sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < kMergeThreads / 32; ++w) sum += red_l[w];
-  const int d = tid % D, grp = tid / D;
-  float y = 0.f;
-#pragma unroll 8
-  for (int i = grp; i < n; i += kGroups) {
-    const float o = a.part_o[slot(i) * D + d];
-    y += weight[i] * o;
-  }
-  part[grp][d] = y;
-  __syncthreads();
-  if (grp == 0) {
+  for (int w = 0; w < kMergeWarps; ++w) sum += red_l[w];
+  if (warp < n) {
 #pragma unroll
-    for (int i = 1; i < kGroups; ++i) y += part[i][d];
+    for (int c = 0; c < kCols; ++c) y[c] = weight[warp] * o0[c];
+  }
+#pragma unroll 4
+  for (int i = warp + kMergeWarps; i < n; i += kMergeWarps) {
+    const float w = weight[i];
+    const float* o = a.part_o + slot(i) * D + lane;
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) y[c] = fmaf(w, o[c * 32], y[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < kCols; ++c) part[warp][c * 32 + lane] = y[c];
+  __syncthreads();
+  if (tid < D) {
+    float z = part[0][tid];
+#pragma unroll
+    for (int w = 1; w < kMergeWarps; ++w) z += part[w][tid];
     const Sequence seq = sequence(a, b);
     const bool real = (row0 + r) % a.n_q < seq.fresh;
     const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
     const int64_t row = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0 + r;
-    reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + d] =
-        __float2bfloat16_rn(inv == 0.f ? 0.f : y * inv);
+    reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + tid] =
+        __float2bfloat16_rn(inv == 0.f ? 0.f : z * inv);
   }
 }
+static_assert(kMergeThreads >= 128, "a thread per column");
 
 // ------------------------------------------------------------------ launch
 
@@ -893,7 +940,7 @@ cudaError_t resident_blocks(Kernel kernel, int smem, int* cache, int* out) {
 }
 
 template <int D, int NT, bool Q4>
-cudaError_t launch_instance(const PagedArgs& a, const Layout& w, cudaStream_t stream) {
+cudaError_t launch_instance(PagedArgs a, const Layout& w, cudaStream_t stream) {
   auto kernel = decode_paged_kernel<D, NT, Q4>;
   constexpr int smem = Shape<D, NT, Q4>::kSmem;
   static unsigned long long configured = 0;
@@ -903,11 +950,16 @@ cudaError_t launch_instance(const PagedArgs& a, const Layout& w, cudaStream_t st
   if (e == cudaSuccess) e = resident_blocks(kernel, smem, resident, &fit);
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(fit < w.blocks ? fit : w.blocks);
+  // few pairs: look at each for what has to be joined; many: at the blocks,
+  // each of which begins at most one that others finish
+  const int64_t pairs = int64_t(a.B) * a.h_kv * a.row_tiles;
+  a.by_pair = pairs <= static_cast<int64_t>(blocks);
   e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess) return e;
   const unsigned rows = static_cast<unsigned>(a.rows < w.tile_rows ? a.rows : w.tile_rows);
-  return launch_pdl(decode_paged_merge_kernel<D>, dim3(blocks, rows), dim3(kMergeThreads), 0,
-                    stream, a, w.tile_rows);
+  return launch_pdl(decode_paged_merge_kernel<D>,
+                    dim3(a.by_pair ? static_cast<unsigned>(pairs) : blocks, rows),
+                    dim3(kMergeThreads), 0, stream, a, w.tile_rows);
 }
 
 template <int D, bool Q4>
