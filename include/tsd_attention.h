@@ -480,7 +480,8 @@ attn_status attn_decode_host_async(const void *q_host, const void *k_cache,
  *   page_table  device int32[B, max_pages]; entries past a sequence's last
  *               row are never read
  *   page_size   a power of two, 16..256 (other powers -> ATTN_ERR_UNSUPPORTED);
- *               max_pages * page_size <= 2^30, else ATTN_ERR_UNSUPPORTED
+ *               max_pages * page_size <= 2^30 and n_pages * h_kv * page_size < 2^36 - 16,
+ *               else ATTN_ERR_UNSUPPORTED
  *   cache_lens  device int32[B]: rows of each sequence, the new tokens included
  *   new_lens    device int32[B]: how many of the call's n_new (n_q) tokens
  *               sequence b really has, clamped to [0, n_new]; NULL: all.

@@ -600,6 +600,7 @@ attn_status paged_check(int B, int h, int h_kv, int n, int d, int n_pages, int p
   if (d != 64 && d != 128) return ATTN_ERR_UNSUPPORTED;
   if (page_size < 16 || page_size > 256) return ATTN_ERR_UNSUPPORTED;
   if (int64_t(max_pages) * page_size > tsd::kPagedMaxRows) return ATTN_ERR_UNSUPPORTED;
+  if (int64_t(n_pages) * h_kv > tsd::kPagedMaxTiles / (page_size / 16)) return ATTN_ERR_UNSUPPORTED;
   if (table == nullptr) return ATTN_ERR_INVALID;
   for (const void* p : {static_cast<const void*>(table), static_cast<const void*>(lens),
                         static_cast<const void*>(new_lens)})

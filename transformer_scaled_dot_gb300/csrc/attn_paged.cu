@@ -51,7 +51,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;                // cached rows of a warp's step
+constexpr int kTile = 16;                // cached rows of a product, within one page
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
 constexpr int kMergeThreads = 128;
@@ -88,8 +88,10 @@ struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
   static constexpr int kScaleBytes = Q4 ? D / 16 : 0;
-  static constexpr int kStageBytes = 2 * kTile * (kRowBytes + kScaleBytes);
-  static constexpr int kStages = Q4 ? 4 : (D == 64 ? 4 : 3);
+  static constexpr int kHalves = Q4 ? 2 : 1;  // tiles of a warp's step
+  static constexpr int kTileBytes = 2 * kTile * (kRowBytes + kScaleBytes);
+  static constexpr int kStageBytes = kHalves * kTileBytes;
+  static constexpr int kStages = 3;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kPitch = D + 4;  // floats of a row of O in shared memory
   static constexpr bool kQInSmem = NT * D > 128;
@@ -161,6 +163,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
+// c = a b, or c += a b
+template <bool F16>
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 template <bool F16>
 __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -225,46 +242,68 @@ __device__ __forceinline__ uint32_t v_code_offset(int row, int byte) {
   return static_cast<uint32_t>(row * 32 + byte);
 }
 
-// Copies the `valid` first of the 16 rows that start at row `at` of the pools
-// into a stage; the rest become zeros. bf16: rows of 2 D bytes, keys then
-// values, 16-byte piece c of row r at c ^ (r & 7), which ldmatrix reads from
-// all banks; 4-bit: both sides' codes, rows moved as above, then their scales.
-template <int D, bool Q4, bool FULL>
-__device__ __forceinline__ void load_tile(uint32_t stage, const PagedArgs& a, int64_t at,
-                                          int valid, int lane) {
-  constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
-  constexpr int kPieces = kRowBytes / 16;              // of a row
-  constexpr int kRounds = kTile * kPieces / 32;        // a lane's pieces of each side
-  const uint8_t* k = a.k + at * kRowBytes + lane * 16;
-  const uint8_t* v = a.v + at * kRowBytes + lane * 16;
-  const int row0 = lane / kPieces, piece = lane % kPieces;
+// A lane's part in copying tiles into stages. bf16: rows of 2 D bytes, keys
+// then values, 16-byte piece c of row r at c ^ (r & 7), which ldmatrix reads
+// from all banks; 4-bit: both sides' codes, rows moved as above, then their
+// scales. Everything that does not depend on the tile is worked out once.
+template <int D, bool Q4>
+struct TileCopy {
+  static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
+  static constexpr int kPieces = kRowBytes / 16;        // of a row
+  static constexpr int kRounds = kTile * kPieces / 32;  // a lane's pieces of each side
+  static constexpr int kStep = 32 / kPieces;            // rows from one round to the next
+  // bf16: rounds whose rows have the same r & 7 share an offset
+  static constexpr int kOffsets = Q4 ? 1 : (8 / kStep < kRounds ? 8 / kStep : kRounds);
+  const uint8_t* k;  // this lane's first piece of row 0 of the pool
+  const uint8_t* v;
+  const uint8_t* scales;
+  uint32_t k_off[kOffsets], v_off[kOffsets], scale_off;
+  int row0;          // the row of its first piece
+  int scale_row;     // the first row whose scales its 16 bytes of scales hold
+  bool has_scales;
+
+  __device__ __forceinline__ TileCopy(const PagedArgs& a, int lane) {
+    k = a.k + lane * 16;
+    v = a.v + lane * 16;
+    row0 = lane / kPieces;
+    const int piece = lane % kPieces;
 #pragma unroll
-  for (int i = 0; i < kRounds; ++i) {
-    const int row = row0 + i * (32 / kPieces);
-    uint32_t k_off, v_off;
-    if constexpr (Q4) {
-      k_off = k_code_offset<D>(row, piece * 16);
-      v_off = v_code_offset<D>(row, piece * 16);
-    } else {
-      // row & 7 is row0 | the rounds' part, so the second is a constant
-      const uint32_t first = row0 * kRowBytes + ((piece ^ row0) << 4);
-      k_off = i * 512 + (first ^ (((i * (32 / kPieces)) & 7) << 4));
-      v_off = k_off;
+    for (int i = 0; i < kOffsets; ++i) {
+      if constexpr (Q4) {
+        k_off[i] = k_code_offset<D>(row0, piece * 16);
+        v_off[i] = kTile * kRowBytes + v_code_offset<D>(row0, piece * 16);
+      } else {
+        k_off[i] = row0 * kRowBytes + ((piece ^ ((row0 + i * kStep) & 7)) << 4);
+        v_off[i] = k_off[i] + kTile * kRowBytes;
+      }
     }
-    cp_async_16<FULL>(stage + k_off, k + i * 512, row < valid);
-    cp_async_16<FULL>(stage + kTile * kRowBytes + v_off, v + i * 512, row < valid);
-  }
-  if constexpr (Q4) {
-    // the scales of 16 rows: D bytes for keys, D for values; 16 bytes hold
-    // several rows' scales, those past `valid` meet codes of zero
-    constexpr int kRowsIn16 = 256 / D;
+    // the scales of 16 rows: D bytes for keys, D for values
     const int part = lane % (D / 16);
-    if (lane < D / 8) {
-      const uint8_t* s = (lane < D / 16 ? a.k_scales : a.v_scales) + at * (D / 16);
-      cp_async_16<FULL>(stage + kTile * D + lane * 16, s + part * 16, part * kRowsIn16 < valid);
+    has_scales = Q4 && lane < D / 8;
+    scales = (lane < D / 16 ? a.k_scales : a.v_scales) + part * 16;
+    scale_off = kTile * D + lane * 16;
+    scale_row = part * (256 / D);
+  }
+
+  // The `valid` first rows of the pools' tile `block` (rows 16 block on); the
+  // rest become zeros. A row's scales past `valid` meet codes of zero.
+  template <bool FULL>
+  __device__ __forceinline__ void load(uint32_t stage, uint32_t block, int valid) const {
+    const uint8_t* ks = k + static_cast<uint64_t>(block) * (kTile * kRowBytes);
+    const uint8_t* vs = v + static_cast<uint64_t>(block) * (kTile * kRowBytes);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const bool there = row0 + i * kStep < valid;
+      cp_async_16<FULL>(stage + k_off[i % kOffsets] + i * 512, ks + i * 512, there);
+      cp_async_16<FULL>(stage + v_off[i % kOffsets] + i * 512, vs + i * 512, there);
+    }
+    if constexpr (Q4) {
+      if (has_scales)
+        cp_async_16<FULL>(stage + scale_off, scales + static_cast<uint64_t>(block) * D,
+                          scale_row < valid);
     }
   }
-}
+};
 
 // ------------------------------------------------------------------ the work's order
 
@@ -347,6 +386,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
   }
 
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
+  const TileCopy<D, Q4> copy(a, lane);
   int begun = -1, begun_last = 0;  // the pair that this block begins and does not finish
 
   while (unit < end) {
@@ -442,40 +482,53 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // ---- this warp's tiles: key0 + (warp + 4 i) * 16, i < tiles
-    const int span = key1 - key0 - warp * kTile;
-    const int tiles = span > 0 ? (span + kUnit - 1) / kUnit : 0;
+    // ---- this warp's steps of kHalves tiles each, a stride apart
+    constexpr int kHalves = S::kHalves, kStride = kHalves * kUnit;
+    const int first_key = key0 + warp * (kHalves * kTile);
+    const int steps = key1 > first_key ? (key1 - first_key + kStride - 1) / kStride : 0;
     const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    const int first_key = key0 + warp * kTile;
-    // the page of tile i: 32 at a time, one per lane, the next 32 on their way
-    auto page_of = [&](int i) {
-      return i < tiles ? __ldcg(table + ((first_key + i * kUnit) >> a.page_shift)) : 0;
+    // tile j's place in the pools, in tiles (kNoBlock: its page is no page);
+    // 32 at a time, one per lane, the next 32 on their way
+    constexpr uint32_t kNoBlock = 0xffffffffu;
+    auto block_of = [&](int j) {
+      const int key = first_key + j / kHalves * kStride + j % kHalves * kTile;
+      if (key >= key1) return 0u;
+      const int page = __ldcg(table + (key >> a.page_shift));
+      if (page < 0 || page >= a.n_pages) {
+        atomicOr(&g_device_error, kErrIndex);
+        return kNoBlock;
+      }
+      return (static_cast<uint32_t>(page * a.h_kv + head) << (a.page_shift - 4)) +
+             ((key & ((1 << a.page_shift) - 1)) >> 4);
     };
-    int pages = page_of(lane), pages_next = page_of(32 + lane);
-    uint32_t skipped = 0;  // bit s: the tile in stage s has no page
-    int fill = 0;          // the stage that is filled next
-    auto issue = [&](int i) {  // tile i into the next stage
-      if (i < tiles) {
-        if ((i & 31) == 0 && i > 0) {
-          pages = pages_next;
-          pages_next = page_of(i + 32 + lane);
+    uint32_t block = block_of(lane), block_next = block_of(32 + lane);
+    uint32_t skipped = 0;        // bit kHalves s + h: tile h of stage s has no page
+    int fill = 0;                // the stage that is filled next
+    uint32_t fill_at = ring;
+    auto issue = [&](int i) {  // step i's tiles into the next stage
+      if (i < steps) {
+        const int j = i * kHalves;
+        if ((j & 31) == 0 && j > 0) {
+          block = block_next;
+          block_next = block_of(j + 32 + lane);
         }
-        const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-        const int key = first_key + i * kUnit;
-        if (page < 0 || page >= a.n_pages) {
-          skipped |= 1u << fill;
-          if (lane == 0) atomicOr(&g_device_error, kErrIndex);
-        } else {
-          skipped &= ~(1u << fill);
-          const int64_t at = ((static_cast<int64_t>(page) * a.h_kv + head) << a.page_shift) +
-                             (key & ((1 << a.page_shift) - 1));
-          const uint32_t stage = ring + fill * S::kStageBytes;
-          if (key1 - key >= kTile) load_tile<D, Q4, true>(stage, a, at, kTile, lane);
-          else load_tile<D, Q4, false>(stage, a, at, key1 - key, lane);
+        skipped &= ~(((1u << kHalves) - 1) << (fill * kHalves));
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          uint32_t from = __shfl_sync(0xffffffffu, block, (j + h) & 31);
+          int valid = key1 - (first_key + i * kStride + h * kTile);
+          if (from == kNoBlock) {
+            skipped |= 1u << (fill * kHalves + h);
+            from = 0;
+            valid = 0;
+          }
+          if (valid >= kTile) copy.template load<true>(fill_at + h * S::kTileBytes, from, valid);
+          else copy.template load<false>(fill_at + h * S::kTileBytes, from, valid);
         }
       }
       cp_async_commit();
-      fill = fill == S::kStages - 1 ? 0 : fill + 1;
+      fill_at += S::kStageBytes;
+      if (++fill == S::kStages) fill = 0, fill_at = ring;
     };
 #pragma unroll
     for (int i = 0; i < S::kStages - 1; ++i) issue(i);
@@ -491,96 +544,134 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       else return make_uint2(qf[nt][s][0], qf[nt][s][1]);
     };
     int stage = 0;
-    for (int i = 0; i < tiles; ++i) {
+    uint32_t at = ring;
+    const int row_lo = Q4 ? cached_row(g) : g;  // of S^T's registers 0, 1; 8 further: 2, 3
+    for (int i = 0; i < steps; ++i) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
       issue(i + S::kStages - 1);
-      const uint32_t at = ring + stage * S::kStageBytes;
-      const bool skip = skipped & (1u << stage);
-      stage = stage == S::kStages - 1 ? 0 : stage + 1;
-      if (skip) continue;
-      const int key = first_key + i * kUnit;
+      const int key = first_key + i * kStride;
 
       // ---- S^T = K Q^T; for one column block even and odd steps apart, as
       // one chain of dependent products would be waited for
-      float x[NT][4], x2[NT][4];
+      float x[kHalves][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int h = 0; h < kHalves; ++h) {
+        const uint32_t tile = at + h * S::kTileBytes;
+        float x2[NT][4];
+        if constexpr (!Q4) {
+          const uint32_t kat = tile + (lane & 15) * (2 * D);
+          const uint32_t swz = (lane >> 4) ^ (lane & 7);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) x[nt][c] = x2[nt][c] = 0.f;
-      if constexpr (!Q4) {
-        const uint32_t kat = at + (lane & 15) * (2 * D);
-        const uint32_t swz = (lane >> 4) ^ (lane & 7);
+          for (int s = 0; s < kSteps; ++s) {
+            uint32_t w[4];
+            ldmatrix4<false>(w, kat + ((swz ^ (2 * s)) << 4));
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          uint32_t w[4];
-          ldmatrix4<false>(w, kat + ((swz ^ (2 * s)) << 4));
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q = query(nt, s);
+              float (&to)[4] = NT == 1 && (s & 1) ? x2[nt] : x[h][nt];
+              if (s == 0 || (NT == 1 && s == 1)) mma_first<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
+              else mma<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
+            }
+          }
+        } else {
+          constexpr int kWords = D / 32;  // of this thread's codes of one row
+          uint32_t w[2][kWords], sc[2];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-          {
-            const uint2 q = query(nt, s);
-            mma<false>(NT == 1 && (s & 1) ? x2[nt] : x[nt], w[0], w[1], w[2], w[3], q.x, q.y);
+          for (int half = 0; half < 2; ++half) {
+            const int row = row_lo + 8 * half;
+            if constexpr (D == 128) {
+              const uint4 v = lds128(tile + k_code_offset<D>(row, t * 16));
+              w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
+              sc[half] = scales_f16x2(lds16(tile + kTile * D + row * 8 + t * 2));
+            } else {
+              const uint2 v = lds64(tile + k_code_offset<D>(row, t * 8));
+              w[half][0] = v.x, w[half][1] = v.y;
+              sc[half] = scales_f16x2(lds8(tile + kTile * D + row * 4 + t) * 0x0101u);
+            }
+          }
+#pragma unroll
+          for (int i4 = 0; i4 < kWords; ++i4) {
+            uint32_t lo[4], hi[4];
+            codes_f16x2(w[0][i4], lo);
+            codes_f16x2(w[1][i4], hi);
+            // d = 128: words 0, 1 are of the thread's first group, 2, 3 of its second
+            const uint32_t s0 = D == 128 ? __byte_perm(sc[0], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[0];
+            const uint32_t s1 = D == 128 ? __byte_perm(sc[1], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[1];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              lo[c] = mul_f16x2(lo[c], s0);
+              hi[c] = mul_f16x2(hi[c], s1);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint2 q0 = query(nt, 2 * i4), q1 = query(nt, 2 * i4 + 1);
+              if (i4 == 0) mma_first<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
+              else mma<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
+              if (i4 == 0 && NT == 1) mma_first<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
+              else mma<true>(NT == 1 ? x2[nt] : x[h][nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
+            }
           }
         }
-      } else {
-        constexpr int kWords = D / 32;  // of this thread's codes of one row
-        uint32_t w[2][kWords], sc[2];
+        if constexpr (NT == 1) {
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const int row = cached_row(g + 8 * half);
-          if constexpr (D == 128) {
-            const uint4 v = lds128(at + k_code_offset<D>(row, t * 16));
-            w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
-            sc[half] = scales_f16x2(lds16(at + kTile * D + row * 8 + t * 2));
-          } else {
-            const uint2 v = lds64(at + k_code_offset<D>(row, t * 8));
-            w[half][0] = v.x, w[half][1] = v.y;
-            sc[half] = scales_f16x2(lds8(at + kTile * D + row * 4 + t) * 0x0101u);
-          }
-        }
-#pragma unroll
-        for (int i4 = 0; i4 < kWords; ++i4) {
-          uint32_t lo[4], hi[4];
-          codes_f16x2(w[0][i4], lo);
-          codes_f16x2(w[1][i4], hi);
-          // d = 128: words 0, 1 are of the thread's first group, 2, 3 of its second
-          const uint32_t s0 = D == 128 ? __byte_perm(sc[0], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[0];
-          const uint32_t s1 = D == 128 ? __byte_perm(sc[1], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[1];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            lo[c] = mul_f16x2(lo[c], s0);
-            hi[c] = mul_f16x2(hi[c], s1);
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 q0 = query(nt, 2 * i4), q1 = query(nt, 2 * i4 + 1);
-            mma<true>(x[nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
-            mma<true>(NT == 1 ? x2[nt] : x[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
-          }
+          for (int c = 0; c < 4; ++c) x[h][0][c] += x2[0][c];
         }
       }
 
-      // ---- masks; x - m, and whether any passes what P may be
-      const int row_lo = Q4 ? cached_row(g) : g, row_hi = row_lo + 8;
-      const bool masked = key + kTile > hidden;
-      bool over = false;
-      float y[NT][4];
+      // ---- masks, in the sequence's last rows or where a page is missing;
+      // there also: is any value of V not finite?
+      bool odd = false;
+      const uint32_t missing = (skipped >> (stage * kHalves)) & ((1u << kHalves) - 1);
+      if (key + kHalves * kTile > hidden || missing != 0) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int h = 0; h < kHalves; ++h) {
+          const int row = key + h * kTile + row_lo;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (NT == 1) x[nt][c] += x2[nt][c];
-          if (masked && key + (c < 2 ? row_lo : row_hi) >= s_limit[nt * 8 + 2 * t + (c & 1)])
-            x[nt][c] = -INFINITY;
-          y[nt][c] = fmaf(x[nt][c], mult[nt][c & 1], -m[nt][c & 1]);
-          over |= y[nt][c] > S::kShift + S::kSlack;
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (row + (c < 2 ? 0 : 8) >= s_limit[nt * 8 + 2 * t + (c & 1)] || (missing >> h & 1))
+                x[h][nt][c] = -INFINITY;
+          const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
+          if constexpr (Q4) {  // a NaN among the scales: 16 rows of D / 16
+            if (lane < D / 4) {
+              const uint32_t w = lds32(vat + kTile * S::kRowBytes + D + lane * 4) & 0x7f7f7f7fu;
+              odd |= ((w + 0x01010101u) & 0x80808080u) != 0;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < kTile * S::kRowBytes / 512; ++j) {
+              const uint4 w = lds128(vat + j * 512 + lane * 16);
+#pragma unroll
+              for (uint32_t e : {w.x, w.y, w.z, w.w})
+                odd |= (e & 0x7f80u) == 0x7f80u || (e & 0x7f800000u) == 0x7f800000u;
+            }
+          }
         }
+        odd = __any_sync(0xffffffffu, odd);
+      }
+
+      // ---- x - m, and whether any passes what P may be
+      bool over = false;
+      float y[kHalves][NT][4];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            y[h][nt][c] = fmaf(x[h][nt][c], mult[nt][c & 1], -m[nt][c & 1]);
+            over |= y[h][nt][c] > S::kShift + S::kSlack;
+          }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(x[nt][c], x[nt][2 + c]) * mult[nt][c];
+            float top = fmaxf(x[0][nt][c], x[0][nt][2 + c]);
+            if constexpr (kHalves == 2) top = fmaxf(top, fmaxf(x[kHalves - 1][nt][c], x[kHalves - 1][nt][2 + c]));
+            top *= mult[nt][c];
 #pragma unroll
             for (int s = 4; s < 32; s <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             const float next = fmaxf(m[nt][c], top - S::kShift);
@@ -592,106 +683,117 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
               o[nt][s][c] *= f;
               o[nt][s][2 + c] *= f;
             }
-            y[nt][c] = fmaf(x[nt][c], mult[nt][c], -next);
-            y[nt][2 + c] = fmaf(x[nt][2 + c], mult[nt][c], -next);
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) {
+              y[h][nt][c] = fmaf(x[h][nt][c], mult[nt][c], -next);
+              y[h][nt][2 + c] = fmaf(x[h][nt][2 + c], mult[nt][c], -next);
+            }
           }
       }
 
       // ---- p, its sum, and P^T as the second product's operand
-      uint32_t p_hi[NT][2], p_lo[NT][2];
+      uint32_t p_hi[kHalves][NT][2], p_lo[kHalves][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+      for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) p[c] = ex2(y[nt][c]);
-        l[nt][0] += p[0] + p[2];
-        l[nt][1] += p[1] + p[3];
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const float p0 = p[2 * half], p1 = p[2 * half + 1];
-          if constexpr (Q4) {
-            p_hi[nt][half] = transpose8x8(pack_f16x2(p0, p1));
-          } else {
-            const uint32_t hi = pack_bf16x2(p0, p1);
-            p_hi[nt][half] = transpose8x8(hi);
-            p_lo[nt][half] = transpose8x8(
-                pack_bf16x2(p0 - bf16_f32(hi & 0xffffu), p1 - bf16_f32(hi >> 16)));
-          }
-        }
-      }
-
-      // ---- O^T += V^T P^T. Registers 0 and 1 of V's operand are two columns
-      // of cached rows r0 and r1, registers 2 and 3 of the rows 8 further
-      const uint32_t vat = at + kTile * S::kRowBytes;
-      uint32_t v_codes[2][2][D / 64], v_scale[2];  // 4-bit: [rows' half][r0, r1][word]
-      bool odd = false;  // a value that is not finite
-      if constexpr (Q4) {
-        const uint32_t sat = at + kTile * D + D;
+          for (int c = 0; c < 4; ++c) p[c] = ex2(y[h][nt][c]);
+          l[nt][0] += p[0] + p[2];
+          l[nt][1] += p[1] + p[3];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int a0 = t + 8 * r, a1 = a0 + 4;
-          if constexpr (D == 128) {
-            const uint2 w0 = lds64(vat + v_code_offset<D>(a0, g * 8));
-            const uint2 w1 = lds64(vat + v_code_offset<D>(a1, g * 8));
-            v_codes[r][0][0] = w0.x, v_codes[r][0][1] = w0.y;
-            v_codes[r][1][0] = w1.x, v_codes[r][1][1] = w1.y;
-          } else {
-            v_codes[r][0][0] = lds32(vat + v_code_offset<D>(a0, g * 4));
-            v_codes[r][1][0] = lds32(vat + v_code_offset<D>(a1, g * 4));
-          }
-          const int group = D == 128 ? g : g >> 1;
-          const uint32_t two = lds8(sat + a0 * (D / 16) + group) |
-                               (lds8(sat + a1 * (D / 16) + group) << 8);
-          if (masked) odd |= (two & 0x7fu) == 0x7fu || (two & 0x7f00u) == 0x7f00u;
-          v_scale[r] = scales_f16x2(two);
-        }
-      }
-      // the operand of kBlock blocks of 16 columns from block s0 on
-      constexpr int kBlock = Q4 ? 4 : 1;
-      auto v_operand = [&](int s0, uint32_t (&va)[kBlock][4]) {
-        if constexpr (!Q4) {
-          const uint32_t row = (lane & 7) + ((lane >> 4) << 3);
-          ldmatrix4<true>(va[0], vat + row * (2 * D) +
-                                     (((2 * s0) ^ ((lane >> 3) & 1) ^ (lane & 7)) << 4));
-        } else {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const uint32_t u = v_codes[r][0][s0 / 4], v = v_codes[r][1][s0 / 4];
-            uint32_t even[4], uneven[4];
-            codes_f16x2((u & 0x0f0f0f0fu) | ((v & 0x0f0f0f0fu) << 4), even);
-            codes_f16x2(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), uneven);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              va[e][2 * r] = mul_f16x2(even[e], v_scale[r]);
-              va[e][2 * r + 1] = mul_f16x2(uneven[e], v_scale[r]);
+          for (int half = 0; half < 2; ++half) {
+            const float p0 = p[2 * half], p1 = p[2 * half + 1];
+            if constexpr (Q4) {
+              p_hi[h][nt][half] = transpose8x8(pack_f16x2(p0, p1));
+            } else {
+              const uint32_t hi = pack_bf16x2(p0, p1);
+              p_hi[h][nt][half] = transpose8x8(hi);
+              p_lo[h][nt][half] = transpose8x8(
+                  pack_bf16x2(p0 - bf16_f32(hi & 0xffffu), p1 - bf16_f32(hi >> 16)));
             }
           }
         }
-      };
-      if constexpr (!Q4) {
-        if (masked) {
+
+      // ---- O^T += V^T P^T. Registers 0 and 1 of V's operand are two columns
+      // of cached rows r0 and r1, registers 2 and 3 of the rows 8 further
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            uint32_t va[1][4];
-            v_operand(s, va);
+      for (int h = 0; h < kHalves; ++h) {
+        const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
+        uint32_t v_codes[2][2][D / 64], v_scale[2];  // 4-bit: [rows' half][r0, r1][word]
+        if constexpr (Q4) {
+          const uint32_t sat = vat + kTile * S::kRowBytes + D;
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              odd |= (va[0][e] & 0x7f80u) == 0x7f80u || (va[0][e] & 0x7f800000u) == 0x7f800000u;
+          for (int r = 0; r < 2; ++r) {
+            const int a0 = t + 8 * r, a1 = a0 + 4;
+            if constexpr (D == 128) {
+              const uint2 w0 = lds64(vat + v_code_offset<D>(a0, g * 8));
+              const uint2 w1 = lds64(vat + v_code_offset<D>(a1, g * 8));
+              v_codes[r][0][0] = w0.x, v_codes[r][0][1] = w0.y;
+              v_codes[r][1][0] = w1.x, v_codes[r][1][1] = w1.y;
+            } else {
+              v_codes[r][0][0] = lds32(vat + v_code_offset<D>(a0, g * 4));
+              v_codes[r][1][0] = lds32(vat + v_code_offset<D>(a1, g * 4));
+            }
+            const int group = D == 128 ? g : g >> 1;
+            v_scale[r] = scales_f16x2(lds8(sat + a0 * (D / 16) + group) |
+                                      (lds8(sat + a1 * (D / 16) + group) << 8));
           }
         }
-      }
-      if (masked && __any_sync(0xffffffffu, odd)) {
-        // 0 times an infinity is no number: the products once for each new
-        // token, with the rows that it does not see cleared, and only the
-        // token's own columns of O taken from them
-        const int r0 = Q4 ? t : 2 * t, r1 = Q4 ? t + 4 : 2 * t + 1;
-        for (int token = 0; token < seq.fresh; ++token) {
-          const int seen = a.causal ? seq.len - seq.fresh + token + 1 : seq.len;
-          uint32_t keep[2];
+        // the operand of kBlock blocks of 16 columns from block s0 on
+        constexpr int kBlock = Q4 ? 4 : 1;
+        auto v_operand = [&](int s0, uint32_t (&va)[kBlock][4]) {
+          if constexpr (!Q4) {
+            const uint32_t row = (lane & 7) + ((lane >> 4) << 3);
+            ldmatrix4<true>(va[0], vat + row * (2 * D) +
+                                       (((2 * s0) ^ ((lane >> 3) & 1) ^ (lane & 7)) << 4));
+          } else {
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-            keep[r] = (key + r0 + 8 * r < seen ? 0xffffu : 0u) |
-                      (key + r1 + 8 * r < seen ? 0xffff0000u : 0u);
+            for (int r = 0; r < 2; ++r) {
+              const uint32_t u = v_codes[r][0][s0 / 4], v = v_codes[r][1][s0 / 4];
+              uint32_t even[4], uneven[4];
+              codes_f16x2((u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u), even);
+              codes_f16x2(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), uneven);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                va[e][2 * r] = mul_f16x2(even[e], v_scale[r]);
+                va[e][2 * r + 1] = mul_f16x2(uneven[e], v_scale[r]);
+              }
+            }
+          }
+        };
+        if (odd) {
+          // 0 times an infinity is no number: the products once for each new
+          // token, with the rows that it does not see cleared, and only the
+          // token's own columns of O taken from them
+          const int r0 = key + h * kTile + (Q4 ? t : 2 * t), r1 = r0 + (Q4 ? 4 : 1);
+          for (int token = 0; token < seq.fresh; ++token) {
+            const int seen = a.causal ? seq.len - seq.fresh + token + 1 : seq.len;
+            uint32_t keep[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              keep[r] = (r0 + 8 * r < seen ? 0xffffu : 0u) | (r1 + 8 * r < seen ? 0xffff0000u : 0u);
+#pragma unroll
+            for (int s = 0; s < kSteps; s += kBlock) {
+              uint32_t va[kBlock][4];
+              v_operand(s, va);
+#pragma unroll
+              for (int e = 0; e < kBlock; ++e)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                  const uint32_t a0 = va[e][0] & keep[0], a1 = va[e][1] & keep[0];
+                  const uint32_t a2 = va[e][2] & keep[1], a3 = va[e][3] & keep[1];
+                  float (&acc)[4] = o[nt][s + e];
+                  float z[4] = {acc[0], acc[1], acc[2], acc[3]};
+                  mma<Q4>(z, a0, a1, a2, a3, p_hi[h][nt][0], p_hi[h][nt][1]);
+                  if constexpr (!Q4) mma<Q4>(z, a0, a1, a2, a3, p_lo[h][nt][0], p_lo[h][nt][1]);
+                  if ((row0 + nt * 8 + 2 * t) % a.n_q == token) acc[0] = z[0], acc[2] = z[2];
+                  if ((row0 + nt * 8 + 2 * t + 1) % a.n_q == token) acc[1] = z[1], acc[3] = z[3];
+                }
+            }
+          }
+        } else {
 #pragma unroll
           for (int s = 0; s < kSteps; s += kBlock) {
             uint32_t va[kBlock][4];
@@ -700,34 +802,17 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
             for (int e = 0; e < kBlock; ++e)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
-                const uint32_t a0 = va[e][0] & keep[0], a1 = va[e][1] & keep[0];
-                const uint32_t a2 = va[e][2] & keep[1], a3 = va[e][3] & keep[1];
-                float (&acc)[4] = o[nt][s + e];
-                float z[4] = {acc[0], acc[1], acc[2], acc[3]};
-                mma<Q4>(z, a0, a1, a2, a3, p_hi[nt][0], p_hi[nt][1]);
-                if constexpr (!Q4) mma<Q4>(z, a0, a1, a2, a3, p_lo[nt][0], p_lo[nt][1]);
-                if ((row0 + nt * 8 + 2 * t) % a.n_q == token) acc[0] = z[0], acc[2] = z[2];
-                if ((row0 + nt * 8 + 2 * t + 1) % a.n_q == token) acc[1] = z[1], acc[3] = z[3];
+                mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_hi[h][nt][0],
+                        p_hi[h][nt][1]);
+                if constexpr (!Q4)
+                  mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_lo[h][nt][0],
+                          p_lo[h][nt][1]);
               }
           }
         }
-      } else {
-#pragma unroll
-        for (int s = 0; s < kSteps; s += kBlock) {
-          uint32_t va[kBlock][4];
-          v_operand(s, va);
-#pragma unroll
-          for (int e = 0; e < kBlock; ++e)
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_hi[nt][0],
-                      p_hi[nt][1]);
-              if constexpr (!Q4)
-                mma<Q4>(o[nt][s + e], va[e][0], va[e][1], va[e][2], va[e][3], p_lo[nt][0],
-                        p_lo[nt][1]);
-            }
-        }
       }
+      at += S::kStageBytes;
+      if (++stage == S::kStages) stage = 0, at = ring;
     }
     cp_async_wait<0>();
 

@@ -225,7 +225,8 @@ cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream);
 
 // One decoding step against a paged cache: the n_q (<= 8) newest tokens'
 // queries of h = group * h_kv heads, end-aligned causal or without a mask.
-constexpr int64_t kPagedMaxRows = 1ll << 30;  // rows of one sequence's pages
+constexpr int64_t kPagedMaxRows = 1ll << 30;   // rows of one sequence's pages
+constexpr int64_t kPagedMaxTiles = 0xfffffffell;  // 16-row tiles of a pool
 struct PagedDecodeProblem {
   PagedCache cache;
   const uint16_t* q;  // [B, h, n_q, d]
