@@ -7,11 +7,12 @@
 //
 // The step is bound by reading the cache, and is laid out around that:
 //
-//  * Work. A unit is 64 cached rows of one (sequence, key head, tile of query
-//    rows). The units of the batch, in that order, are cut into as many equal
-//    ranges as blocks fit on the device, from the lengths that the device
-//    holds: sequences of uneven lengths keep all SMs reading to the end, and
-//    pages that a sequence does not have cost nothing. A range's first and
+//  * Work. A unit is 64 cached rows of one pair, a pair being a (sequence, key
+//    head, tile of query rows); a few units more stand for what a pair costs
+//    by itself. The units of the batch, in that order, are cut into as many
+//    equal ranges as blocks fit on the device, from the lengths that the
+//    device holds: sequences of uneven lengths keep all SMs reading to the end,
+//    and pages that a sequence does not have cost nothing. A range's first and
 //    last sequence may be shared with the neighbouring blocks; those leave
 //    partial results (m, l = sum p, O = sum p v, in fp32) in the workspace
 //    and the merge kernel joins them.
@@ -53,6 +54,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                // cached rows of a product, within one page
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
+constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
 constexpr int kMergeThreads = 128;
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
@@ -98,7 +100,11 @@ struct Shape {
   // p = 2^(x - m) is at most 2^(kShift + kSlack); f16 holds up to 2^15.99
   static constexpr float kShift = Q4 ? 11.f : 0.f, kSlack = Q4 ? 4.f : 8.f;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
-  static constexpr int kSmem = kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+  // a warp's part of O fits into one stage of its ring
+  static constexpr bool kAhead = kRows * kPitch * 4 <= kStageBytes;
+  static constexpr int kSmem = kAhead || kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
+  // blocks that share an SM; more of them with fewer registers each were slower
+  static constexpr int kMinBlocks = NT > 1 ? 1 : (Q4 || D == 64 ? 3 : 2);
 };
 
 // ------------------------------------------------------------------ instructions
@@ -310,16 +316,29 @@ struct TileCopy {
 // Sequence b's rows that count, and its units.
 struct Sequence {
   int len, fresh;  // cached rows, new tokens
-  int units;       // at least one: its output has to be written
+  int units;       // of rows
 };
 __device__ __forceinline__ Sequence sequence(const PagedArgs& a, int b) {
   Sequence s;
   const int capacity = a.max_pages << a.page_shift;
   s.len = a.lens ? min(max(__ldcg(a.lens + b), 0), capacity) : capacity;
   s.fresh = a.new_lens ? min(max(__ldcg(a.new_lens + b), 0), a.n_q) : a.n_q;
-  s.units = s.fresh > 0 ? max((s.len + kUnit - 1) / kUnit, 1) : 1;
+  s.units = s.fresh > 0 ? (s.len + kUnit - 1) / kUnit : 0;
   return s;
 }
+// The units of each of its pairs, the first `extra` of which stand for no
+// rows; at least one, as its output has to be written.
+__device__ __forceinline__ int pair_units(const Sequence& s, int extra) {
+  return max(s.units + extra, 1);
+}
+
+// A block's consecutive units of one pair.
+struct Segment {
+  int64_t unit;  // the first one's number
+  int b, pair;
+  int units, chunk, take;  // of the pair: all, those before, those that are the block's
+  int len, fresh;
+};
 
 // Floor of x / y, in 32 bits where they suffice.
 __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
@@ -330,7 +349,8 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 // ------------------------------------------------------------------ the kernel
 
 template <int D, int NT, bool Q4>
-__global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs a) {
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
+    decode_paged_kernel(const PagedArgs a) {
   using S = Shape<D, NT, Q4>;
   constexpr int kSteps = D / 16;  // products of S, and blocks of 16 columns of O
   extern __shared__ __align__(128) uint8_t smem[];
@@ -338,6 +358,9 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
   __shared__ float s_mult[S::kRows];
   __shared__ int s_limit[S::kRows];
   __shared__ uint2 s_q[S::kQInSmem ? kSteps * NT : 1][32];
+  // kept out of the registers that the inner loop needs
+  __shared__ Segment s_seg;
+  __shared__ int64_t s_rest, s_plan[2];  // units after the segment; all units, all blocks
   const int tid = static_cast<int>(threadIdx.x);
   const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   griddep_wait();  // the cache, queries, lengths and tables may come from the previous kernel
@@ -346,28 +369,32 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
   // this block's range of units: each warp by itself sums the sequences' units
   const int pairs = a.h_kv * a.row_tiles;  // (key head, row tile) of a sequence
   int64_t total = 0;
+  int none = 0;  // sequences without rows
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     int u = b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+    none += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.B && u == 0));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) u += __shfl_xor_sync(0xffffffffu, u, s);
     total += u;
   }
   total *= pairs;
+  // a pair's own cost counts as far as the blocks have that much to do: with
+  // a unit or two for each it would only leave blocks without rows
+  const int extra = static_cast<int>(min(quotient(total, gridDim.x), static_cast<int64_t>(kPairUnits)));
+  total += static_cast<int64_t>(pairs) * (extra > 0 ? static_cast<int64_t>(a.B) * extra : none);
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);
   const int64_t me = blockIdx.x;
-  if (me >= blocks) {
-    if (tid == 0 && !a.by_pair) a.split[me] = make_int2(-1, 0);
-    return;
-  }
-  const int64_t each = quotient(total, blocks), left = total - each * blocks;
-  int64_t unit = me * each + quotient(me * left, blocks);
-  const int64_t end = (me + 1) * each + quotient((me + 1) * left, blocks);
-  int b = 0;
-  int64_t base = 0;  // units of one pair of all sequences before b
+  if (tid == 0 && !a.by_pair) a.split[me] = make_int2(-1, 0);
+  if (me >= blocks) return;
+  const int64_t each = quotient(total, blocks), over_all = total - each * blocks;
+  Segment seg;
+  seg.unit = me * each + quotient(me * over_all, blocks);
+  int64_t rest = (me + 1) * each + quotient((me + 1) * over_all, blocks) - seg.unit;
   {
-    const int64_t want = quotient(unit, pairs);
+    const int64_t want = quotient(seg.unit, pairs);
+    int64_t base = 0;  // units of one pair of all sequences before b
     for (int b0 = 0;; b0 += 32) {
-      const int u = b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+      const int u = b0 + lane < a.B ? pair_units(sequence(a, b0 + lane), extra) : 0;
       int upto = u;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
@@ -377,54 +404,131 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       const unsigned past = __ballot_sync(0xffffffffu, base + upto > want);
       if (past != 0u || b0 + 32 >= a.B) {  // the second: for certain to end
         const int first = past != 0u ? __ffs(past) - 1 : 31;
-        b = min(b0 + first, a.B - 1);
+        seg.b = min(b0 + first, a.B - 1);
         base += __shfl_sync(0xffffffffu, upto - u, first);
         break;
       }
       base += __shfl_sync(0xffffffffu, upto, 31);
     }
+    const Sequence seq = sequence(a, seg.b);
+    seg.len = seq.len;
+    seg.fresh = seq.fresh;
+    seg.units = pair_units(seq, extra);
+    const int64_t local = seg.unit - base * pairs;
+    seg.pair = static_cast<int>(quotient(local, seg.units));
+    seg.chunk = static_cast<int>(local - static_cast<int64_t>(seg.pair) * seg.units);
+    seg.take = static_cast<int>(min(rest, static_cast<int64_t>(seg.units - seg.chunk)));
+    rest -= seg.take;
+  }
+  if (tid == 0) {
+    s_plan[0] = total;
+    s_plan[1] = blocks;
   }
 
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   const TileCopy<D, Q4> copy(a, lane);
-  int begun = -1, begun_last = 0;  // the pair that this block begins and does not finish
+  constexpr int kHalves = S::kHalves, kStride = kHalves * kUnit;
+  constexpr uint32_t kNoBlock = 0xffffffffu;
 
-  while (unit < end) {
-    const Sequence seq = sequence(a, b);
-    const int64_t local = unit - base * pairs;
-    const int pair = static_cast<int>(quotient(local, seq.units));
-    const int chunk = static_cast<int>(local - static_cast<int64_t>(pair) * seq.units);
-    const int take = static_cast<int>(min(end - unit, static_cast<int64_t>(seq.units - chunk)));
-    const int head = pair / a.row_tiles, row0 = pair % a.row_tiles * S::kRows;
-    const int rows = min(S::kRows, a.rows - row0);
+  // the part of a segment that this warp's copies go by
+  int first_key, steps, key1, head;
+  const int32_t* table;
+  uint32_t block, block_next;  // of the steps' tiles, 32 at a time, one per lane
+  uint32_t skipped = 0;        // bit kHalves s + h: tile h of stage s has no page
+  int fill = 0, stage = 0;     // the stages that are filled and read next
+  uint32_t fill_at = ring, at = ring;
+  // tile j's place in the pools, in tiles (kNoBlock: its page is no page)
+  auto block_of = [&](int j) {
+    const int key = first_key + j / kHalves * kStride + j % kHalves * kTile;
+    if (key >= key1) return 0u;
+    const int page = __ldcg(table + (key >> a.page_shift));
+    if (page < 0 || page >= a.n_pages) {
+      atomicOr(&g_device_error, kErrIndex);
+      return kNoBlock;
+    }
+    return (static_cast<uint32_t>(page * a.h_kv + head) << (a.page_shift - 4)) +
+           ((key & ((1 << a.page_shift) - 1)) >> 4);
+  };
+  auto issue = [&](int i) {  // step i's tiles into the next stage
+    if (i < steps) {
+      const int j = i * kHalves;
+      if ((j & 31) == 0 && j > 0) {
+        block = block_next;
+        block_next = block_of(j + 32 + lane);
+      }
+      skipped &= ~(((1u << kHalves) - 1) << (fill * kHalves));
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        uint32_t from = __shfl_sync(0xffffffffu, block, (j + h) & 31);
+        int valid = key1 - (first_key + i * kStride + h * kTile);
+        if (from == kNoBlock) {
+          skipped |= 1u << (fill * kHalves + h);
+          from = 0;
+          valid = 0;
+        }
+        if (valid >= kTile) copy.template load<true>(fill_at + h * S::kTileBytes, from, valid);
+        else copy.template load<false>(fill_at + h * S::kTileBytes, from, valid);
+      }
+    }
+    cp_async_commit();
+    fill_at += S::kStageBytes;
+    if (++fill == S::kStages) fill = 0, fill_at = ring;
+  };
+  // a segment's first copies, into all stages but the last; the ring is empty
+  auto begin = [&](const Segment& sg) {
+    fill = stage = 0;
+    fill_at = at = ring;
+    skipped = 0;
+    head = sg.pair / a.row_tiles;
+    table = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
     // rows [key0, key1) of the cache; none if every token is padding
-    const int key0 = chunk * kUnit;
-    const int key1 = seq.fresh > 0 ? min(seq.len, (chunk + take) * kUnit) : 0;
-    const int64_t q_row0 = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0;
+    const int key0 = max(sg.chunk - extra, 0) * kUnit;
+    key1 = sg.fresh > 0 ? min(sg.len, max(sg.chunk + sg.take - extra, 0) * kUnit) : 0;
+    // this warp's steps of kHalves tiles each, a stride apart
+    first_key = key0 + warp * (kHalves * kTile);
+    steps = key1 > first_key ? (key1 - first_key + kStride - 1) / kStride : 0;
+    block = block_of(lane);
+    block_next = block_of(32 + lane);
+#pragma unroll
+    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+  };
+  begin(seg);
+
+  while (true) {
+    const int row0 = seg.pair % a.row_tiles * S::kRows;
+    const int rows = min(S::kRows, a.rows - row0);
+    const int64_t q_row0 = (static_cast<int64_t>(seg.b) * a.h_kv + seg.pair / a.row_tiles) * a.rows + row0;
 
     // ---- queries as the products' operand: registers 0 and 1 of step s hold
     // the columns that the threads' K registers of that step hold. In shared
     // memory where they would take too many registers.
-    uint32_t qf[S::kQInSmem ? 1 : NT][S::kQInSmem ? 1 : kSteps][2];
+    constexpr int kMine = S::kQInSmem ? 1 : NT;  // column blocks of this warp
+    uint32_t qf[kMine][kSteps][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (S::kQInSmem && nt != warp) continue;  // a warp for each
-      uint32_t w[kSteps][2];
-      const bool live = nt * 8 + g < rows;
-      const uint16_t* qp = a.q + (q_row0 + nt * 8 + g) * D;
+    for (int i = 0; i < kMine; ++i) {
+      const int r = (S::kQInSmem ? warp : i) * 8 + g;
+      const bool live = r < rows;
+      const uint16_t* qp = a.q + (q_row0 + r) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
         if constexpr (Q4) {
           const uint2 two = live ? __ldcg(reinterpret_cast<const uint2*>(qp + t * (D / 4) + 4 * s))
                                  : make_uint2(0, 0);
-          w[s][0] = two.x;
-          w[s][1] = two.y;
+          qf[i][s][0] = two.x;
+          qf[i][s][1] = two.y;
         } else {
           const uint32_t* src = reinterpret_cast<const uint32_t*>(qp + 16 * s + 2 * t);
-          w[s][0] = live ? __ldcg(src) : 0u;
-          w[s][1] = live ? __ldcg(src + 4) : 0u;
+          qf[i][s][0] = live ? __ldcg(src) : 0u;
+          qf[i][s][1] = live ? __ldcg(src + 4) : 0u;
         }
       }
+    }
+
+#pragma unroll
+    for (int n = 0; n < kMine; ++n) {
+      uint32_t (&w)[kSteps][2] = qf[n];
+      const int nt = S::kQInSmem ? warp : n;
+      if (nt >= NT) continue;
       if constexpr (Q4) {
         // the row's largest magnitude decides a power of two that brings it
         // below 2^9; what is 2^-33 of it or less may lose bits
@@ -450,27 +554,26 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         const float d0 = __int_as_float((127 - up0) << 23), d1 = __int_as_float((127 - up1) << 23);
         if (t == 0) s_mult[nt * 8 + g] = fmaxf(a.scale_log2 * d0 * d1, 1.2e-38f);
       }
+      if constexpr (S::kQInSmem) {
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if constexpr (S::kQInSmem) {
-          s_q[s * NT + nt][lane] = make_uint2(w[s][0], w[s][1]);
-        } else {
-          qf[nt][s][0] = w[s][0];
-          qf[nt][s][1] = w[s][1];
-        }
+        for (int s = 0; s < kSteps; ++s) s_q[s * NT + nt][lane] = make_uint2(w[s][0], w[s][1]);
       }
     }
     if (tid < S::kRows) {  // row tid of the tile sees the cached rows before its limit
       const int token = (row0 + tid) % a.n_q;
       int limit = 0x7fffffff;  // rows that nobody reads need no mask
-      if (tid < rows && token < seq.fresh) {
-        limit = seq.len;
-        if (a.causal) limit = min(limit, seq.len - seq.fresh + token + 1);
+      if (tid < rows && token < seg.fresh) {
+        limit = seg.len;
+        if (a.causal) limit = min(limit, seg.len - seg.fresh + token + 1);
       }
       s_limit[tid] = limit;
     }
+    if (tid == 0) {
+      s_seg = seg;
+      s_rest = rest;
+    }
     // cached rows from here on are hidden from some row of the tile
-    const int hidden = a.causal ? min(seq.len, seq.len - seq.fresh + 1) : seq.len;
+    const int hidden = a.causal ? min(seg.len, seg.len - seg.fresh + 1) : seg.len;
 
     float o[NT][kSteps][4];
     float m[NT][2], l[NT][2];
@@ -482,58 +585,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // ---- this warp's steps of kHalves tiles each, a stride apart
-    constexpr int kHalves = S::kHalves, kStride = kHalves * kUnit;
-    const int first_key = key0 + warp * (kHalves * kTile);
-    const int steps = key1 > first_key ? (key1 - first_key + kStride - 1) / kStride : 0;
-    const int32_t* table = a.table + static_cast<int64_t>(b) * a.max_pages;
-    // tile j's place in the pools, in tiles (kNoBlock: its page is no page);
-    // 32 at a time, one per lane, the next 32 on their way
-    constexpr uint32_t kNoBlock = 0xffffffffu;
-    auto block_of = [&](int j) {
-      const int key = first_key + j / kHalves * kStride + j % kHalves * kTile;
-      if (key >= key1) return 0u;
-      const int page = __ldcg(table + (key >> a.page_shift));
-      if (page < 0 || page >= a.n_pages) {
-        atomicOr(&g_device_error, kErrIndex);
-        return kNoBlock;
-      }
-      return (static_cast<uint32_t>(page * a.h_kv + head) << (a.page_shift - 4)) +
-             ((key & ((1 << a.page_shift) - 1)) >> 4);
-    };
-    uint32_t block = block_of(lane), block_next = block_of(32 + lane);
-    uint32_t skipped = 0;        // bit kHalves s + h: tile h of stage s has no page
-    int fill = 0;                // the stage that is filled next
-    uint32_t fill_at = ring;
-    auto issue = [&](int i) {  // step i's tiles into the next stage
-      if (i < steps) {
-        const int j = i * kHalves;
-        if ((j & 31) == 0 && j > 0) {
-          block = block_next;
-          block_next = block_of(j + 32 + lane);
-        }
-        skipped &= ~(((1u << kHalves) - 1) << (fill * kHalves));
-#pragma unroll
-        for (int h = 0; h < kHalves; ++h) {
-          uint32_t from = __shfl_sync(0xffffffffu, block, (j + h) & 31);
-          int valid = key1 - (first_key + i * kStride + h * kTile);
-          if (from == kNoBlock) {
-            skipped |= 1u << (fill * kHalves + h);
-            from = 0;
-            valid = 0;
-          }
-          if (valid >= kTile) copy.template load<true>(fill_at + h * S::kTileBytes, from, valid);
-          else copy.template load<false>(fill_at + h * S::kTileBytes, from, valid);
-        }
-      }
-      cp_async_commit();
-      fill_at += S::kStageBytes;
-      if (++fill == S::kStages) fill = 0, fill_at = ring;
-    };
-#pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
-
-    __syncthreads();  // s_limit, s_mult, s_q
+    __syncthreads();  // s_limit, s_mult, s_q, s_seg
     float mult[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -543,8 +595,6 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       if constexpr (S::kQInSmem) return s_q[s * NT + nt][lane];
       else return make_uint2(qf[nt][s][0], qf[nt][s][1]);
     };
-    int stage = 0;
-    uint32_t at = ring;
     const int row_lo = Q4 ? cached_row(g) : g;  // of S^T's registers 0, 1; 8 further: 2, 3
     for (int i = 0; i < steps; ++i) {
       cp_async_wait<S::kStages - 2>();
@@ -768,8 +818,10 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
           // token, with the rows that it does not see cleared, and only the
           // token's own columns of O taken from them
           const int r0 = key + h * kTile + (Q4 ? t : 2 * t), r1 = r0 + (Q4 ? 4 : 1);
-          for (int token = 0; token < seq.fresh; ++token) {
-            const int seen = a.causal ? seq.len - seq.fresh + token + 1 : seq.len;
+          const int fresh = s_seg.fresh, len = s_seg.len;
+          const int row0 = s_seg.pair % a.row_tiles * S::kRows;
+          for (int token = 0; token < fresh; ++token) {
+            const int seen = a.causal ? len - fresh + token + 1 : len;
             uint32_t keep[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r)
@@ -814,7 +866,35 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       at += S::kStageBytes;
       if (++stage == S::kStages) stage = 0, at = ring;
     }
-    cp_async_wait<0>();
+    // ---- what comes next, its first copies on their way before this segment
+    // is finished where O has room beside them: in the stage left free
+    const Segment done = s_seg;
+    rest = s_rest;
+    const bool more = rest > 0;
+    if (more) {
+      seg.unit = done.unit + done.take;
+      seg.b = done.b;
+      seg.pair = done.pair + 1;
+      seg.chunk = 0;
+      seg.units = done.units;
+      seg.len = done.len;
+      seg.fresh = done.fresh;
+      if (seg.pair == pairs) {
+        seg.pair = 0;
+        ++seg.b;
+        const Sequence seq = sequence(a, seg.b);
+        seg.len = seq.len;
+        seg.fresh = seq.fresh;
+        seg.units = pair_units(seq, extra);
+      }
+      seg.take = static_cast<int>(min(rest, static_cast<int64_t>(seg.units)));
+      rest -= seg.take;
+      if (S::kAhead) {
+        __syncwarp();  // no lane reads a stage any more
+        begin(seg);
+      }
+    }
+    if (!S::kAhead || !more) cp_async_wait<0>();
 
     // ---- the four warps' results of these units, joined in shared memory
 #pragma unroll
@@ -825,8 +905,13 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         for (int s = 4; s < 32; s <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], s);
         if (g == 0) s_ml[warp][nt * 8 + 2 * t + c] = make_float2(m[nt][c], l[nt][c]);
       }
-    __syncthreads();  // also: no warp uses its ring any more
-    float* o_smem = reinterpret_cast<float*>(smem);
+    __syncthreads();  // also: without kAhead no warp uses its ring any more
+    // warp w's rows of O: [S::kRows][S::kPitch] floats
+    auto o_smem = [&](int w) {
+      return reinterpret_cast<float*>(
+          smem + (S::kAhead ? (w * S::kStages + S::kStages - 1) * S::kStageBytes
+                            : w * S::kRows * S::kPitch * 4));
+    };
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -836,7 +921,7 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
         const float f = ex2(m[nt][c] - top);  // a warp without a row has O = l = 0
-        float* dst = o_smem + (warp * S::kRows + r) * S::kPitch;
+        float* dst = o_smem(warp) + r * S::kPitch;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
           // the two columns of block s that this thread has
@@ -846,9 +931,13 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
         }
       }
     __syncthreads();
-    const bool whole = chunk == 0 && take == seq.units;
-    const int64_t slot = 2 * me + (chunk == 0 ? 1 : 0);
-    for (int i = tid; i < rows * (D / 2); i += kThreads) {
+    const bool whole = done.chunk == 0 && done.take == done.units;
+    const int64_t slot = 2 * me + (done.chunk == 0 ? 1 : 0);
+    const int done_row0 = done.pair % a.row_tiles * S::kRows;
+    const int done_rows = min(S::kRows, a.rows - done_row0);
+    const int64_t out_row0 =
+        (static_cast<int64_t>(done.b) * a.h_kv + done.pair / a.row_tiles) * a.rows + done_row0;
+    for (int i = tid; i < done_rows * (D / 2); i += kThreads) {
       const int r = i / (D / 2), d = i % (D / 2) * 2;
       float top = s_ml[0][r].x;
 #pragma unroll
@@ -858,40 +947,34 @@ __global__ void __launch_bounds__(kThreads) decode_paged_kernel(const PagedArgs 
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = s_ml[w][r];
         sum += ml.y * ex2(ml.x - top);
-        const float2 y = *reinterpret_cast<const float2*>(o_smem + (w * S::kRows + r) * S::kPitch + d);
+        const float2 y = *reinterpret_cast<const float2*>(o_smem(w) + r * S::kPitch + d);
         y0 += y.x;
         y1 += y.y;
       }
       if (whole) {
-        const bool real = (row0 + r) % a.n_q < seq.fresh;
+        const bool real = (done_row0 + r) % a.n_q < done.fresh;
         // no row seen (sum 0), or padding: 0; a sum that is no number stays one
         const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
-        *reinterpret_cast<uint32_t*>(a.out + (q_row0 + r) * D + d) =
+        *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * D + d) =
             inv == 0.f ? 0u : pack_bf16x2(y0 * inv, y1 * inv);
       } else {
         *reinterpret_cast<float2*>(a.part_o + (slot * S::kRows + r) * D + d) = make_float2(y0, y1);
         if (d == 0) a.part_ml[slot * S::kRows + r] = make_float2(top, sum);
       }
     }
-    __syncthreads();  // shared memory is free for the next sequence
-    if (chunk == 0) {
+    if (tid == 0 && done.chunk == 0) {
       // the block of this pair's last unit
-      const int64_t last = base * pairs + static_cast<int64_t>(pair + 1) * seq.units;
-      const int last_block = static_cast<int>(quotient(last * blocks - 1, total));
-      if (a.by_pair) {
-        if (tid == 0) a.split[b * pairs + pair] = make_int2(whole ? -1 : static_cast<int>(me), last_block);
-      } else if (!whole) {
-        begun = b * pairs + pair;
-        begun_last = last_block;
-      }
+      const int64_t upto = done.unit + done.units;
+      const int last = static_cast<int>(quotient(upto * s_plan[1] - 1, s_plan[0]));
+      if (a.by_pair)
+        a.split[done.b * pairs + done.pair] = make_int2(whole ? -1 : static_cast<int>(me), last);
+      else if (!whole)
+        a.split[me] = make_int2(done.b * pairs + done.pair, last);
     }
-    unit += take;
-    if (unit == (base + seq.units) * pairs) {
-      base += seq.units;
-      ++b;
-    }
+    __syncthreads();  // O's and the segment's shared memory is free
+    if (!more) break;
+    if (!S::kAhead) begin(seg);
   }
-  if (tid == 0 && !a.by_pair) a.split[me] = make_int2(begun, begun_last);
 }
 
 // Joins the partial results of one query row of a pair that several blocks
@@ -992,7 +1075,7 @@ Layout layout(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pag
   const int rows = h / h_kv * n_q;
   w.tile_rows = 8 * column_blocks(rows);
   w.row_tiles = (rows + w.tile_rows - 1) / w.tile_rows;
-  const int64_t per_pair = (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
+  const int64_t per_pair = 1 + (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
   w.units = int64_t(B) * h_kv * w.row_tiles * per_pair;
   w.blocks = static_cast<int>(w.units < kMaxBlocks ? w.units : kMaxBlocks);
   auto align = [](size_t x) { return (x + 255u) & ~size_t(255u); };
