@@ -41,6 +41,8 @@
 // of the row's largest; and P is rounded to f16: to 11 bits, well below the
 // output's 8, where it is at least 2^-25 of the row's largest in its warp
 // (m is 2^kShift below that), and to 2^-36 of that below.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -596,11 +598,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       else return make_uint2(qf[nt][s][0], qf[nt][s][1]);
     };
     const int row_lo = Q4 ? cached_row(g) : g;  // of S^T's registers 0, 1; 8 further: 2, 3
-    for (int i = 0; i < steps; ++i) {
-      cp_async_wait<S::kStages - 2>();
-      __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
-      issue(i + S::kStages - 1);
-      const int key = first_key + i * kStride;
+    // one step; MASKED: some row of it may be hidden from some query
+    auto step = [&](auto masked, int key) {
+      constexpr bool kMasked = decltype(masked)::value;
 
       // ---- S^T = K Q^T; for one column block even and odd steps apart, as
       // one chain of dependent products would be waited for
@@ -672,8 +672,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       // ---- masks, in the sequence's last rows or where a page is missing;
       // there also: is any value of V not finite?
       bool odd = false;
-      const uint32_t missing = (skipped >> (stage * kHalves)) & ((1u << kHalves) - 1);
-      if (key + kHalves * kTile > hidden || missing != 0) {
+      if constexpr (kMasked) {
+        const uint32_t missing = (skipped >> (stage * kHalves)) & ((1u << kHalves) - 1);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           const int row = key + h * kTile + row_lo;
@@ -813,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
             }
           }
         };
-        if (odd) {
+        if (kMasked && odd) {
           // 0 times an infinity is no number: the products once for each new
           // token, with the rows that it does not see cleared, and only the
           // token's own columns of O taken from them
@@ -863,6 +863,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
           }
         }
       }
+    };
+    for (int i = 0; i < steps; ++i) {
+      cp_async_wait<S::kStages - 2>();
+      __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
+      issue(i + S::kStages - 1);
+      const int key = first_key + i * kStride;
+      if (key + kHalves * kTile > hidden || ((skipped >> (stage * kHalves)) & ((1u << kHalves) - 1)) != 0)
+        step(std::true_type{}, key);
+      else
+        step(std::false_type{}, key);
       at += S::kStageBytes;
       if (++stage == S::kStages) stage = 0, at = ring;
     }
