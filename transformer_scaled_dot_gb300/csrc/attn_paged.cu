@@ -98,7 +98,8 @@ struct Shape {
   static constexpr int kStages = 3;
   static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
   static constexpr int kPitch = D + 4;  // floats of a row of O in shared memory
-  static constexpr bool kQInSmem = NT * D > 128;
+  // a 4-bit cache's inner loop has no registers to spare for Q
+  static constexpr bool kQInSmem = Q4 || NT * D > 128;
   // p = 2^(x - m) is at most 2^(kShift + kSlack); f16 holds up to 2^15.99
   static constexpr float kShift = Q4 ? 11.f : 0.f, kSlack = Q4 ? 4.f : 8.f;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
@@ -357,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
   constexpr int kSteps = D / 16;  // products of S, and blocks of 16 columns of O
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps][S::kRows];
+  __shared__ float2 s_join[S::kRows];
   __shared__ float s_mult[S::kRows];
   __shared__ int s_limit[S::kRows];
   __shared__ uint2 s_q[S::kQInSmem ? kSteps * NT : 1][32];
@@ -372,8 +374,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
   const int pairs = a.h_kv * a.row_tiles;  // (key head, row tile) of a sequence
   int64_t total = 0;
   int none = 0;  // sequences without rows
+  const Sequence early = sequence(a, min(lane, a.B - 1));  // the first 32, not loaded again
   for (int b0 = 0; b0 < a.B; b0 += 32) {
-    int u = b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+    int u = b0 == 0 ? early.units : b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+    if (b0 + lane >= a.B) u = 0;
     none += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.B && u == 0));
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) u += __shfl_xor_sync(0xffffffffu, u, s);
@@ -396,7 +400,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     const int64_t want = quotient(seg.unit, pairs);
     int64_t base = 0;  // units of one pair of all sequences before b
     for (int b0 = 0;; b0 += 32) {
-      const int u = b0 + lane < a.B ? pair_units(sequence(a, b0 + lane), extra) : 0;
+      const Sequence seq = b0 == 0 ? early : sequence(a, min(b0 + lane, a.B - 1));
+      const int u = b0 + lane < a.B ? pair_units(seq, extra) : 0;
       int upto = u;
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) {
@@ -405,17 +410,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       }
       const unsigned past = __ballot_sync(0xffffffffu, base + upto > want);
       if (past != 0u || b0 + 32 >= a.B) {  // the second: for certain to end
-        const int first = past != 0u ? __ffs(past) - 1 : 31;
-        seg.b = min(b0 + first, a.B - 1);
+        const int first = past != 0u ? __ffs(past) - 1 : (a.B - 1) & 31;
+        seg.b = b0 + first;
         base += __shfl_sync(0xffffffffu, upto - u, first);
+        seg.len = __shfl_sync(0xffffffffu, seq.len, first);
+        seg.fresh = __shfl_sync(0xffffffffu, seq.fresh, first);
+        seg.units = __shfl_sync(0xffffffffu, u, first);
         break;
       }
       base += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const Sequence seq = sequence(a, seg.b);
-    seg.len = seq.len;
-    seg.fresh = seq.fresh;
-    seg.units = pair_units(seq, extra);
     const int64_t local = seg.unit - base * pairs;
     seg.pair = static_cast<int>(quotient(local, seg.units));
     seg.chunk = static_cast<int>(local - static_cast<int64_t>(seg.pair) * seg.units);
@@ -602,8 +606,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     auto step = [&](auto masked, int key) {
       constexpr bool kMasked = decltype(masked)::value;
 
-      // ---- S^T = K Q^T; for one column block even and odd steps apart, as
-      // one chain of dependent products would be waited for
+      // ---- S^T = K Q^T; for one column block of one tile even and odd steps
+      // apart, as one chain of dependent products would be waited for
+      constexpr bool kTwoChains = NT * kHalves == 1;
       float x[kHalves][NT][4];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
@@ -619,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               const uint2 q = query(nt, s);
-              float (&to)[4] = NT == 1 && (s & 1) ? x2[nt] : x[h][nt];
-              if (s == 0 || (NT == 1 && s == 1)) mma_first<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
+              float (&to)[4] = kTwoChains && (s & 1) ? x2[nt] : x[h][nt];
+              if (s == 0 || (kTwoChains && s == 1)) mma_first<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
               else mma<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
             }
           }
@@ -658,12 +663,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
               const uint2 q0 = query(nt, 2 * i4), q1 = query(nt, 2 * i4 + 1);
               if (i4 == 0) mma_first<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
               else mma<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
-              if (i4 == 0 && NT == 1) mma_first<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
-              else mma<true>(NT == 1 ? x2[nt] : x[h][nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
+              if (i4 == 0 && kTwoChains) mma_first<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
+              else mma<true>(kTwoChains ? x2[nt] : x[h][nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
             }
           }
         }
-        if constexpr (NT == 1) {
+        if constexpr (kTwoChains) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) x[h][0][c] += x2[0][c];
         }
@@ -702,8 +707,34 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
         odd = __any_sync(0xffffffffu, odd);
       }
 
+      // ---- 4-bit: V's codes and scales on their way while the softmax is done.
+      // [tile][rows' half][cached rows r0, r1][word]
+      uint32_t v_codes[kHalves][2][2][D / 64], v_scale[kHalves][2];
+      if constexpr (Q4) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
+          const uint32_t sat = vat + kTile * S::kRowBytes + D;
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int a0 = t + 8 * r, a1 = a0 + 4;
+            if constexpr (D == 128) {
+              const uint2 w0 = lds64(vat + v_code_offset<D>(a0, g * 8));
+              const uint2 w1 = lds64(vat + v_code_offset<D>(a1, g * 8));
+              v_codes[h][r][0][0] = w0.x, v_codes[h][r][0][1] = w0.y;
+              v_codes[h][r][1][0] = w1.x, v_codes[h][r][1][1] = w1.y;
+            } else {
+              v_codes[h][r][0][0] = lds32(vat + v_code_offset<D>(a0, g * 4));
+              v_codes[h][r][1][0] = lds32(vat + v_code_offset<D>(a1, g * 4));
+            }
+            const int group = D == 128 ? g : g >> 1;
+            v_scale[h][r] = __byte_perm(lds8(sat + a0 * (D / 16) + group),
+                                        lds8(sat + a1 * (D / 16) + group), 0x0040);
+          }
+        }
+      }
+
       // ---- x - m, and whether any passes what P may be
-      bool over = false;
       float y[kHalves][NT][4];
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
@@ -712,9 +743,16 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             y[h][nt][c] = fmaf(x[h][nt][c], mult[nt][c & 1], -m[nt][c & 1]);
-            over |= y[h][nt][c] > S::kShift + S::kSlack;
           }
-      if (__any_sync(0xffffffffu, over)) {
+      float highest = kLowest;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          highest = fmax3(highest, y[h][nt][0], y[h][nt][1]);
+          highest = fmax3(highest, y[h][nt][2], y[h][nt][3]);
+        }
+      if (__any_sync(0xffffffffu, highest > S::kShift + S::kSlack)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -771,26 +809,6 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
         const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
-        uint32_t v_codes[2][2][D / 64], v_scale[2];  // 4-bit: [rows' half][r0, r1][word]
-        if constexpr (Q4) {
-          const uint32_t sat = vat + kTile * S::kRowBytes + D;
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int a0 = t + 8 * r, a1 = a0 + 4;
-            if constexpr (D == 128) {
-              const uint2 w0 = lds64(vat + v_code_offset<D>(a0, g * 8));
-              const uint2 w1 = lds64(vat + v_code_offset<D>(a1, g * 8));
-              v_codes[r][0][0] = w0.x, v_codes[r][0][1] = w0.y;
-              v_codes[r][1][0] = w1.x, v_codes[r][1][1] = w1.y;
-            } else {
-              v_codes[r][0][0] = lds32(vat + v_code_offset<D>(a0, g * 4));
-              v_codes[r][1][0] = lds32(vat + v_code_offset<D>(a1, g * 4));
-            }
-            const int group = D == 128 ? g : g >> 1;
-            v_scale[r] = scales_f16x2(lds8(sat + a0 * (D / 16) + group) |
-                                      (lds8(sat + a1 * (D / 16) + group) << 8));
-          }
-        }
         // the operand of kBlock blocks of 16 columns from block s0 on
         constexpr int kBlock = Q4 ? 4 : 1;
         auto v_operand = [&](int s0, uint32_t (&va)[kBlock][4]) {
@@ -801,14 +819,15 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
           } else {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const uint32_t u = v_codes[r][0][s0 / 4], v = v_codes[r][1][s0 / 4];
+              const uint32_t u = v_codes[h][r][0][s0 / 4], v = v_codes[h][r][1][s0 / 4];
+              const uint32_t sc = scales_f16x2(v_scale[h][r]);
               uint32_t even[4], uneven[4];
               codes_f16x2((u & 0x0f0f0f0fu) | ((v << 4) & 0xf0f0f0f0u), even);
               codes_f16x2(((u >> 4) & 0x0f0f0f0fu) | (v & 0xf0f0f0f0u), uneven);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                va[e][2 * r] = mul_f16x2(even[e], v_scale[r]);
-                va[e][2 * r + 1] = mul_f16x2(uneven[e], v_scale[r]);
+                va[e][2 * r] = mul_f16x2(even[e], sc);
+                va[e][2 * r + 1] = mul_f16x2(uneven[e], sc);
               }
             }
           }
@@ -940,6 +959,14 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
           dst[d0 + (Q4 ? 1 : 8)] = o[nt][s][2 + c] * f;
         }
       }
+    if (tid < S::kRows) {
+      float top = s_ml[0][tid].x, sum = 0.f;
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][tid].x);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += s_ml[w][tid].y * ex2(s_ml[w][tid].x - top);
+      s_join[tid] = make_float2(top, sum);
+    }
     __syncthreads();
     const bool whole = done.chunk == 0 && done.take == done.units;
     const int64_t slot = 2 * me + (done.chunk == 0 ? 1 : 0);
@@ -949,27 +976,23 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
         (static_cast<int64_t>(done.b) * a.h_kv + done.pair / a.row_tiles) * a.rows + done_row0;
     for (int i = tid; i < done_rows * (D / 2); i += kThreads) {
       const int r = i / (D / 2), d = i % (D / 2) * 2;
-      float top = s_ml[0][r].x;
-#pragma unroll
-      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[w][r].x);
-      float sum = 0.f, y0 = 0.f, y1 = 0.f;
+      float y0 = 0.f, y1 = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 ml = s_ml[w][r];
-        sum += ml.y * ex2(ml.x - top);
         const float2 y = *reinterpret_cast<const float2*>(o_smem(w) + r * S::kPitch + d);
         y0 += y.x;
         y1 += y.y;
       }
+      const float2 join = s_join[r];
       if (whole) {
         const bool real = (done_row0 + r) % a.n_q < done.fresh;
         // no row seen (sum 0), or padding: 0; a sum that is no number stays one
-        const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
+        const float inv = real && join.y != 0.f ? a.v_factor / join.y : 0.f;
         *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * D + d) =
             inv == 0.f ? 0u : pack_bf16x2(y0 * inv, y1 * inv);
       } else {
         *reinterpret_cast<float2*>(a.part_o + (slot * S::kRows + r) * D + d) = make_float2(y0, y1);
-        if (d == 0) a.part_ml[slot * S::kRows + r] = make_float2(top, sum);
+        if (d == 0) a.part_ml[slot * S::kRows + r] = join;
       }
     }
     if (tid == 0 && done.chunk == 0) {
