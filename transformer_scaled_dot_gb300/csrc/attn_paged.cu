@@ -56,6 +56,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                // cached rows of a product, within one page
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
+// Sequences of at most this many rows are not split: their pairs' four warps
+// take four tiles each at the most, which is shorter than a merge.
+constexpr int kUnsplitRows = 4 * kUnit;
 constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
 constexpr int kMergeThreads = 128;
@@ -82,6 +85,7 @@ struct PagedArgs {
   float* part_o;   // [blocks][2][rows of a tile][d]
   float2* part_ml; // [blocks][2][rows of a tile]
   int B, h_kv, n_q, rows, row_tiles, n_pages, page_shift, max_pages;
+  bool unsplit;  // every pair is one unit, whatever its rows
   bool causal;
   float scale_log2;  // scale log2(e), with the keys' factor
   float v_factor;
@@ -373,30 +377,45 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
   // this block's range of units: each warp by itself sums the sequences' units
   const int pairs = a.h_kv * a.row_tiles;  // (key head, row tile) of a sequence
   int64_t total = 0;
-  int none = 0;  // sequences without rows
-  const Sequence early = sequence(a, min(lane, a.B - 1));  // the first 32, not loaded again
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    int u = b0 == 0 ? early.units : b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
-    if (b0 + lane >= a.B) u = 0;
-    none += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.B && u == 0));
+  int extra = 0;
+  Sequence early = {};  // the first 32, not loaded again
+  if (!a.unsplit) early = sequence(a, min(lane, a.B - 1));
+  if (a.unsplit) {
+    total = static_cast<int64_t>(a.B) * pairs;
+  } else {
+    int none = 0;  // sequences without rows
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      int u = b0 == 0 ? early.units : b0 + lane < a.B ? sequence(a, b0 + lane).units : 0;
+      if (b0 + lane >= a.B) u = 0;
+      none += __popc(__ballot_sync(0xffffffffu, b0 + lane < a.B && u == 0));
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) u += __shfl_xor_sync(0xffffffffu, u, s);
-    total += u;
+      for (int s = 16; s > 0; s >>= 1) u += __shfl_xor_sync(0xffffffffu, u, s);
+      total += u;
+    }
+    total *= pairs;
+    // a pair's own cost counts as far as the blocks have that much to do: with
+    // a unit or two for each it would only leave blocks without rows
+    extra = static_cast<int>(min(quotient(total, gridDim.x), static_cast<int64_t>(kPairUnits)));
+    total += static_cast<int64_t>(pairs) * (extra > 0 ? static_cast<int64_t>(a.B) * extra : none);
   }
-  total *= pairs;
-  // a pair's own cost counts as far as the blocks have that much to do: with
-  // a unit or two for each it would only leave blocks without rows
-  const int extra = static_cast<int>(min(quotient(total, gridDim.x), static_cast<int64_t>(kPairUnits)));
-  total += static_cast<int64_t>(pairs) * (extra > 0 ? static_cast<int64_t>(a.B) * extra : none);
   const int64_t blocks = min(static_cast<int64_t>(gridDim.x), total);
   const int64_t me = blockIdx.x;
-  if (tid == 0 && !a.by_pair) a.split[me] = make_int2(-1, 0);
+  if (tid == 0 && !a.by_pair && !a.unsplit) a.split[me] = make_int2(-1, 0);
   if (me >= blocks) return;
   const int64_t each = quotient(total, blocks), over_all = total - each * blocks;
   Segment seg;
   seg.unit = me * each + quotient(me * over_all, blocks);
   int64_t rest = (me + 1) * each + quotient((me + 1) * over_all, blocks) - seg.unit;
-  {
+  if (a.unsplit) {
+    seg.b = static_cast<int>(quotient(seg.unit, pairs));
+    seg.pair = static_cast<int>(seg.unit - static_cast<int64_t>(seg.b) * pairs);
+    const Sequence seq = sequence(a, seg.b);
+    seg.len = seq.len;
+    seg.fresh = seq.fresh;
+    seg.units = seg.take = 1;
+    seg.chunk = 0;
+    --rest;
+  } else {
     const int64_t want = quotient(seg.unit, pairs);
     int64_t base = 0;  // units of one pair of all sequences before b
     for (int b0 = 0;; b0 += 32) {
@@ -489,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     table = a.table + static_cast<int64_t>(sg.b) * a.max_pages;
     // rows [key0, key1) of the cache; none if every token is padding
     const int key0 = max(sg.chunk - extra, 0) * kUnit;
-    key1 = sg.fresh > 0 ? min(sg.len, max(sg.chunk + sg.take - extra, 0) * kUnit) : 0;
+    key1 = a.unsplit ? sg.len : min(sg.len, max(sg.chunk + sg.take - extra, 0) * kUnit);
+    if (sg.fresh == 0) key1 = 0;
     // this warp's steps of kHalves tiles each, a stride apart
     first_key = key0 + warp * (kHalves * kTile);
     steps = key1 > first_key ? (key1 - first_key + kStride - 1) / kStride : 0;
@@ -914,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
         const Sequence seq = sequence(a, seg.b);
         seg.len = seq.len;
         seg.fresh = seq.fresh;
-        seg.units = pair_units(seq, extra);
+        seg.units = a.unsplit ? 1 : pair_units(seq, extra);
       }
       seg.take = static_cast<int>(min(rest, static_cast<int64_t>(seg.units)));
       rest -= seg.take;
@@ -974,28 +994,28 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     const int done_rows = min(S::kRows, a.rows - done_row0);
     const int64_t out_row0 =
         (static_cast<int64_t>(done.b) * a.h_kv + done.pair / a.row_tiles) * a.rows + done_row0;
-    for (int i = tid; i < done_rows * (D / 2); i += kThreads) {
-      const int r = i / (D / 2), d = i % (D / 2) * 2;
-      float y0 = 0.f, y1 = 0.f;
+    for (int i = tid; i < done_rows * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float2 y = *reinterpret_cast<const float2*>(o_smem(w) + r * S::kPitch + d);
-        y0 += y.x;
-        y1 += y.y;
+        const float4 z = *reinterpret_cast<const float4*>(o_smem(w) + r * S::kPitch + d);
+        y.x += z.x, y.y += z.y, y.z += z.z, y.w += z.w;
       }
       const float2 join = s_join[r];
       if (whole) {
         const bool real = (done_row0 + r) % a.n_q < done.fresh;
         // no row seen (sum 0), or padding: 0; a sum that is no number stays one
         const float inv = real && join.y != 0.f ? a.v_factor / join.y : 0.f;
-        *reinterpret_cast<uint32_t*>(a.out + (out_row0 + r) * D + d) =
-            inv == 0.f ? 0u : pack_bf16x2(y0 * inv, y1 * inv);
+        *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * D + d) =
+            inv == 0.f ? make_uint2(0u, 0u)
+                       : make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
       } else {
-        *reinterpret_cast<float2*>(a.part_o + (slot * S::kRows + r) * D + d) = make_float2(y0, y1);
+        *reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + d) = y;
         if (d == 0) a.part_ml[slot * S::kRows + r] = join;
       }
     }
-    if (tid == 0 && done.chunk == 0) {
+    if (tid == 0 && done.chunk == 0 && !a.unsplit) {
       // the block of this pair's last unit
       const int64_t upto = done.unit + done.units;
       const int last = static_cast<int>(quotient(upto * s_plan[1] - 1, s_plan[0]));
@@ -1156,7 +1176,7 @@ cudaError_t launch_instance(PagedArgs a, const Layout& w, cudaStream_t stream) {
   const int64_t pairs = int64_t(a.B) * a.h_kv * a.row_tiles;
   a.by_pair = pairs <= static_cast<int64_t>(blocks);
   e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, a);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || a.unsplit) return e;
   const unsigned rows = static_cast<unsigned>(a.rows < w.tile_rows ? a.rows : w.tile_rows);
   return launch_pdl(decode_paged_merge_kernel<D>,
                     dim3(a.by_pair ? static_cast<unsigned>(pairs) : blocks, rows),
@@ -1208,6 +1228,7 @@ cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream
   a.n_pages = c.n_pages;
   a.page_shift = c.page_shift;
   a.max_pages = c.max_pages;
+  a.unsplit = (c.max_pages << c.page_shift) <= kUnsplitRows;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f * (q4 ? c.k_factor : 1.f);
   a.v_factor = q4 ? c.v_factor : 1.f;
