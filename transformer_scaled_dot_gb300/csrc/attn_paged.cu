@@ -56,9 +56,15 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                // cached rows of a product, within one page
 constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
-// Sequences of at most this many rows are not split: their pairs' four warps
-// take four tiles each at the most, which is shorter than a merge.
-constexpr int kUnsplitRows = 4 * kUnit;
+// Caches of at most this many rows are not split: a block takes each pair
+// whole and no merge is launched. 7 sequences of 900 rows at 32 query and 8
+// key heads of 128: 10.3 us against 11.4, 4-bit 10.4 against 14.5; of 300
+// rows 6.1 against 9.9. The wide tiles of 28 query rows take longer for a row:
+// 2 sequences of 900 rows at 4 key heads 17.6 us against 13.5 in 4 bits, but
+// 7 of them 17.7 against 19.8.
+constexpr int unsplit_rows(int tile_rows, int64_t pairs) {
+  return tile_rows > 16 && pairs < 24 ? 512 : 1280;
+}
 constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
 constexpr int kMergeThreads = 128;
@@ -1228,7 +1234,8 @@ cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream
   a.n_pages = c.n_pages;
   a.page_shift = c.page_shift;
   a.max_pages = c.max_pages;
-  a.unsplit = (c.max_pages << c.page_shift) <= kUnsplitRows;
+  a.unsplit = (c.max_pages << c.page_shift) <=
+              unsplit_rows(w.tile_rows, int64_t(p.B) * c.h_kv * w.row_tiles);
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f * (q4 ? c.k_factor : 1.f);
   a.v_factor = q4 ? c.v_factor : 1.f;
