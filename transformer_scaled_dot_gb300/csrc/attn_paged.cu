@@ -232,6 +232,14 @@ __device__ __forceinline__ void codes_f16x2(uint32_t w, uint32_t (&x)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, d;}"
       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(w));
 }
+// one half of a pair twice (an operand's modifier, no instruction of its own)
+template <bool HIGH>
+__device__ __forceinline__ uint32_t twice(uint32_t x) {
+  uint32_t r;
+  if constexpr (HIGH) asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {h, h};}" : "=r"(r) : "r"(x));
+  else asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; mov.b32 %0, {l, l};}" : "=r"(r) : "r"(x));
+  return r;
+}
 // two e4m3 bytes -> a pair of f16 (exact)
 __device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
   uint32_t r;
@@ -488,17 +496,25 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
         block_next = block_of(j + 32 + lane);
       }
       skipped &= ~(((1u << kHalves) - 1) << (fill * kHalves));
+      uint32_t from[kHalves];
+      bool common = key1 - (first_key + i * kStride) >= kHalves * kTile;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        uint32_t from = __shfl_sync(0xffffffffu, block, (j + h) & 31);
-        int valid = key1 - (first_key + i * kStride + h * kTile);
-        if (from == kNoBlock) {
-          skipped |= 1u << (fill * kHalves + h);
-          from = 0;
-          valid = 0;
+        from[h] = __shfl_sync(0xffffffffu, block, (j + h) & 31);
+        common = common && from[h] != kNoBlock;
+      }
+      if (common) {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
+          copy.template load<true>(fill_at + h * S::kTileBytes, from[h], kTile);
+      } else {
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h) {
+          const bool missing = from[h] == kNoBlock;
+          if (missing) skipped |= 1u << (fill * kHalves + h);
+          copy.template load<false>(fill_at + h * S::kTileBytes, missing ? 0u : from[h],
+                                    missing ? 0 : key1 - (first_key + i * kStride + h * kTile));
         }
-        if (valid >= kTile) copy.template load<true>(fill_at + h * S::kTileBytes, from, valid);
-        else copy.template load<false>(fill_at + h * S::kTileBytes, from, valid);
       }
     }
     cp_async_commit();
@@ -668,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
             } else {
               const uint2 v = lds64(tile + k_code_offset<D>(row, t * 8));
               w[half][0] = v.x, w[half][1] = v.y;
-              sc[half] = scales_f16x2(lds8(tile + kTile * D + row * 4 + t) * 0x0101u);
+              sc[half] = scales_f16x2(lds8(tile + kTile * D + row * 4 + t));
             }
           }
 #pragma unroll
@@ -677,8 +693,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
             codes_f16x2(w[0][i4], lo);
             codes_f16x2(w[1][i4], hi);
             // d = 128: words 0, 1 are of the thread's first group, 2, 3 of its second
-            const uint32_t s0 = D == 128 ? __byte_perm(sc[0], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[0];
-            const uint32_t s1 = D == 128 ? __byte_perm(sc[1], 0, i4 < 2 ? 0x1010 : 0x3232) : sc[1];
+            const uint32_t s0 = i4 < 2 ? twice<false>(sc[0]) : twice<true>(sc[0]);
+            const uint32_t s1 = i4 < 2 ? twice<false>(sc[1]) : twice<true>(sc[1]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               lo[c] = mul_f16x2(lo[c], s0);
