@@ -67,7 +67,7 @@ constexpr int unsplit_rows(int tile_rows, int64_t pairs) {
 }
 constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
-constexpr int kMergeThreads = 128;
+constexpr int kMergeThreads = 256;
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
 // Query rows of a block's tile: 8 per column block of the products.
@@ -470,8 +470,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
   constexpr uint32_t kNoBlock = 0xffffffffu;
 
   // the part of a segment that this warp's copies go by
-  int first_key, steps, key1, head;
-  const int32_t* table;
+  int first_key = 0, key1 = 0, head = 0;
+  const int32_t* table = nullptr;
+  int to_load = 0;             // rows from the next step to load to key1, less than 1: none
+  int next_tile = 0, refill = 0;  // the next tile to load; where block runs out
   uint32_t block, block_next;  // of the steps' tiles, 32 at a time, one per lane
   uint32_t skipped = 0;        // bit kHalves s + h: tile h of stage s has no page
   int fill = 0, stage = 0;     // the stages that are filled and read next
@@ -488,19 +490,18 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     return (static_cast<uint32_t>(page * a.h_kv + head) << (a.page_shift - 4)) +
            ((key & ((1 << a.page_shift) - 1)) >> 4);
   };
-  auto issue = [&](int i) {  // step i's tiles into the next stage
-    if (i < steps) {
-      const int j = i * kHalves;
-      if ((j & 31) == 0 && j > 0) {
+  auto issue = [&]() {  // the next step's tiles into the next stage
+    if (to_load > 0) {
+      if (next_tile == refill) {
         block = block_next;
-        block_next = block_of(j + 32 + lane);
+        refill += 32;
+        block_next = block_of(refill + lane);
       }
-      skipped &= ~(((1u << kHalves) - 1) << (fill * kHalves));
       uint32_t from[kHalves];
-      bool common = key1 - (first_key + i * kStride) >= kHalves * kTile;
+      bool common = to_load >= kHalves * kTile;
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        from[h] = __shfl_sync(0xffffffffu, block, (j + h) & 31);
+        from[h] = __shfl_sync(0xffffffffu, block, next_tile + h);  // of 32 lanes
         common = common && from[h] != kNoBlock;
       }
       if (common) {
@@ -513,9 +514,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
           const bool missing = from[h] == kNoBlock;
           if (missing) skipped |= 1u << (fill * kHalves + h);
           copy.template load<false>(fill_at + h * S::kTileBytes, missing ? 0u : from[h],
-                                    missing ? 0 : key1 - (first_key + i * kStride + h * kTile));
+                                    missing ? 0 : to_load - h * kTile);
         }
       }
+      to_load -= kStride;
+      next_tile += kHalves;
     }
     cp_async_commit();
     fill_at += S::kStageBytes;
@@ -534,11 +537,13 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     if (sg.fresh == 0) key1 = 0;
     // this warp's steps of kHalves tiles each, a stride apart
     first_key = key0 + warp * (kHalves * kTile);
-    steps = key1 > first_key ? (key1 - first_key + kStride - 1) / kStride : 0;
+    to_load = key1 - first_key;
+    next_tile = 0;
+    refill = 32;
     block = block_of(lane);
     block_next = block_of(32 + lane);
 #pragma unroll
-    for (int i = 0; i < S::kStages - 1; ++i) issue(i);
+    for (int i = 0; i < S::kStages - 1; ++i) issue();
   };
   begin(seg);
 
@@ -652,12 +657,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       // apart, as one chain of dependent products would be waited for
       constexpr bool kTwoChains = NT * kHalves == 1;
       float x[kHalves][NT][4];
+      if constexpr (!Q4) {
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) {
-        const uint32_t tile = at + h * S::kTileBytes;
-        float x2[NT][4];
-        if constexpr (!Q4) {
-          const uint32_t kat = tile + (lane & 15) * (2 * D);
+        for (int h = 0; h < kHalves; ++h) {
+          float x2[NT][4];
+          const uint32_t kat = at + h * S::kTileBytes + (lane & 15) * (2 * D);
           const uint32_t swz = (lane >> 4) ^ (lane & 7);
 #pragma unroll
           for (int s = 0; s < kSteps; ++s) {
@@ -671,30 +675,40 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
               else mma<false>(to, w[0], w[1], w[2], w[3], q.x, q.y);
             }
           }
-        } else {
-          constexpr int kWords = D / 32;  // of this thread's codes of one row
-          uint32_t w[2][kWords], sc[2];
+          if constexpr (kTwoChains) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) x[h][0][c] += x2[0][c];
+          }
+        }
+      } else {
+        constexpr int kWords = D / 32;  // of this thread's codes of one row
+        uint32_t w[kHalves][2][kWords], sc[kHalves][2];
+#pragma unroll
+        for (int h = 0; h < kHalves; ++h)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
+            const uint32_t tile = at + h * S::kTileBytes;
             const int row = row_lo + 8 * half;
             if constexpr (D == 128) {
               const uint4 v = lds128(tile + k_code_offset<D>(row, t * 16));
-              w[half][0] = v.x, w[half][1] = v.y, w[half][2] = v.z, w[half][3] = v.w;
-              sc[half] = scales_f16x2(lds16(tile + kTile * D + row * 8 + t * 2));
+              w[h][half][0] = v.x, w[h][half][1] = v.y, w[h][half][2] = v.z, w[h][half][3] = v.w;
+              sc[h][half] = scales_f16x2(lds16(tile + kTile * D + row * 8 + t * 2));
             } else {
               const uint2 v = lds64(tile + k_code_offset<D>(row, t * 8));
-              w[half][0] = v.x, w[half][1] = v.y;
-              sc[half] = scales_f16x2(lds8(tile + kTile * D + row * 4 + t));
+              w[h][half][0] = v.x, w[h][half][1] = v.y;
+              sc[h][half] = scales_f16x2(lds8(tile + kTile * D + row * 4 + t));
             }
           }
 #pragma unroll
-          for (int i4 = 0; i4 < kWords; ++i4) {
+        for (int i4 = 0; i4 < kWords; ++i4)
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
             uint32_t lo[4], hi[4];
-            codes_f16x2(w[0][i4], lo);
-            codes_f16x2(w[1][i4], hi);
+            codes_f16x2(w[h][0][i4], lo);
+            codes_f16x2(w[h][1][i4], hi);
             // d = 128: words 0, 1 are of the thread's first group, 2, 3 of its second
-            const uint32_t s0 = i4 < 2 ? twice<false>(sc[0]) : twice<true>(sc[0]);
-            const uint32_t s1 = i4 < 2 ? twice<false>(sc[1]) : twice<true>(sc[1]);
+            const uint32_t s0 = i4 < 2 ? twice<false>(sc[h][0]) : twice<true>(sc[h][0]);
+            const uint32_t s1 = i4 < 2 ? twice<false>(sc[h][1]) : twice<true>(sc[h][1]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               lo[c] = mul_f16x2(lo[c], s0);
@@ -705,15 +719,9 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
               const uint2 q0 = query(nt, 2 * i4), q1 = query(nt, 2 * i4 + 1);
               if (i4 == 0) mma_first<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
               else mma<true>(x[h][nt], lo[0], hi[0], lo[1], hi[1], q0.x, q0.y);
-              if (i4 == 0 && kTwoChains) mma_first<true>(x2[nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
-              else mma<true>(kTwoChains ? x2[nt] : x[h][nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
+              mma<true>(x[h][nt], lo[2], hi[2], lo[3], hi[3], q1.x, q1.y);
             }
           }
-        }
-        if constexpr (kTwoChains) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) x[h][0][c] += x2[0][c];
-        }
       }
 
       // ---- masks, in the sequence's last rows or where a page is missing;
@@ -721,6 +729,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       bool odd = false;
       if constexpr (kMasked) {
         const uint32_t missing = (skipped >> (stage * kHalves)) & ((1u << kHalves) - 1);
+        skipped &= ~(missing << (stage * kHalves));
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
           const int row = key + h * kTile + row_lo;
@@ -925,18 +934,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
         }
       }
     };
-    for (int i = 0; i < steps; ++i) {
+    const int tail = key1 + kHalves * kTile - hidden;  // closer to key1 than this: masks
+    for (int rest_rows = key1 - first_key; rest_rows > 0; rest_rows -= kStride) {
       cp_async_wait<S::kStages - 2>();
       __syncwarp();  // the other lanes' copies; and all have read the stage that is filled next
-      issue(i + S::kStages - 1);
-      const int key = first_key + i * kStride;
-      if (key + kHalves * kTile > hidden || ((skipped >> (stage * kHalves)) & ((1u << kHalves) - 1)) != 0)
-        step(std::true_type{}, key);
-      else
-        step(std::false_type{}, key);
+      issue();
+      if (rest_rows < tail || skipped != 0) step(std::true_type{}, key1 - rest_rows);
+      else step(std::false_type{}, 0);
       at += S::kStageBytes;
       if (++stage == S::kStages) stage = 0, at = ring;
     }
+
     // ---- what comes next, its first copies on their way before this segment
     // is finished where O has room beside them: in the stage left free
     const Segment done = s_seg;
@@ -1053,18 +1061,19 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 }
 
 // Joins the partial results of one query row of a pair that several blocks
-// worked on: a warp takes every fourth contribution, its lanes the columns.
-// It is a chain of three reads (who, m and l, O); a warp's first O is read
-// along with the second.
+// worked on: groups of D / 4 threads take every kGroups-th contribution, 16
+// bytes to a thread. It is a chain of three reads (who, m and l, O); a
+// group's first O is read along with the second.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const PagedArgs a,
                                                                           int tile_rows) {
   constexpr int kMergeWarps = kMergeThreads / 32;
-  constexpr int kCols = D / 32;
+  constexpr int kGroups = kMergeThreads / (D / 4);
   __shared__ float weight[kMaxBlocks];
-  __shared__ float part[kMergeWarps][D];
+  __shared__ float4 part[kGroups][D / 4];
   __shared__ float red[kMergeWarps], red_l[kMergeWarps];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
+  const int group = tid / (D / 4), col = tid % (D / 4);
   griddep_wait();  // the partials are complete
   griddep_launch_dependents();
   const int2 split = a.split[blockIdx.x];
@@ -1080,12 +1089,11 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   auto slot = [&](int i) {
     return (static_cast<int64_t>(2 * (first + i)) + (i == 0 ? 1 : 0)) * tile_rows + r;
   };
-  float o0[kCols], y[kCols];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) {
-    o0[c] = warp < n ? a.part_o[slot(warp) * D + c * 32 + lane] : 0.f;
-    y[c] = 0.f;
-  }
+  auto part_o = [&](int i) {
+    return *reinterpret_cast<const float4*>(a.part_o + slot(i) * D + 4 * col);
+  };
+  float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (group < n) y = part_o(group);
   float top = kLowest;
   for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, a.part_ml[slot(i)].x);
 #pragma unroll
@@ -1108,33 +1116,34 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   sum = 0.f;
 #pragma unroll
   for (int w = 0; w < kMergeWarps; ++w) sum += red_l[w];
-  if (warp < n) {
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) y[c] = weight[warp] * o0[c];
+  if (group < n) {
+    const float w = weight[group];
+    y.x *= w, y.y *= w, y.z *= w, y.w *= w;
   }
-#pragma unroll 4
-  for (int i = warp + kMergeWarps; i < n; i += kMergeWarps) {
+#pragma unroll 8
+  for (int i = group + kGroups; i < n; i += kGroups) {
     const float w = weight[i];
-    const float* o = a.part_o + slot(i) * D + lane;
-#pragma unroll
-    for (int c = 0; c < kCols; ++c) y[c] = fmaf(w, o[c * 32], y[c]);
+    const float4 o = part_o(i);
+    y.x = fmaf(w, o.x, y.x), y.y = fmaf(w, o.y, y.y);
+    y.z = fmaf(w, o.z, y.z), y.w = fmaf(w, o.w, y.w);
   }
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) part[warp][c * 32 + lane] = y[c];
+  part[group][col] = y;
   __syncthreads();
-  if (tid < D) {
-    float z = part[0][tid];
+  if (group == 0) {
 #pragma unroll
-    for (int w = 1; w < kMergeWarps; ++w) z += part[w][tid];
+    for (int g = 1; g < kGroups; ++g) {
+      const float4 o = part[g][col];
+      y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
+    }
     const Sequence seq = sequence(a, b);
     const bool real = (row0 + r) % a.n_q < seq.fresh;
     const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
     const int64_t row = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0 + r;
-    reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + tid] =
-        __float2bfloat16_rn(inv == 0.f ? 0.f : z * inv);
+    *reinterpret_cast<uint2*>(a.out + row * D + 4 * col) =
+        inv == 0.f ? make_uint2(0u, 0u)
+                   : make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
   }
 }
-static_assert(kMergeThreads >= 128, "a thread per column");
 
 // ------------------------------------------------------------------ launch
 
