@@ -67,7 +67,7 @@ constexpr int unsplit_rows(int tile_rows, int64_t pairs) {
 }
 constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
 constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 256;       // at most
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
 // Query rows of a block's tile: 8 per column block of the products.
@@ -1061,17 +1061,17 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 }
 
 // Joins the partial results of one query row of a pair that several blocks
-// worked on: groups of D / 4 threads take every kGroups-th contribution, 16
+// worked on: groups of D / 4 threads share the contributions, 16
 // bytes to a thread. It is a chain of three reads (who, m and l, O); a
 // group's first O is read along with the second.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const PagedArgs a,
                                                                           int tile_rows) {
-  constexpr int kMergeWarps = kMergeThreads / 32;
-  constexpr int kGroups = kMergeThreads / (D / 4);
+  constexpr int kMostGroups = kMergeThreads / (D / 4);
+  const int threads = static_cast<int>(blockDim.x), warps = threads / 32, groups = threads / (D / 4);
   __shared__ float weight[kMaxBlocks];
-  __shared__ float4 part[kGroups][D / 4];
-  __shared__ float red[kMergeWarps], red_l[kMergeWarps];
+  __shared__ float4 part[kMostGroups][D / 4];
+  __shared__ float red[kMergeThreads / 32], red_l[kMergeThreads / 32];
   const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
   const int group = tid / (D / 4), col = tid % (D / 4);
   griddep_wait();  // the partials are complete
@@ -1095,15 +1095,14 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
   if (group < n) y = part_o(group);
   float top = kLowest;
-  for (int i = tid; i < n; i += kMergeThreads) top = fmaxf(top, a.part_ml[slot(i)].x);
+  for (int i = tid; i < n; i += threads) top = fmaxf(top, a.part_ml[slot(i)].x);
 #pragma unroll
   for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
   if (lane == 0) red[warp] = top;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) top = fmaxf(top, red[w]);
+  for (int w = 0; w < warps; ++w) top = fmaxf(top, red[w]);
   float sum = 0.f;
-  for (int i = tid; i < n; i += kMergeThreads) {
+  for (int i = tid; i < n; i += threads) {
     const float2 ml = a.part_ml[slot(i)];
     const float w = ex2(ml.x - top);
     weight[i] = w;
@@ -1114,14 +1113,13 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   if (lane == 0) red_l[warp] = sum;
   __syncthreads();
   sum = 0.f;
-#pragma unroll
-  for (int w = 0; w < kMergeWarps; ++w) sum += red_l[w];
+  for (int w = 0; w < warps; ++w) sum += red_l[w];
   if (group < n) {
     const float w = weight[group];
     y.x *= w, y.y *= w, y.z *= w, y.w *= w;
   }
 #pragma unroll 8
-  for (int i = group + kGroups; i < n; i += kGroups) {
+  for (int i = group + groups; i < n; i += groups) {
     const float w = weight[i];
     const float4 o = part_o(i);
     y.x = fmaf(w, o.x, y.x), y.y = fmaf(w, o.y, y.y);
@@ -1130,8 +1128,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
   part[group][col] = y;
   __syncthreads();
   if (group == 0) {
-#pragma unroll
-    for (int g = 1; g < kGroups; ++g) {
+    for (int g = 1; g < groups; ++g) {
       const float4 o = part[g][col];
       y.x += o.x, y.y += o.y, y.z += o.z, y.w += o.w;
     }
@@ -1209,9 +1206,11 @@ cudaError_t launch_instance(PagedArgs a, const Layout& w, cudaStream_t stream) {
   e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, a);
   if (e != cudaSuccess || a.unsplit) return e;
   const unsigned rows = static_cast<unsigned>(a.rows < w.tile_rows ? a.rows : w.tile_rows);
+  // more threads to a row where a pair has many contributions on the average
+  const unsigned threads = pairs * 4 <= static_cast<int64_t>(blocks) ? kMergeThreads : 128;
   return launch_pdl(decode_paged_merge_kernel<D>,
                     dim3(a.by_pair ? static_cast<unsigned>(pairs) : blocks, rows),
-                    dim3(kMergeThreads), 0, stream, a, w.tile_rows);
+                    dim3(threads), 0, stream, a, w.tile_rows);
 }
 
 template <int D, bool Q4>
