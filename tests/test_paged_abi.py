@@ -39,6 +39,7 @@ COMMON = [
     (dict(page_size=24), INVALID),                               # not a power of two
     (dict(page_size=8), UNSUPPORTED), (dict(page_size=512), UNSUPPORTED),
     (dict(max_pages=(1 << 26) + 1), UNSUPPORTED),                # more than 2^30 rows
+    (dict(n_pages=(1 << 31) - 1, page_size=256, max_pages=1), UNSUPPORTED),  # 2^40 rows in the pool
     (dict(table=None), INVALID), (dict(table=FAKE + 2), INVALID), (dict(lens=FAKE + 1), INVALID),
     (dict(new=FAKE + 2), INVALID), (dict(q=FAKE + 8), INVALID),
     (dict(k_cache=None), INVALID), (dict(v_cache=None), INVALID), (dict(k_cache=FAKE + 4), INVALID),
@@ -55,6 +56,8 @@ ONLY_APPEND = [
     (dict(k_out=FAKE + 2), INVALID), (dict(B=40000, n=60000), INVALID),
 ]
 ONLY_DECODE = [
+    (dict(B=65535, h=65528, h_kv=8), INVALID),                   # 2^32 rows of queries
+    (dict(B=60000, h=4096, h_kv=4096, page_size=256, max_pages=1 << 22), UNSUPPORTED),  # 2^52 units
     (dict(n=0), INVALID), (dict(n=9), UNSUPPORTED), (dict(q=None), INVALID), (dict(out=None), INVALID),
     (dict(out=FAKE + 2), INVALID), (dict(mask=2), INVALID), (dict(mask=4), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(ws=None), INVALID),

@@ -304,6 +304,12 @@ DECODE_CASES = [
     (1, 8, 2, 1, 128, 16, [5003], None, True),                       # one long sequence, split
     (2, 4, 1, 2, 64, 64, [9001, 1], None, True),
     (300, 2, 1, 1, 64, 16, [b % 19 for b in range(300)], None, True),  # more sequences than threads
+    (70, 16, 8, 1, 64, 16, [(389 * b) % 1500 for b in range(70)], None, True),  # more pairs than blocks
+    (400, 2, 2, 2, 128, 32, [5000] + [(7 * b) % 60 for b in range(399)], None, True),  # one long among short
+    (1000, 1, 1, 1, 64, 64, [(b * b) % 97 for b in range(999)] + [2500], None, False),
+    (3, 8, 8, 1, 128, 16, [1280, 1290, 4], None, True),              # just too long to be left whole
+    (3, 8, 8, 1, 128, 16, [1264, 1250, 4], None, True),              # just short enough
+    (33, 12, 4, 8, 64, 16, [(211 * b) % 2100 for b in range(33)], [b % 9 for b in range(33)], True),
 ]
 decode_ids = lambda c: "B{}h{}kv{}q{}d{}p{}x{}".format(*c[:6], max(c[6]))
 
@@ -483,6 +489,50 @@ def test_decode_repeats_to_the_bit_and_on_other_streams(tsd, q4):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o.view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("q4", [False, True], ids=["bf16", "q4"])
+def test_pools_past_32_bit_offsets(tsd, q4):
+    """Pages whose elements lie past 2^32 (bf16) and 2^31 (4-bit codes) from the pool's start:
+    the decoding step over them equals that over a small pool, and the append reaches them."""
+    import torch
+    h_kv, d, page, n_pages = 8, 128, 256, 20000 if q4 else 17000
+    small = DecodeCase((2, 16, h_kv, 1, d, page, [700, 300], None, True), q4, seed=31)
+    want = small.run(tsd)
+    torch.cuda.synchronize()
+    places = [n_pages - 1, 3, n_pages - 2, n_pages // 2 + 1, 0, n_pages - 7, n_pages - 9]
+    used = sorted(set(int(x) for x in small.table.ravel() if x >= 0))
+    move = {old: places[i] for i, old in enumerate(used)}
+    big = []
+    for pool in small.pools:
+        t = torch.empty((n_pages,) + tuple(pool.shape[1:]), dtype=pool.dtype, device="cuda")
+        for old, new in move.items():
+            t[new].copy_(pool[old])
+        big.append(t)
+    assert big[0].numel() > (1 << 31 if q4 else 1 << 32)
+    table = np.vectorize(lambda x: move.get(int(x), -1))(small.table).astype(np.int32)
+    small.n_pages = n_pages
+    got = small.run(tsd, pools=big, table=to_dev_i32(table))
+    torch.cuda.synchronize()
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+    # three new tokens on the last page
+    x = torch.randn(1, 3, 3 * h_kv, d, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    x = x.to(torch.bfloat16)
+    tab, lens = to_dev_i32([[n_pages - 1]]), to_dev_i32([200])
+    little = [torch.zeros((1,) + tuple(p.shape[1:]), dtype=p.dtype, device="cuda") for p in big]
+    st = (9 * h_kv * d, d, 3 * h_kv * d)
+    for pools, table, n in ((little, to_dev_i32([[0]]), 1), (big, tab, n_pages)):
+        args = (x, *st, x[:, :, h_kv:], x[:, :, 2 * h_kv:], *st, torch.empty(1, h_kv, 3, d, dtype=x.dtype, device="cuda"),
+                None, *pools)
+        rest = (table, lens, None, None, 0, 0, 0, 1, h_kv, h_kv, 3, d, n, page, 1)
+        if q4:
+            tsd.attn_cache_append_q4(*args, 0.01, 0.01, *rest)
+        else:
+            tsd.attn_cache_append(*args, *rest)
+    torch.cuda.synchronize()
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+    for a, b in zip(little, big):
+        assert torch.equal(a[0, :, 197:200].view(torch.uint8), b[n_pages - 1, :, 197:200].view(torch.uint8))
 
 
 # ------------------------------------------------------------------ together
