@@ -65,8 +65,10 @@ constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
 constexpr int unsplit_rows(int tile_rows, int64_t pairs) {
   return tile_rows > 16 && pairs < 24 ? 512 : 1280;
 }
-constexpr int kPairUnits = 6;            // what starting and ending a pair costs, in units
-constexpr int kMaxBlocks = 1216;         // 8 blocks on each of 152 SMs
+// What starting and ending a pair costs, in units (48 sequences of up to 16384
+// rows in 4 bits: 117 us with 1, 116 with 2, 114 with 4, 109 with 6, 109 with 8).
+constexpr int kPairUnits = 6;
+constexpr int kMaxBlocks = 608;          // 4 blocks on each of 152 SMs, more than fit
 constexpr int kMergeThreads = 256;       // at most
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
@@ -116,7 +118,8 @@ struct Shape {
   // a warp's part of O fits into one stage of its ring
   static constexpr bool kAhead = kRows * kPitch * 4 <= kStageBytes;
   static constexpr int kSmem = kAhead || kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
-  // blocks that share an SM; more of them with fewer registers each were slower
+  // blocks that share an SM: the registers that leaves each thread. A fourth
+  // of a 4-bit cache's spills: 103 us in place of 96 (the batch above).
   static constexpr int kMinBlocks = NT > 1 ? 1 : (Q4 || D == 64 ? 3 : 2);
 };
 
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
   const int32_t* table = nullptr;
   int to_load = 0;             // rows from the next step to load to key1, less than 1: none
   int next_tile = 0, refill = 0;  // the next tile to load; where block runs out
-  uint32_t block, block_next;  // of the steps' tiles, 32 at a time, one per lane
+  uint32_t block = 0, block_next = 0;  // of the steps' tiles, 32 at a time, one per lane
   uint32_t skipped = 0;        // bit kHalves s + h: tile h of stage s has no page
   int fill = 0, stage = 0;     // the stages that are filled and read next
   uint32_t fill_at = ring, at = ring;
@@ -487,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       atomicOr(&g_device_error, kErrIndex);
       return kNoBlock;
     }
-    return (static_cast<uint32_t>(page * a.h_kv + head) << (a.page_shift - 4)) +
+    return ((static_cast<uint32_t>(page) * a.h_kv + head) << (a.page_shift - 4)) +
            ((key & ((1 << a.page_shift) - 1)) >> 4);
   };
   auto issue = [&]() {  // the next step's tiles into the next stage
@@ -655,12 +658,12 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 
       // ---- S^T = K Q^T; for one column block of one tile even and odd steps
       // apart, as one chain of dependent products would be waited for
-      constexpr bool kTwoChains = NT * kHalves == 1;
+      [[maybe_unused]] constexpr bool kTwoChains = NT * kHalves == 1;
       float x[kHalves][NT][4];
       if constexpr (!Q4) {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
-          float x2[NT][4];
+          [[maybe_unused]] float x2[NT][4];
           const uint32_t kat = at + h * S::kTileBytes + (lane & 15) * (2 * D);
           const uint32_t swz = (lane >> 4) ^ (lane & 7);
 #pragma unroll
@@ -760,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 
       // ---- 4-bit: V's codes and scales on their way while the softmax is done.
       // [tile][rows' half][cached rows r0, r1][word]
-      uint32_t v_codes[kHalves][2][2][D / 64], v_scale[kHalves][2];
+      [[maybe_unused]] uint32_t v_codes[kHalves][2][2][D / 64], v_scale[kHalves][2];
       if constexpr (Q4) {
 #pragma unroll
         for (int h = 0; h < kHalves; ++h) {
@@ -831,7 +834,8 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       }
 
       // ---- p, its sum, and P^T as the second product's operand
-      uint32_t p_hi[kHalves][NT][2], p_lo[kHalves][NT][2];
+      uint32_t p_hi[kHalves][NT][2];
+      [[maybe_unused]] uint32_t p_lo[kHalves][NT][2];  // bf16 only
 #pragma unroll
       for (int h = 0; h < kHalves; ++h)
 #pragma unroll
@@ -859,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
       // of cached rows r0 and r1, registers 2 and 3 of the rows 8 further
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) {
-        const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
+        [[maybe_unused]] const uint32_t vat = at + h * S::kTileBytes + kTile * S::kRowBytes;
         // the operand of kBlock blocks of 16 columns from block s0 on
         constexpr int kBlock = Q4 ? 4 : 1;
         auto v_operand = [&](int s0, uint32_t (&va)[kBlock][4]) {
