@@ -59,12 +59,8 @@ constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
 // Caches of at most this many rows are not split: a block takes each pair
 // whole and no merge is launched. 7 sequences of 900 rows at 32 query and 8
 // key heads of 128: 10.3 us against 11.4, 4-bit 10.4 against 14.5; of 300
-// rows 6.1 against 9.9. The wide tiles of 28 query rows take longer for a row:
-// 2 sequences of 900 rows at 4 key heads 17.6 us against 13.5 in 4 bits, but
-// 7 of them 17.7 against 19.8.
-constexpr int unsplit_rows(int tile_rows, int64_t pairs) {
-  return tile_rows > 16 && pairs < 24 ? 512 : 1280;
-}
+// rows 6.1 against 9.9.
+constexpr int64_t kUnsplitRows = 1280;
 // What starting and ending a pair costs, in units (48 sequences of up to 16384
 // rows in 4 bits: 117 us with 1, 116 with 2, 114 with 4, 109 with 6, 109 with 8).
 constexpr int kPairUnits = 6;
@@ -72,8 +68,22 @@ constexpr int kMaxBlocks = 608;          // 4 blocks on each of 152 SMs, more th
 constexpr int kMergeThreads = 256;       // at most
 constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
-// Query rows of a block's tile: 8 per column block of the products.
-int column_blocks(int rows) { return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4); }
+// Query rows of a block's tile, 8, 16 or 32. A wide tile reads the cache once
+// for all of its rows; a narrow one is done sooner, and its blocks share the
+// cache's rows through L2. With 28 query rows to a key head (d = 128, bf16):
+// unsplit, 1000 rows, 12 pairs 10.8, 13.6 and 19.2 us; 64 pairs 14.6, 14.9
+// and 19.7; 160 pairs 37.2, 30.5 and 27.2. Split, 2500 rows, 40 pairs 23.4,
+// 21.4 and 24.9 us; 5000 rows, 28 pairs 26.9, 23.2 and 24.8; 4000 rows, 128
+// pairs 99, 60 and 49.
+int tile_rows(int rows, int64_t pairs, int64_t capacity) {
+  auto tiles = [&](int tile) { return pairs * ((rows + tile - 1) / tile); };
+  if (rows <= 8) return 8;
+  if (capacity <= kUnsplitRows) {
+    if (tiles(8) <= 200) return 8;
+    return rows <= 16 || tiles(16) <= 304 ? 16 : 32;
+  }
+  return rows <= 16 || pairs * (capacity / kUnit) <= 4096 ? 16 : 32;
+}
 
 struct PagedArgs {
   const uint16_t* q;
@@ -1158,7 +1168,7 @@ struct Layout {
 Layout layout(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pages) {
   Layout w;
   const int rows = h / h_kv * n_q;
-  w.tile_rows = 8 * column_blocks(rows);
+  w.tile_rows = tile_rows(rows, int64_t(B) * h_kv, int64_t(max_pages) * page_size);
   w.row_tiles = (rows + w.tile_rows - 1) / w.tile_rows;
   const int64_t per_pair = 1 + (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
   w.units = int64_t(B) * h_kv * w.row_tiles * per_pair;
@@ -1262,8 +1272,7 @@ cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream
   a.n_pages = c.n_pages;
   a.page_shift = c.page_shift;
   a.max_pages = c.max_pages;
-  a.unsplit = (c.max_pages << c.page_shift) <=
-              unsplit_rows(w.tile_rows, int64_t(p.B) * c.h_kv * w.row_tiles);
+  a.unsplit = (int64_t(c.max_pages) << c.page_shift) <= kUnsplitRows;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f * (q4 ? c.k_factor : 1.f);
   a.v_factor = q4 ? c.v_factor : 1.f;
