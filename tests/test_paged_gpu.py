@@ -309,7 +309,13 @@ DECODE_CASES = [
     (1000, 1, 1, 1, 64, 64, [(b * b) % 97 for b in range(999)] + [2500], None, False),
     (3, 8, 8, 1, 128, 16, [1280, 1290, 4], None, True),              # just too long to be left whole
     (3, 8, 8, 1, 128, 16, [1264, 1250, 4], None, True),              # just short enough
+    # wide query tiles (16 and 32 rows), whole and split, of both head sizes
     (33, 12, 4, 8, 64, 16, [(211 * b) % 2100 for b in range(33)], [b % 9 for b in range(33)], True),
+    (3, 12, 4, 4, 128, 16, [1400, 5, 2000], None, True),
+    (40, 28, 4, 4, 128, 32, [(97 * b) % 300 for b in range(40)], None, True),
+    (42, 28, 4, 4, 128, 16, [(411 * b) % 1700 for b in range(42)], [4 - b % 5 for b in range(42)], True),
+    (60, 18, 1, 2, 64, 16, [(31 * b) % 200 for b in range(60)], None, False),
+    (5, 36, 2, 2, 64, 16, [1, 1500, 33, 700, 64], None, False),
 ]
 decode_ids = lambda c: "B{}h{}kv{}q{}d{}p{}x{}".format(*c[:6], max(c[6]))
 
@@ -420,11 +426,18 @@ def test_decode_queries_of_any_size(tsd, d):
 
 
 @pytest.mark.parametrize("q4", [False, True], ids=["bf16", "q4"])
-@pytest.mark.parametrize("n_q,new", [(4, [4, 2]), (8, [8, 5])])
-def test_rows_that_a_query_does_not_see_do_not_reach_it(tsd, q4, n_q, new):
+@pytest.mark.parametrize("case", [
+    (2, 8, 4, 4, 64, 16, [37, 90], [4, 2], True),
+    (2, 8, 4, 8, 128, 16, [37, 90], [8, 5], True),
+    (2, 8, 4, 8, 64, 16, [37, 1500], [8, 5], True),                        # 16 query rows to a tile
+    (2, 8, 4, 8, 128, 16, [37, 1500], [7, 8], True),
+    (80, 14, 2, 4, 64, 16, [9 + b for b in range(80)], [1 + b % 4 for b in range(80)], True),   # 32
+    (80, 14, 2, 4, 128, 16, [9 + b for b in range(80)], [1 + b % 4 for b in range(80)], True),
+], ids=decode_ids)
+def test_rows_that_a_query_does_not_see_do_not_reach_it(tsd, q4, case):
     """Infinities and NaN in a later token's key and value: earlier tokens' outputs are as
     without them; the token that sees them has no finite output to compare."""
-    case = (2, 8, 4, n_q, 64, 16, [37, 90], new, True)
+    new = case[7]
     c = DecodeCase(case, q4, seed=4)
     pools = [p.clone() for p in c.pools]
     for b, L in enumerate(case[6]):
@@ -438,7 +451,7 @@ def test_rows_that_a_query_does_not_see_do_not_reach_it(tsd, q4, n_q, new):
             pools[1][at, :, slot, 6] = float("nan")
     got = to_host_f64(c.run(tsd, pools=pools))
     clean = to_host_f64(c.run(tsd))
-    for b in range(2):
+    for b in range(case[0]):
         m = new[b]
         assert np.array_equal(got[b, :, :m - 1], clean[b, :, :m - 1])
         assert not np.any(np.isfinite(got[b, :, m - 1]).all(-1))
