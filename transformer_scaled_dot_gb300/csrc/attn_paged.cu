@@ -52,15 +52,18 @@ namespace tsd {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;                // cached rows of a product, within one page
-constexpr int kUnit = kWarps * kTile;    // cached rows of a unit of work
+constexpr int kTile = 16;  // cached rows of a product, within one page
+constexpr int kUnit = 64;  // cached rows of a unit of work: a tile for each of four warps
 // Caches of at most this many rows are not split: a block takes each pair
 // whole and no merge is launched. 7 sequences of 900 rows at 32 query and 8
 // key heads of 128: 10.3 us against 11.4, 4-bit 10.4 against 14.5; of 300
 // rows 6.1 against 9.9.
 constexpr int64_t kUnsplitRows = 1280;
+// Where there is an SM for every pair too, a block of eight warps is done with
+// more than 256 rows sooner (3 sequences of 1100 rows, 8 key heads of 128: 9.4
+// us in place of 11.3; of 100 rows 4.6 in place of 4.3, of 1900 rows 12.6, and
+// split 11.6).
+constexpr int64_t kAlone = 152, kFewRows = 256;
 // What starting and ending a pair costs, in units (48 sequences of up to 16384
 // rows in 4 bits: 117 us with 1, 116 with 2, 114 with 4, 109 with 6, 109 with 8).
 constexpr int kPairUnits = 6;
@@ -75,14 +78,18 @@ constexpr float kLowest = -3.4028234e38f;  // m before the first row
 // and 19.7; 160 pairs 37.2, 30.5 and 27.2. Split, 2500 rows, 40 pairs 23.4,
 // 21.4 and 24.9 us; 5000 rows, 28 pairs 26.9, 23.2 and 24.8; 4000 rows, 128
 // pairs 99, 60 and 49.
-int tile_rows(int rows, int64_t pairs, int64_t capacity) {
+struct Plan {
+  int tile_rows;
+  bool unsplit, eight_warps;
+};
+Plan plan(int rows, int64_t pairs, int64_t capacity) {
   auto tiles = [&](int tile) { return pairs * ((rows + tile - 1) / tile); };
-  if (rows <= 8) return 8;
-  if (capacity <= kUnsplitRows) {
-    if (tiles(8) <= 200) return 8;
-    return rows <= 16 || tiles(16) <= 304 ? 16 : 32;
-  }
-  return rows <= 16 || pairs * (capacity / kUnit) <= 4096 ? 16 : 32;
+  const bool unsplit = capacity <= kUnsplitRows;
+  if (unsplit && tiles(8) <= kAlone) return {8, true, capacity > kFewRows};
+  if (rows <= 8 || (unsplit && tiles(8) <= 200)) return {8, unsplit, false};
+  if (rows <= 16 || (unsplit ? tiles(16) <= 304 : pairs * (capacity / kUnit) <= 4096))
+    return {16, unsplit, false};
+  return {32, unsplit, false};
 }
 
 struct PagedArgs {
@@ -109,8 +116,9 @@ struct PagedArgs {
   float v_factor;
 };
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, int W>
 struct Shape {
+  static constexpr int kWarps = W, kThreads = 32 * W;
   static constexpr int kRows = 8 * NT;
   static constexpr int kRowBytes = Q4 ? D / 2 : 2 * D;
   static constexpr int kScaleBytes = Q4 ? D / 16 : 0;
@@ -130,7 +138,7 @@ struct Shape {
   static constexpr int kSmem = kAhead || kRingBytes > kMergeBytes ? kRingBytes : kMergeBytes;
   // blocks that share an SM: the registers that leaves each thread. A fourth
   // of a 4-bit cache's spills: 103 us in place of 96 (the batch above).
-  static constexpr int kMinBlocks = NT > 1 ? 1 : (Q4 || D == 64 ? 3 : 2);
+  static constexpr int kMinBlocks = NT > 1 || W > 4 ? 1 : (Q4 || D == 64 ? 3 : 2);
 };
 
 // ------------------------------------------------------------------ instructions
@@ -382,10 +390,11 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t y) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int D, int NT, bool Q4>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
+template <int D, int NT, bool Q4, int W>
+__global__ void __launch_bounds__(32 * W, Shape<D, NT, Q4, W>::kMinBlocks)
     decode_paged_kernel(const PagedArgs a) {
-  using S = Shape<D, NT, Q4>;
+  using S = Shape<D, NT, Q4, W>;
+  constexpr int kWarps = S::kWarps, kThreads = S::kThreads;
   constexpr int kSteps = D / 16;  // products of S, and blocks of 16 columns of O
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps][S::kRows];
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
 
   const uint32_t ring = smem_u32(smem) + warp * (S::kStages * S::kStageBytes);
   const TileCopy<D, Q4> copy(a, lane);
-  constexpr int kHalves = S::kHalves, kStride = kHalves * kUnit;
+  constexpr int kHalves = S::kHalves, kStride = kHalves * kWarps * kTile;
   constexpr uint32_t kNoBlock = 0xffffffffu;
 
   // the part of a segment that this warp's copies go by
@@ -989,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, NT, Q4>::kMinBlocks)
     }
     if (!S::kAhead || !more) cp_async_wait<0>();
 
-    // ---- the four warps' results of these units, joined in shared memory
+    // ---- the warps' results of these units, joined in shared memory
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1160,6 +1169,7 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
 
 struct Layout {
   int row_tiles, tile_rows;
+  bool unsplit, eight_warps;
   int64_t units;          // at most
   int blocks;             // at most
   size_t ml_off, o_off, total;
@@ -1168,7 +1178,10 @@ struct Layout {
 Layout layout(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pages) {
   Layout w;
   const int rows = h / h_kv * n_q;
-  w.tile_rows = tile_rows(rows, int64_t(B) * h_kv, int64_t(max_pages) * page_size);
+  const Plan p = plan(rows, int64_t(B) * h_kv, int64_t(max_pages) * page_size);
+  w.tile_rows = p.tile_rows;
+  w.unsplit = p.unsplit;
+  w.eight_warps = p.eight_warps;
   w.row_tiles = (rows + w.tile_rows - 1) / w.tile_rows;
   const int64_t per_pair = 1 + (int64_t(max_pages) * page_size + kUnit - 1) / kUnit;
   w.units = int64_t(B) * h_kv * w.row_tiles * per_pair;
@@ -1183,7 +1196,7 @@ Layout layout(int B, int h, int h_kv, int n_q, int d, int page_size, int max_pag
 
 // Blocks of this instance that fit on the current device at once (cached per device).
 template <typename Kernel>
-cudaError_t resident_blocks(Kernel kernel, int smem, int* cache, int* out) {
+cudaError_t resident_blocks(Kernel kernel, int threads, int smem, int* cache, int* out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1192,7 +1205,7 @@ cudaError_t resident_blocks(Kernel kernel, int smem, int* cache, int* out) {
     int sms = 0, per_sm = 0;
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, smem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem);
     if (e != cudaSuccess) return e;
     if (sms < 1 || per_sm < 1) return cudaErrorInvalidConfiguration;
     n = sms * per_sm;
@@ -1202,22 +1215,22 @@ cudaError_t resident_blocks(Kernel kernel, int smem, int* cache, int* out) {
   return cudaSuccess;
 }
 
-template <int D, int NT, bool Q4>
+template <int D, int NT, bool Q4, int W>
 cudaError_t launch_instance(PagedArgs a, const Layout& w, cudaStream_t stream) {
-  auto kernel = decode_paged_kernel<D, NT, Q4>;
-  constexpr int smem = Shape<D, NT, Q4>::kSmem;
+  auto kernel = decode_paged_kernel<D, NT, Q4, W>;
+  constexpr int smem = Shape<D, NT, Q4, W>::kSmem;
   static unsigned long long configured = 0;
   static int resident[64] = {};
   cudaError_t e = set_smem_once(kernel, smem, &configured);
   int fit = 0;
-  if (e == cudaSuccess) e = resident_blocks(kernel, smem, resident, &fit);
+  if (e == cudaSuccess) e = resident_blocks(kernel, 32 * W, smem, resident, &fit);
   if (e != cudaSuccess) return e;
   const unsigned blocks = static_cast<unsigned>(fit < w.blocks ? fit : w.blocks);
   // few pairs: look at each for what has to be joined; many: at the blocks,
   // each of which begins at most one that others finish
   const int64_t pairs = int64_t(a.B) * a.h_kv * a.row_tiles;
   a.by_pair = pairs <= static_cast<int64_t>(blocks);
-  e = launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, stream, a);
+  e = launch_pdl(kernel, dim3(blocks), dim3(32 * W), smem, stream, a);
   if (e != cudaSuccess || a.unsplit) return e;
   const unsigned rows = static_cast<unsigned>(a.rows < w.tile_rows ? a.rows : w.tile_rows);
   // more threads to a row where a pair has many contributions on the average
@@ -1229,9 +1242,10 @@ cudaError_t launch_instance(PagedArgs a, const Layout& w, cudaStream_t stream) {
 
 template <int D, bool Q4>
 cudaError_t launch_rows(const PagedArgs& a, const Layout& w, cudaStream_t stream) {
-  if (w.tile_rows == 8) return launch_instance<D, 1, Q4>(a, w, stream);
-  if (w.tile_rows == 16) return launch_instance<D, 2, Q4>(a, w, stream);
-  return launch_instance<D, 4, Q4>(a, w, stream);
+  if (w.eight_warps) return launch_instance<D, 1, Q4, 8>(a, w, stream);
+  if (w.tile_rows == 8) return launch_instance<D, 1, Q4, 4>(a, w, stream);
+  if (w.tile_rows == 16) return launch_instance<D, 2, Q4, 4>(a, w, stream);
+  return launch_instance<D, 4, Q4, 4>(a, w, stream);
 }
 
 }  // namespace
@@ -1272,7 +1286,7 @@ cudaError_t launch_decode_paged(const PagedDecodeProblem& p, cudaStream_t stream
   a.n_pages = c.n_pages;
   a.page_shift = c.page_shift;
   a.max_pages = c.max_pages;
-  a.unsplit = (int64_t(c.max_pages) << c.page_shift) <= kUnsplitRows;
+  a.unsplit = w.unsplit;
   a.causal = p.causal;
   a.scale_log2 = p.scale * 1.4426950408889634f * (q4 ? c.k_factor : 1.f);
   a.v_factor = q4 ? c.v_factor : 1.f;
