@@ -285,6 +285,25 @@ def test_append_in_place_and_without_queries(tsd):
     assert tsd.attn_get_device_status() == tsd.ATTN_OK
 
 
+def test_append_of_almost_only_padding(tsd):
+    """The largest n_new: three tokens and 2^31 - 4 that are padding, which is never read."""
+    import torch
+    n, d, page, h_kv = 2 ** 31 - 1, 64, 16, 2
+    rng = np.random.default_rng(17)
+    bits, x = bf16(rng, 2, 3, h_kv, d)
+    k, v = to_dev_bf16(bits)
+    pools = [torch.zeros(2, h_kv, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    tsd.attn_cache_append(None, 0, 0, 0, k, v, 0, d, h_kv * d, None, None, *pools,
+                          to_dev_i32([[1, 0]]), to_dev_i32([17]), to_dev_i32([3]), None, 0, 0, 0,
+                          1, h_kv, h_kv, n, d, 2, page, 2)
+    torch.cuda.synchronize()
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+    for pool, rows in zip(pools, x):
+        want = np.zeros((2, h_kv, page, d))
+        want[1, :, 14], want[1, :, 15], want[0, :, 0] = rows  # positions 14, 15 and 16
+        assert np.array_equal(to_host_f64(pool), want)
+
+
 # ------------------------------------------------------------------ decode
 
 DECODE_CASES = [

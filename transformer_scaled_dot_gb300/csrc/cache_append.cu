@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kItems == 1 ? 512 : 256, kItems == 1 ? 1 : 3)
   constexpr int kLanes = D / 16;  // threads of a row
   griddep_wait();  // inputs, lengths and tables may come from the previous kernel
   griddep_launch_dependents();
-  const int groups = (p.n_new + span - 1) / span;
+  const int groups = (p.n_new - 1) / span + 1;  // n_new + span may pass 32 bits
   const int b = static_cast<int>(blockIdx.x) / groups;
   const int t0 = static_cast<int>(blockIdx.x) % groups * span;
   const PagedCache& c = p.cache;
@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(kItems == 1 ? 512 : 256, kItems == 1 ? 1 : 3)
   const int64_t start = static_cast<int64_t>(len) - m;  // token t's position is start + t
   const int64_t places = static_cast<int64_t>(c.max_pages) << c.page_shift;
   const int64_t known = p.rope_kind != 0 ? min(places, static_cast<int64_t>(p.rope_rows)) : places;
-  int t1 = min(t0 + span, m);
-  if (t1 <= t0) return;
+  if (m <= t0) return;
+  int t1 = m - t0 < span ? m : t0 + span;
   if (start + t1 > known) {
     if (threadIdx.x == 0) atomicOr(&g_device_error, kErrIndex);
     t1 = static_cast<int>(max(known - start, static_cast<int64_t>(t0)));
@@ -283,7 +283,7 @@ cudaError_t launch_items(const AppendProblem& p, int span, cudaStream_t stream) 
   const int rows = (p.q ? p.h : 0) + 2 * p.cache.h_kv;
   const int64_t wanted = (int64_t(rows) * (D / 16) + kItems - 1) / kItems;
   const unsigned threads = wanted >= kMost ? kMost : static_cast<unsigned>((wanted + 31) / 32 * 32);
-  const int64_t groups = (p.n_new + span - 1) / span;
+  const int64_t groups = (p.n_new - 1) / span + 1;
   return launch_pdl(cache_append_kernel<D, Q4, kItems>, dim3(static_cast<unsigned>(p.B * groups)),
                     dim3(threads), 0, stream, p, span);
 }
