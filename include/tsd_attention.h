@@ -579,7 +579,8 @@ attn_status attn_cache_append_q4(const void *q, int64_t q_sb, int64_t q_sh, int6
  *       the cache already). ATTN_MASK_NONE: every query sees all cache_lens[b]
  *       rows (cross-attention to encoder states kept in a cache). Others ->
  *       ATTN_ERR_INVALID
- *   scale       0 -> 1/sqrt(d)
+ *   scale       0 -> 1/sqrt(d); scale log2(e), with a 4-bit cache's k_factor, has
+ *       to be finite in fp32, else ATTN_ERR_INVALID
  *   workspace   device, 16-byte aligned, >= attn_decode_paged_workspace_bytes(...)
  *       bytes of scratch (0 for sizes that the call refuses)
  * Rows of `out` that see no row, padding tokens' among them, are 0. Rows at

@@ -62,15 +62,22 @@ ONLY_DECODE = [
     (dict(out=FAKE + 2), INVALID), (dict(mask=2), INVALID), (dict(mask=4), INVALID),
     (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(ws=None), INVALID),
     (dict(ws=FAKE + 8), INVALID), (dict(ws_bytes=0), INVALID), (dict(h=0), OK),
+    (dict(scale=3e38), INVALID),                                 # times log2(e): infinite
+    (dict(scale=2e38, h=0), OK),
 ]
 ONLY_Q4 = [
     (dict(k_scales=None), INVALID), (dict(v_scales=FAKE + 2), INVALID), (dict(k_factor=0.0), INVALID),
     (dict(v_factor=-1.0), INVALID), (dict(v_factor=float("inf")), INVALID),
     (dict(k_factor=float("nan")), INVALID), (dict(k_factor=1e-38), INVALID),
 ]
+ONLY_DECODE_Q4 = [
+    (dict(scale=1e10, k_factor=2.0 ** 100), INVALID),            # their product is infinite
+    (dict(scale=1e8, k_factor=2.0 ** 100, h=0), OK),
+]
 CASES = [(name, change, expect) for name in CALLS
          for change, expect in COMMON + (ONLY_APPEND if "append" in name else ONLY_DECODE) +
-         (ONLY_Q4 if "q4" in name else [])]
+         (ONLY_Q4 if "q4" in name else []) +
+         (ONLY_DECODE_Q4 if name == "attn_decode_paged_q4" else [])]
 
 
 @pytest.fixture(scope="module")

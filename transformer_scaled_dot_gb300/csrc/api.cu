@@ -710,6 +710,9 @@ attn_status run_decode_paged(const void* q, const void* k_cache, const void* k_s
   if (s != ATTN_OK) return s;
   if (mask_kind != ATTN_MASK_NONE && mask_kind != ATTN_MASK_CAUSAL) return ATTN_ERR_INVALID;
   if (!valid_scale(scale)) return ATTN_ERR_INVALID;
+  // the factor of the logits to base 2: 0 times an infinite one would be no number
+  if (!std::isfinite(resolve_scale(scale, d) * 1.4426950408889634f * (q4 ? k_factor : 1.f)))
+    return ATTN_ERR_INVALID;
   for (const void* p : {q, static_cast<const void*>(out), static_cast<const void*>(workspace)})
     if (p == nullptr || !aligned16(p)) return ATTN_ERR_INVALID;
   s = pool_check(k_cache, v_cache, k_scales, v_scales, q4, k_factor, v_factor);
