@@ -491,6 +491,23 @@ def test_decode_leaves_out_rows_without_a_page(tsd, q4):
     c.check(tsd, out, [k[:, i] for k, i in zip(c.k_rows, keep)], [v[:, i] for v, i in zip(c.v_rows, keep)])
 
 
+@pytest.mark.parametrize("lens", [[200, 200, 150], [1500, 1500, 1490]], ids=["whole", "split"])
+@pytest.mark.parametrize("q4", [False, True], ids=["bf16", "q4"])
+def test_sequences_that_share_pages(tsd, q4, lens):
+    """A common beginning held once: the same page in several tables, and twice in one."""
+    c = DecodeCase((3, 8, 2, 2, 64, 16, lens, None, True), q4, seed=31)
+    table = c.table.copy()
+    table[1, :-4], table[2, :8] = table[0, :-4], table[0, 0]
+    c.k_rows, c.v_rows = list(c.k_rows), list(c.v_rows)
+    for rows in (c.k_rows, c.v_rows):
+        last = (lens[1] + 15) // 16
+        shared = min(table.shape[1] - 4, last) * 16
+        rows[1] = np.concatenate([rows[0][:, :shared], rows[1][:, shared:]], 1)
+        rows[2] = np.concatenate([np.tile(rows[0][:, :16], (1, 8, 1)), rows[2][:, 128:]], 1)
+    c.check(tsd, c.run(tsd, table=to_dev_i32(table)))
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+
+
 @pytest.mark.parametrize("q4", [False, True], ids=["bf16", "q4"])
 def test_decode_clamps_lengths(tsd, q4):
     """Lengths past the page table count as its rows; no lengths: all of them; negative: none."""
