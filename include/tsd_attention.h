@@ -584,8 +584,9 @@ attn_status attn_cache_append_q4(const void *q, int64_t q_sb, int64_t q_sh, int6
  *   workspace   device, 16-byte aligned, >= attn_decode_paged_workspace_bytes(...)
  *       bytes of scratch (0 for sizes that the call refuses)
  * Rows of `out` that see no row, padding tokens' among them, are 0. Rows at
- * or past cache_lens[b] are never used, whatever they hold. Errors as
- * attn_decode.
+ * or past cache_lens[b] are never used, whatever they hold. An infinity in a
+ * value that a query sees is one in its output (a NaN if the row's weight is
+ * below fp32's range, or both infinities meet). Errors as attn_decode.
  */
 size_t attn_decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
                                          int max_pages);

@@ -1,0 +1,69 @@
+"""GPU tests of the paged cache at the ends of its numbers' ranges: infinite and
+very large values, very large and very small queries and factors. The cases and
+their 64-bit definitions are test_paged_gpu's and paged_util's."""
+import numpy as np
+import pytest
+
+import synthetic
+
+import paged_util as pu
+from gpu_util import to_dev_bf16, to_host_f64
+from test_paged_gpu import DecodeCase, dev, tsd  # noqa: F401 (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def set_rows(c, pool, b, position, column, value):
+    """One column of one cached row, of every key head, in a copy of a bf16 pool."""
+    page = c.case[5]
+    pool[int(c.table[b, position // page]), :, position % page, column] = value
+
+
+INFINITE_CASES = [
+    # B, h, h_kv, n_q, d, page, lens, new_lens or None, causal; the positions are counted from the end
+    (2, 8, 8, 1, 64, 16, [200, 40], None, True),                       # whole, eight warps' block
+    (2, 8, 2, 1, 128, 16, [700, 3000], None, True),                    # split
+    (2, 8, 2, 3, 64, 16, [90, 1700], [3, 2], True),                    # 12 query rows, a padded sequence
+    (3, 28, 4, 4, 128, 32, [500, 1411, 64], [4, 1, 3], True),          # 28 query rows
+    (80, 14, 2, 4, 64, 16, [9 + b for b in range(80)], None, True),    # wide tiles, whole
+    (43, 28, 4, 4, 128, 16, [(411 * b) % 2500 for b in range(43)], None, False),  # wide tiles, split, no mask
+]
+
+
+@pytest.mark.parametrize("case", INFINITE_CASES, ids=lambda c: "B{}h{}kv{}q{}d{}x{}".format(*c[:5], max(c[6])))
+def test_an_infinite_value_that_a_query_sees_is_infinite_in_its_output(tsd, case):
+    """Column 3 holds +inf, column 4 -inf, column 5 one of each (no number), in the first row and
+    near the end of each sequence; the other columns are as the definition has them."""
+    B, h, h_kv, n_q, d, page, lens, new, causal = case
+    c = DecodeCase(case, False, seed=40)
+    pools = [p.clone() for p in c.pools]
+    places = [[] for _ in range(B)]  # (position, column, value)
+    for b, L in enumerate(lens):
+        if L < 6:
+            continue
+        for position in {0, L // 2, L - 1}:
+            places[b] += [(position, 3, np.inf), (position, 4, -np.inf)]
+        places[b] += [(1, 5, np.inf), (2, 5, -np.inf)]
+        for position, column, value in places[b]:
+            set_rows(c, pools[1], b, position, column, value)
+    clean = []
+    for b, rows in enumerate(c.v_rows):
+        rows = rows.copy()
+        for position, column, _ in places[b]:
+            rows[:, position, column] = 0
+        clean.append(rows)
+    got = to_host_f64(c.run(tsd, pools=pools))
+    ref, mass, size = pu.decode(c.q, c.k_rows, clean, lens, c.new, causal, 1 / np.sqrt(d))
+    want = ref.copy()
+    for b, L in enumerate(lens):
+        for t in range(c.new[b]):
+            seen = min(L, L - c.new[b] + t + 1) if causal else L
+            for position, column, value in places[b]:
+                if position < seen:
+                    with np.errstate(invalid="ignore"):
+                        want[b, :, t, column] += value
+    tol = pu.decode_tolerance(ref, mass, size, max(max(lens), 1), d)
+    finite = np.isfinite(want)
+    assert np.all(np.abs(got - ref)[finite] <= tol[finite])
+    assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK

@@ -38,8 +38,11 @@
 //    maximum over the warp, only a vote.
 //
 // Numbers: S, the softmax and O in fp32. With a bf16 cache P is split into
-// two bf16 parts, p = hi + lo (16 bits), at the cost of a second product
-// that the tensor cores have time for. With a 4-bit cache code * scale has
+// two bf16 parts, p = hi + lo to within 1.1 2^-16 of p, at the cost of a second
+// product that the tensor cores have time for. Neither is below 0, and lo is
+// not 0 unless p is as good as that: an infinite value that a query sees, times
+// either, is the same infinity (with hi rounded to nearest, lo is 0 or less
+// half of the time, and the sum of the products would be no number). With a 4-bit cache code * scale has
 // 6 significant bits and is formed in f16 without rounding; q is brought to
 // f16 by a power of two per row, which keeps every bf16 value within 2^-33
 // of the row's largest; and P is rounded to f16: to 11 bits, well below the
@@ -847,10 +850,13 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT, Q4, W>::kMinBlocks)
             if constexpr (Q4) {
               p_hi[h][nt][half] = transpose8x8(pack_f16x2(p0, p1));
             } else {
-              const uint32_t hi = pack_bf16x2(p0, p1);
+              // hi cut off, so that the rest is no less than 0; and 2^-20 of p
+              // more, so that it is not 0
+              const uint32_t hi = __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+              constexpr float kAbove = 1.f + 0x1p-20f;
               p_hi[h][nt][half] = transpose8x8(hi);
-              p_lo[h][nt][half] = transpose8x8(
-                  pack_bf16x2(p0 - bf16_f32(hi & 0xffffu), p1 - bf16_f32(hi >> 16)));
+              p_lo[h][nt][half] = transpose8x8(pack_bf16x2(fmaf(p0, kAbove, -bf16_f32(hi & 0xffffu)),
+                                                           fmaf(p1, kAbove, -bf16_f32(hi >> 16))));
             }
           }
         }
