@@ -586,7 +586,10 @@ attn_status attn_cache_append_q4(const void *q, int64_t q_sb, int64_t q_sh, int6
  * Rows of `out` that see no row, padding tokens' among them, are 0. Rows at
  * or past cache_lens[b] are never used, whatever they hold. An infinity in a
  * value that a query sees is one in its output (a NaN if the row's weight is
- * below fp32's range, or both infinities meet). Errors as attn_decode.
+ * below fp32's range, or both infinities meet). The weighted values are added
+ * up in fp32 before the division by the weights' sum, the largest weight being
+ * 1 at most: a bf16 cache's |v| of one column have to add up to fp32's range.
+ * Errors as attn_decode.
  */
 size_t attn_decode_paged_workspace_bytes(int B, int h, int h_kv, int n_q, int d, int page_size,
                                          int max_pages);

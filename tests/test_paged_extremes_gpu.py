@@ -67,3 +67,41 @@ def test_an_infinite_value_that_a_query_sees_is_infinite_in_its_output(tsd, case
     assert np.all(np.abs(got - ref)[finite] <= tol[finite])
     assert np.array_equal(got[~finite], want[~finite], equal_nan=True)
     assert tsd.attn_get_device_status() == tsd.ATTN_OK
+
+
+@pytest.mark.parametrize("case", [
+    (2, 4, 4, 1, 64, 16, [200, 37], None, True),
+    (2, 8, 2, 2, 128, 16, [900, 2500], None, True),
+    (3, 28, 4, 4, 64, 32, [500, 1411, 64], [4, 1, 3], True),
+    (80, 14, 2, 4, 128, 16, [30 + b for b in range(80)], None, True),
+], ids=lambda c: "B{}h{}kv{}q{}d{}x{}".format(*c[:5], max(c[6])))
+@pytest.mark.parametrize("rise", [2.0, 7.4, 30.0])
+def test_values_near_the_largest_bf16(tsd, case, rise):
+    """Two thirds into each sequence a row has a logit that is `rise` powers of 2 above the other
+    rows' and values near bf16's largest; the other rows' are a thousandth of that. No sum of
+    weights of at most 1 times values passes fp32's range."""
+    B, h, h_kv, n_q, d, page, lens, new, causal = case
+    c = DecodeCase(case, False, seed=50)
+    rng = np.random.default_rng(51)
+    q = np.zeros((B, h, n_q, d))
+    q[..., 0] = 1
+    pools = [p.clone() for p in c.pools]
+    k_rows, v_rows = [], []
+    f64 = lambda x: synthetic.bf16_bits_to_f64(synthetic.f32_to_bf16_bits(np.asarray(x, dtype=np.float32)))
+    for b, L in enumerate(lens):
+        k, v = c.k_rows[b].copy(), f64(c.v_rows[b] * 3e34)
+        k[..., 0] = f64(rng.uniform(-0.3, 0.3, k.shape[:2]))
+        at = 2 * L // 3
+        k[:, at, 0] = f64(rise)
+        v[:, at] = f64(3.3e38 * rng.choice([-1.0, 1.0], (h_kv, d)) * rng.uniform(0.9, 1.0, (h_kv, d)))
+        p = np.arange(L)
+        place = c.table[b, p // page], slice(None), p % page
+        for pool, rows in zip(pools, (k, v)):
+            pool.view(c.torch.int16)[place] = dev(synthetic.f32_to_bf16_bits(
+                rows.swapaxes(0, 1).astype(np.float32)).view(np.int16))
+        k_rows.append(k)
+        v_rows.append(v)
+    scale = float(np.float32(np.log(2)))
+    out = c.run(tsd, q=to_dev_bf16(synthetic.f32_to_bf16_bits(q.astype(np.float32))), pools=pools,
+                scale=scale)
+    c.check(tsd, out, k_rows, v_rows, q=q, scale=scale)

@@ -33,9 +33,9 @@
 //    does not care about the order of its terms, a thread's K columns are
 //    the ones that its 16 bytes hold, Q being laid out to match, and the two
 //    rows that share a register of V are interleaved before the conversion.
-//  * Softmax. The exponents' reference m follows the running maximum only
-//    when a value exceeds it by 2^kSlack: the common tile then needs no
-//    maximum over the warp, only a vote.
+//  * Softmax. The exponents' reference m is 2^kShift below the running maximum
+//    when it is set, and follows it only when a p would pass 2^(kShift +
+//    kSlack): the common tile then needs no maximum over the warp, only a vote.
 //
 // Numbers: S, the softmax and O in fp32. With a bf16 cache P is split into
 // two bf16 parts, p = hi + lo to within 1.1 2^-16 of p, at the cost of a second
@@ -137,8 +137,9 @@ struct Shape {
   static constexpr int kPitch = D + 4;  // floats of a row of O in shared memory
   // a 4-bit cache's inner loop has no registers to spare for Q
   static constexpr bool kQInSmem = Q4 || NT * D > 128;
-  // p = 2^(x - m) is at most 2^(kShift + kSlack); f16 holds up to 2^15.99
-  static constexpr float kShift = Q4 ? 11.f : 0.f, kSlack = Q4 ? 4.f : 8.f;
+  // p = 2^(x - m) is at most 2^(kShift + kSlack): f16 holds up to 2^15.99, and
+  // a bf16 value times 1 is in fp32's range
+  static constexpr float kShift = Q4 ? 11.f : -8.f, kSlack = Q4 ? 4.f : 8.f;
   static constexpr int kMergeBytes = kWarps * kRows * kPitch * 4;
   // a warp's part of O fits into one stage of its ring
   static constexpr bool kAhead = kRows * kPitch * 4 <= kStageBytes;
