@@ -105,3 +105,16 @@ def test_values_near_the_largest_bf16(tsd, case, rise):
     out = c.run(tsd, q=to_dev_bf16(synthetic.f32_to_bf16_bits(q.astype(np.float32))), pools=pools,
                 scale=scale)
     c.check(tsd, out, k_rows, v_rows, q=q, scale=scale)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_4_bit_logits_of_zero_with_the_largest_queries(tsd, d):
+    """Keys of zero against queries up to bf16's largest and a large factor: every logit is 0, and
+    the output the mean of the values."""
+    c = DecodeCase((2, 8, 2, 2, d, 16, [130, 1500], None, True), True, seed=60)
+    c.factors = (2.0 ** 20, 0.03)
+    pools = [c.torch.zeros_like(c.pools[0])] + c.pools[1:]
+    q = np.where(np.arange(8)[None, :, None, None] % 2, 3.3e38, 1.0) * np.sign(c.q)
+    bits = synthetic.f32_to_bf16_bits(q.astype(np.float32))
+    out = c.run(tsd, q=to_dev_bf16(bits), pools=pools, scale=1.0)
+    c.check(tsd, out, [np.zeros_like(k) for k in c.k_rows], q=synthetic.bf16_bits_to_f64(bits), scale=1.0)

@@ -633,9 +633,10 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT, Q4, W>::kMinBlocks)
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             w[s][i] = pack_f16x2(bf16_f32(w[s][i] & 0xffffu) * f0 * f1, bf16_f32(w[s][i] >> 16) * f0 * f1);
-        // the factor from S to x; not 0, which would make the masks' -inf no number
+        // the factor from S to x; not 0, which would make the masks' -inf no
+        // number, and finite, as an infinite one would make so a product of 0
         const float d0 = __int_as_float((127 - up0) << 23), d1 = __int_as_float((127 - up1) << 23);
-        if (t == 0) s_mult[nt * 8 + g] = fmaxf(a.scale_log2 * d0 * d1, 1.2e-38f);
+        if (t == 0) s_mult[nt * 8 + g] = fminf(fmaxf(a.scale_log2 * d0 * d1, 1.2e-38f), 3.4e38f);
       }
       if constexpr (S::kQInSmem) {
 #pragma unroll
