@@ -643,15 +643,15 @@ attn_status run_cache_append(const void* q, int64_t q_sb, int64_t q_sh, int64_t 
   if (cache_lens == nullptr) return ATTN_ERR_INVALID;
   if ((q == nullptr) != (q_out == nullptr)) return ATTN_ERR_INVALID;
   if (!k || !v) return ATTN_ERR_INVALID;
-  for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out),
-                        static_cast<const void*>(rope)})
+  for (const void* p : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_out)})
     if (!aligned16(p)) return ATTN_ERR_INVALID;
   for (int64_t st : {q_sb, q_sh, q_sr, kv_sb, kv_sh, kv_sr})
     if (st < 0 || st % 8 != 0) return ATTN_ERR_INVALID;
   if (rope_kind != ATTN_ROPE_NONE && rope_kind != ATTN_ROPE_HALVES && rope_kind != ATTN_ROPE_PAIRS)
     return ATTN_ERR_INVALID;
   if (rope_kind != ATTN_ROPE_NONE) {
-    if (rope == nullptr || rope_rows < 1 || rope_dim < 2 || rope_dim > d || rope_dim % 2 != 0)
+    if (rope == nullptr || !aligned16(rope) || rope_rows < 1 || rope_dim < 2 || rope_dim > d ||
+        rope_dim % 2 != 0)
       return ATTN_ERR_INVALID;
     if (rope_dim % 32 != 0) return ATTN_ERR_UNSUPPORTED;
   }
