@@ -154,10 +154,10 @@ def _ptr(x):
     """Address of a torch tensor (device or host), a numpy array (host), or an int."""
     if x is None:
         return None
-    try:
-        return x.data_ptr()
-    except AttributeError:
-        return x if isinstance(x, int) else x.ctypes.data
+    if isinstance(x, int):
+        return x
+    data_ptr = getattr(x, "data_ptr", None)
+    return x.ctypes.data if data_ptr is None else data_ptr()
 
 
 def _current_stream():
