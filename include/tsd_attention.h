@@ -479,6 +479,9 @@ attn_status attn_decode_host_async(const void *q_host, const void *k_cache,
  *
  *   page_table  device int32[B, max_pages]; entries past a sequence's last
  *               row are never read
+ *   max_pages   the host sees this and not the lengths: a decoding step over
+ *               short sequences is a few microseconds faster under a table
+ *               no wider than they need (max_pages * page_size <= 1280 rows above all)
  *   page_size   a power of two, 16..256 (other powers -> ATTN_ERR_UNSUPPORTED);
  *               max_pages * page_size <= 2^30 and n_pages * h_kv * page_size < 2^36 - 16,
  *               else ATTN_ERR_UNSUPPORTED

@@ -42,12 +42,13 @@
 // product that the tensor cores have time for. Neither is below 0, and lo is
 // not 0 unless p is as good as that: an infinite value that a query sees, times
 // either, is the same infinity (with hi rounded to nearest, lo is 0 or less
-// half of the time, and the sum of the products would be no number). With a 4-bit cache code * scale has
-// 6 significant bits and is formed in f16 without rounding; q is brought to
-// f16 by a power of two per row, which keeps every bf16 value within 2^-33
-// of the row's largest; and P is rounded to f16: to 11 bits, well below the
-// output's 8, where it is at least 2^-25 of the row's largest in its warp
-// (m is 2^kShift below that), and to 2^-36 of that below.
+// half of the time, and the sum of the products would be no number). With a
+// 4-bit cache code * scale has 6 significant bits and is formed in f16 without
+// rounding; q is brought to f16 by a power of two per row, exactly down to 2^-25
+// of the row's largest value, and within 2^-33 of that largest below; and P is
+// rounded to f16: to 11 bits, well below the output's 8, where it is at least
+// 2^-25 of the row's largest in its warp (m is 2^kShift below that), and to 2^-36
+// of that below.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -71,8 +72,10 @@ constexpr int64_t kUnsplitRows = 1280;
 // us in place of 11.3; of 100 rows 4.6 in place of 4.3, of 1900 rows 12.6, and
 // split 11.6).
 constexpr int64_t kAlone = 152, kFewRows = 256;
-// What starting and ending a pair costs, in units (48 sequences of up to 16384
-// rows in 4 bits: 117 us with 1, 116 with 2, 114 with 4, 109 with 6, 109 with 8).
+// What starting and ending a pair costs, in units. 1, 3, 6 and 12, in us: 48
+// sequences of up to 16384 rows in 4 bits 101.6, 99.0, 94.9 and 96.0; 64 of up to
+// 8192 in bf16 173.7, 172.4, 171.9 and 173.8; 7 of up to 5001 with 28 query rows
+// 21.9, 20.9, 21.1 and 21.3; one of 131072 in 4 bits 36.5, 36.6, 37.1 and 37.3.
 constexpr int kPairUnits = 6;
 constexpr int kMaxBlocks = 608;          // 4 blocks on each of 152 SMs, more than fit
 constexpr int kMergeThreads = 256;       // at most
@@ -80,11 +83,25 @@ constexpr float kLowest = -3.4028234e38f;  // m before the first row
 
 // Query rows of a block's tile, 8, 16 or 32. A wide tile reads the cache once
 // for all of its rows; a narrow one is done sooner, and its blocks share the
-// cache's rows through L2. With 28 query rows to a key head (d = 128, bf16):
-// unsplit, 1000 rows, 12 pairs 10.8, 13.6 and 19.2 us; 64 pairs 14.6, 14.9
-// and 19.7; 160 pairs 37.2, 30.5 and 27.2. Split, 2500 rows, 40 pairs 23.4,
-// 21.4 and 24.9 us; 5000 rows, 28 pairs 26.9, 23.2 and 24.8; 4000 rows, 128
-// pairs 99, 60 and 49.
+// cache's rows through L2 (but each copies them: 4 tokens of 28 heads over 4
+// key heads, 41.6 MB of rows, bring 85 MB from L2 to the SMs in two tiles of
+// 16). Tiles of 8, 16 and 32, in us, at (pairs x rows each); the first three unsplit:
+//                        12x1000     64x1000     160x1000    40x2500     28x5000     128x4000
+// 28 rows, d 128, bf16  11  14  19    15  16  20    40  33  28    25  23  26    33  27  27    158  73  57
+//                4 bit  10  12  17    16  14  18    29  27  24    22  20  24    25  22  24     65  51  47
+//           d 64, bf16   9  10  13    12  11  13    23  22  18    17  16  18    21  19  19     52  44  36
+//                4 bit   8   9  11    11  10  12    20  19  14    17  16  18    19  17  17     46  37  30
+// 12 rows, d 128, bf16  11  13  18    13  14  19    28  20  26    20  20  23    25  23  25     66  49  52
+//                4 bit  10  12  16    11  12  16    16  15  22    17  17  20    19  18  23     38  30  42
+//           d 64, bf16   9  10  13     9  10  13    13  13  17    14  14  16    16  16  18     35  31  32
+//                4 bit   8   9  11     9   9  11    11  11  14    14  14  15    15  14  16     27  22  27
+// 10 rows are like 12, and 24 like 28. What the rule takes is 10 % off the best
+// of these three at most (64x1000 of 28 rows, d 128, bf16), and is better where
+// eight warps are taken (12x1000: 6.7 to 9.5).
+// All of it goes by the rows that the page table has room for: the host does not
+// know the lengths. 24 sequences of 100 to 900 rows, 32 query and 8 key heads of
+// 128, take 14.1 us (4 bits 10.8) under a table as wide as they need and 18.7
+// (15.0) under one of 32768 rows.
 struct Plan {
   int tile_rows;
   bool unsplit, eight_warps;
@@ -613,8 +630,10 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT, Q4, W>::kMinBlocks)
       const int nt = S::kQInSmem ? warp : n;
       if (nt >= NT) continue;
       if constexpr (Q4) {
-        // the row's largest magnitude decides a power of two that brings it
-        // below 2^9; what is 2^-33 of it or less may lose bits
+        // the row's largest magnitude decides a power of two that brings it to
+        // 2^8 or more, below 2^9. f16's least step is 2^-24: a value of 8 bits is
+        // exact from 2^-17 on (2^-25 of the largest or more), and smaller ones
+        // are off by half that step, 2^-33 of the largest, at most
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)

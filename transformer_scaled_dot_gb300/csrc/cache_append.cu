@@ -22,8 +22,9 @@
 // heads from token to token, the next token's pieces on their way while it
 // writes this one's. 8 prompts of 1900 to 4096 tokens, 48 rows of 64 each, in
 // bf16: 325 MB in 52 us, 6.3 TB/s, 0.92 of a plain copy's rate. 3 prompts of
-// 1203 to 2777, 48 rows of 128, in 4 bits: 140 MB in 32 us, 4.4 TB/s, bound by
-// instructions (0.67 of the issue slots).
+// 1203 to 2777, 48 rows of 128, in 4 bits: 140 MB in 32 us, 4.4 TB/s, at 0.67
+// of the issue slots, with 24 warps to an SM (80 registers, 68 bytes of them
+// spilled) and 2.3 rounds of blocks; 4 prompts of 8192 run at 0.80 of a copy's.
 #include <cuda_bf16.h>
 
 #include "kernels.h"
@@ -34,7 +35,10 @@ namespace tsd {
 namespace {
 
 constexpr int kMaxSpan = 4;      // tokens of a block; no more than the smallest page's 16
-constexpr int kWave = 152 * 10;  // blocks on the device at once
+// Up to this many tokens a block takes one of them and a thread one head; above
+// it a thread takes three heads, and a block a token more for each time this
+// many, up to kMaxSpan (launch_cache_append).
+constexpr int kFewTokens = 1520;
 
 __device__ __forceinline__ float4 ld_f4(const float* p) {
   return *reinterpret_cast<const float4*>(p);
@@ -295,18 +299,24 @@ cudaError_t launch_cache_append(const AppendProblem& p, cudaStream_t stream) {
   if (tokens < 1 || tokens > INT32_MAX || (p.cache.d != 64 && p.cache.d != 128))
     return cudaErrorInvalidValue;
   const bool q4 = p.cache.k_scales != nullptr;
-  // a head to a thread and a token to a block while the blocks find room on
-  // the device together: the shortest way through (0.5 to 0.8 us of 3 shorter
-  // than three heads). Else three heads and up to four tokens, whose loads
-  // overlap (32768 tokens of 48 rows: 52 us; two heads 54, four 59; one, two
-  // or eight tokens to a block 66, 54 and 58).
+  // A head to a thread is the shortest way through, three heads' loads overlap.
+  // One head against three, in us: 8 query and 2 x 8 key and value heads of 64,
+  // bf16, 32 tokens 2.1 and 2.8, 400 2.6 and 3.0, 800 3.5 and 3.1, 1520 4.6 and
+  // 3.5, 32768 85 and 36; 4 bits 2.8 and 4.7, 3.3 and 5.1, 4.6 and 5.2, 5.9 and
+  // 5.5, 100 and 51. More rows to a token cross sooner: 32 and 2 x 8 heads of
+  // 128, bf16, 96 tokens 2.8 and 3.0, 200 4.0 and 3.3, 800 10.0 and 5.0, 1520 21
+  // and 9.3; 4 bits 3.3 and 4.2, 5.0 and 4.5, 12.8 and 6.7, 24 and 11. One number
+  // for all fits the first of these in 4 bits, and is late for the others.
+  // Of the larger choices, 32768 tokens of 48 rows of 64 in bf16: 52 us; two
+  // heads 54, four 59; one, two or eight tokens to a block 66, 54 and 58. In 4
+  // bits two heads take as long as three (8331 tokens of 48 rows of 128: 32.0).
   const bool wide = p.cache.d == 128;
-  if (tokens <= kWave) {
+  if (tokens <= kFewTokens) {
     if (wide) return q4 ? launch_items<128, true, 1>(p, 1, stream) : launch_items<128, false, 1>(p, 1, stream);
     return q4 ? launch_items<64, true, 1>(p, 1, stream) : launch_items<64, false, 1>(p, 1, stream);
   }
-  const int64_t waves = (tokens + kWave - 1) / kWave;
-  const int span = waves < kMaxSpan ? static_cast<int>(waves) : kMaxSpan;
+  const int64_t times = (tokens + kFewTokens - 1) / kFewTokens;
+  const int span = times < kMaxSpan ? static_cast<int>(times) : kMaxSpan;
   if (wide) return q4 ? launch_items<128, true, 3>(p, span, stream) : launch_items<128, false, 3>(p, span, stream);
   return q4 ? launch_items<64, true, 3>(p, span, stream) : launch_items<64, false, 3>(p, span, stream);
 }
