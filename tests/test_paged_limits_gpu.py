@@ -205,3 +205,40 @@ def test_first_calls_inside_a_capture(tsd):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+def test_the_smallest_factor_over_the_longest_cache(tsd):
+    """Values of 2^-100 under weights whose sum is near the largest that a 4-bit cache can have: the
+    rows that a block begins with have logits 3.9 powers of 2 below all others, so that weights
+    reach 2^14.9 times 2^30 rows. Every value is the same, and so is the output."""
+    import torch
+    d, page = 64, 256
+    # rows for which 2^-100 over the sum, 2^11 (its logits' rise) rows, is 17.5 of fp32's least steps
+    rows = int(2.0 ** 38 / 17.5 / 2.0 ** 3.9)
+    max_pages = rows // page
+    rows = max_pages * page
+    codes = torch.zeros(2, 1, page, d // 2, dtype=torch.uint8, device="cuda")
+    codes[1, :, :, 0] = 2  # a key's first column: 0 on page 0, 1 on page 1
+    v_codes = torch.full_like(codes, 0x22)
+    scales = torch.full((2, 1, page, d // 16), 0x38, dtype=torch.uint8, device="cuda")
+    table = np.ones((1, max_pages), dtype=np.int32)
+    blocks = 3 * torch.cuda.get_device_properties(0).multi_processor_count
+    units = rows // 64 + 6  # of 64 rows, six standing for none
+    for block in range(blocks):
+        first = max(block * units // blocks - 6, 0) * 64 // page
+        table[0, first:first + 2] = 0
+    q = torch.zeros(1, 1, 1, d, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1
+    out = torch.empty_like(q)
+    wsb = tsd.attn_decode_paged_workspace_bytes(1, 1, 1, 1, d, page, max_pages)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    tsd.attn_decode_paged_q4(q, codes, scales, v_codes, scales, 1.0, 2.0 ** -100, out, to_dev_i32(table),
+                             to_dev_i32([rows]), None, 1, 1, 1, 1, d, 2, page, max_pages, 0,
+                             3.9 * np.log(2), ws, wsb)
+    torch.cuda.synchronize()
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+    got = to_host_f64(out).ravel() * 2.0 ** 100
+    # bf16's rounding; a weight's to 11 bits; a warp's sums, one product of 16 rows after the other
+    # in 32 bits (2^-23 of the sum so far, half of it on the average), in O and in the weights' own
+    steps = rows / 16 / 4 / blocks
+    assert np.all(np.abs(got - 1) <= 2.0 ** -8 + 2.0 ** -11 + 2 * steps * 2.0 ** -24), got

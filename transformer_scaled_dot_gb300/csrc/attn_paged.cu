@@ -294,6 +294,14 @@ __device__ __forceinline__ uint32_t scales_f16x2(uint32_t two) {
 }
 __device__ __forceinline__ float bf16_f32(uint32_t bits) { return __uint_as_float(bits << 16); }
 
+// Four values of O times the inverse of the weights' sum, then the values'
+// factor, as bf16. (The factor over a sum of up to 2^45 may be below fp32's
+// normal numbers.)
+__device__ __forceinline__ uint2 output4(const float4& y, float inv, float factor) {
+  return make_uint2(pack_bf16x2(y.x * inv * factor, y.y * inv * factor),
+                    pack_bf16x2(y.z * inv * factor, y.w * inv * factor));
+}
+
 // ------------------------------------------------------------------ the ring
 
 // Where the 4-bit tile's rows lie in shared memory, so that a warp's loads of
@@ -1084,10 +1092,9 @@ __global__ void __launch_bounds__(32 * W, Shape<D, NT, Q4, W>::kMinBlocks)
       if (whole) {
         const bool real = (done_row0 + r) % a.n_q < done.fresh;
         // no row seen (sum 0), or padding: 0; a sum that is no number stays one
-        const float inv = real && join.y != 0.f ? a.v_factor / join.y : 0.f;
+        const float inv = real && join.y != 0.f ? 1.f / join.y : 0.f;
         *reinterpret_cast<uint2*>(a.out + (out_row0 + r) * D + d) =
-            inv == 0.f ? make_uint2(0u, 0u)
-                       : make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+            inv == 0.f ? make_uint2(0u, 0u) : output4(y, inv, Q4 ? a.v_factor : 1.f);
       } else {
         *reinterpret_cast<float4*>(a.part_o + (slot * S::kRows + r) * D + d) = y;
         if (d == 0) a.part_ml[slot * S::kRows + r] = join;
@@ -1182,11 +1189,10 @@ __global__ void __launch_bounds__(kMergeThreads) decode_paged_merge_kernel(const
     }
     const Sequence seq = sequence(a, b);
     const bool real = (row0 + r) % a.n_q < seq.fresh;
-    const float inv = real && sum != 0.f ? a.v_factor / sum : 0.f;
+    const float inv = real && sum != 0.f ? 1.f / sum : 0.f;
     const int64_t row = (static_cast<int64_t>(b) * a.h_kv + head) * a.rows + row0 + r;
     *reinterpret_cast<uint2*>(a.out + row * D + 4 * col) =
-        inv == 0.f ? make_uint2(0u, 0u)
-                   : make_uint2(pack_bf16x2(y.x * inv, y.y * inv), pack_bf16x2(y.z * inv, y.w * inv));
+        inv == 0.f ? make_uint2(0u, 0u) : output4(y, inv, a.v_factor);
   }
 }
 
