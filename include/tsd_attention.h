@@ -53,8 +53,10 @@ typedef enum attn_status {
                                     (e.g. a head size the bf16 kernel has no variant for) */
     ATTN_ERR_CUDA = 3,           /* a CUDA runtime/driver call failed; see attn_last_cuda_error() */
     ATTN_ERR_DEVICE_TIMEOUT = 4, /* a kernel's bounded wait ran out (attn_get_device_status) */
-    ATTN_ERR_DEVICE_INDEX = 5    /* a page index, or a new token's position, was out of range: its
+    ATTN_ERR_DEVICE_INDEX = 5,   /* a page index, or a new token's position, was out of range: its
                                     row was left out (attn_get_device_status) */
+    ATTN_ERR_DEVICE_VALUE = 6    /* a beam's logits or score held a NaN or +infinity: the beam was
+                                    left out (attn_get_device_status) */
 } attn_status;
 
 /* mask_kind bit flags */
@@ -616,11 +618,201 @@ attn_status attn_decode_paged_q4(const void *q, const void *k_codes, const void 
                                  void *workspace, size_t workspace_bytes, tsd_stream_t stream);
 
 /*
+ * Keeping a paged cache's pages. The calls below keep the page table that
+ * attn_cache_append and attn_decode_paged read, between them: they give rows
+ * of the table pages, share pages between rows, take them back and move them.
+ * ("Attention Is All You Need 해부" (sj-techlog), section "KV cache는 추론의
+ * 같은 계산을 반복하지 않게 한다", gives the cache; its pages are this library's.)
+ * The state is two device arrays that the caller sets up and owns:
+ *
+ *   page_table  int32[B, max_pages]; -1 (any negative entry) holds no page
+ *   ref_counts  int32[n_pages]: how many entries, of this and any other table
+ *               over the same pool, name the page; 0: the page is free
+ *
+ * An empty table is all -1, an empty pool all 0. Row r of the table is a
+ * sequence. Where a call takes new pages, it takes the free pages of the
+ * lowest numbers, in the order of the rows and of each row's pages; what a
+ * call does follows from its arguments alone, and nothing is kept between
+ * calls. Counts that are not what the table says give wrong tables, never an
+ * access out of range. An entry or a number that is out of range is left out and
+ * attn_get_device_status answers ATTN_ERR_DEVICE_INDEX once. Calls that change
+ * the same ref_counts have to be ordered by their stream.
+ *   page_size, max_pages, B: as above; n_pages <= 2^30, else ATTN_ERR_UNSUPPORTED
+ *   every array: device memory, 4-byte aligned; a null or misaligned pointer
+ *   or a bad size -> ATTN_ERR_INVALID. B = 0 launches nothing (but for
+ *   attn_cache_compact)
+ *
+ * A step of beam search over a paged cache is
+ *   attn_cache_fork(table, lens, counts, parents, ...)  the rows beam_select chose
+ *   attn_cache_reserve(...)     places for the new tokens; cache_lens with them
+ *   attn_cache_copy(...)        the pages that reserve listed, all layers
+ *   and then attn_cache_append and attn_decode_paged in every layer.
+ */
+
+/*
+ * attn_cache_fork -- row r of the table becomes row parents[r], all rows at
+ * once: rows that continue the same row share its pages, and pages that no row
+ * names any more are free.
+ *   parents     int32[B]: a row's number, its own to stay as it is, or -1: the
+ *               row is empty afterwards
+ *   cache_lens  int32[B], in place: lens[r] becomes lens[parents[r]] (0 for -1).
+ *               NULL: not wanted
+ *   B <= 32768, else ATTN_ERR_UNSUPPORTED
+ * A parent out of range leaves its row as it is. One launch.
+ */
+attn_status attn_cache_fork(int32_t *page_table, int32_t *cache_lens, int32_t *ref_counts,
+                            const int32_t *parents, int B, int n_pages, int max_pages,
+                            tsd_stream_t stream);
+
+/*
+ * attn_cache_release -- row b keeps the pages of its first keep_lens[b] rows
+ * of the cache and gives the others back: 0 frees a sequence, a smaller length
+ * takes back speculated tokens, a negative number leaves the row as it is.
+ *   keep_lens   int32[B], or NULL: all rows are freed
+ * One launch.
+ */
+attn_status attn_cache_release(int32_t *page_table, int32_t *ref_counts, const int32_t *keep_lens,
+                               int B, int n_pages, int page_size, int max_pages,
+                               tsd_stream_t stream);
+
+/*
+ * attn_cache_reserve -- before attn_cache_append with the same cache_lens,
+ * new_lens and n_new: every page that the new tokens are written into exists
+ * and belongs to its row alone. The positions are cache_lens[b] - new_lens[b]
+ * .. cache_lens[b] - 1; of the pages that hold them,
+ *   a missing one is taken from the free pages;
+ *   one that other entries name too is left, and a free page taken in its
+ *   place. Where all that name it are rows of this call that write it, the
+ *   first of them keeps it. If the page holds earlier rows of the sequence (its
+ *   first page can), a copy of them is listed.
+ *   copies      int32[B, 3], written: (from page, to page, rows), in the order
+ *               of the sequences; entries past n_copies[0] are left as they were.
+ *               attn_cache_copy carries them out: no page is both from and to
+ *   n_copies    int32[1], written
+ *   n_missing   int32[1], written: 0, or how many pages are wanting. Then
+ *               nothing is changed and nothing listed
+ *   workspace   device, 16-byte aligned, >= attn_cache_pages_workspace_bytes(B,
+ *               n_pages) bytes of scratch (0 for sizes that the calls refuse)
+ * Positions past max_pages * page_size get no page. One launch.
+ */
+size_t attn_cache_pages_workspace_bytes(int B, int n_pages);
+attn_status attn_cache_reserve(int32_t *page_table, int32_t *ref_counts, const int32_t *cache_lens,
+                               const int32_t *new_lens, int32_t *copies, int32_t *n_copies,
+                               int32_t *n_missing, int B, int n_new, int n_pages, int page_size,
+                               int max_pages, void *workspace, size_t workspace_bytes,
+                               tsd_stream_t stream);
+
+/*
+ * attn_cache_compact -- moves the used pages to the front of the pool, so that
+ * its end can be given up or used otherwise. With U used pages, the k-th
+ * highest page from U on moves to the k-th lowest free page.
+ *   table_out   int32[B, max_pages], counts_out int32[n_pages]: the table and
+ *               the counts after the moves; may be page_table and ref_counts
+ *               themselves, and do not overlap them otherwise. B may be 0
+ *   copies      int32[max_copies, 3], written: (from, to, page_size) for
+ *               attn_cache_copy, which has to follow before the cache is read;
+ *               entries past n_copies[0] are left as they were
+ *   max_copies  at most so many pages move; >= min(U, n_pages - U) moves all
+ *   n_copies, n_used  int32[1], written: the moves, and U
+ *   workspace   as attn_cache_reserve
+ * All entries of tables that name pages of the pool have to be in page_table.
+ * Two launches (one for B = 0).
+ */
+attn_status attn_cache_compact(const int32_t *page_table, const int32_t *ref_counts,
+                               int32_t *table_out, int32_t *counts_out, int32_t *copies,
+                               int32_t *n_copies, int32_t *n_used, int B, int n_pages,
+                               int page_size, int max_pages, int max_copies, void *workspace,
+                               size_t workspace_bytes, tsd_stream_t stream);
+
+/*
+ * attn_cache_copy -- copies the first `rows` rows of page `from` to page `to`,
+ * of every head, of keys and values, in all layers, for every (from, to, rows)
+ * of a list.
+ *   k_cache, v_cache  the first layer's pools [n_pages, h_kv, page_size, d]
+ *               bf16; layer i's begin layer_rows * i rows of d columns further on
+ *   copies      int32[max_copies, 3]; n_copies int32[1], how many of them there
+ *               are (clamped to [0, max_copies]), or NULL: all
+ *   n_layers    >= 0; layer_rows a multiple of 16, >= n_pages * h_kv * page_size
+ *               (ignored for one layer), else ATTN_ERR_INVALID
+ *   h_kv * page_size * d <= 2^29, else ATTN_ERR_UNSUPPORTED
+ * No page may be `to` of two copies, or `from` of one and `to` of another. A
+ * copy with a number out of range is left out. One launch.
+ */
+attn_status attn_cache_copy(void *k_cache, void *v_cache, const int32_t *copies,
+                            const int32_t *n_copies, int max_copies, int n_layers,
+                            int64_t layer_rows, int h_kv, int d, int n_pages, int page_size,
+                            tsd_stream_t stream);
+
+/* attn_cache_copy_q4 -- attn_cache_copy of a 4-bit cache's codes and scales. */
+attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, void *v_scales,
+                               const int32_t *copies, const int32_t *n_copies, int max_copies,
+                               int n_layers, int64_t layer_rows, int h_kv, int d, int n_pages,
+                               int page_size, tsd_stream_t stream);
+
+/*
+ * beam_select -- one step of beam search ("[논문 리뷰]Attention Is All You
+ * Need" (kimjiil.github.io) and "Attention Is All You Need 해부" (sj-techlog)
+ * decode with beams of 4 and a length penalty alpha = 0.6; how a step handles
+ * ended hypotheses is this library's choice). Row b * beams + k of the logits is what beam k of sentence b says of
+ * its next token. With s the beams' scores (their tokens' summed log
+ * probabilities),
+ *   total(k, v) = s_k + x_kv - log sum_u exp x_ku,
+ * the 2 * beams best pairs of a sentence (`beams` without an end token; fewer
+ * where fewer are above -infinity), by total and then by lowest k * vocab + v,
+ * are its candidates.
+ *   The first `beams` candidates that are not the end token are the next beams.
+ *   Those that are the end token end there, with score total / ((5 + n) /
+ *   6)^alpha at n = lengths[b] tokens; the best `beams` of them and of the
+ *   hypotheses that ended before are kept, best first, earlier ones first among equals.
+ *
+ *   logits      bf16, 2-byte aligned; element (row, v) at row * row_stride + v,
+ *               row_stride >= vocab (16-byte aligned rows are faster)
+ *   scores      fp32[B, beams]; -infinity: no hypothesis (its logits are not
+ *               read). At a sentence's start: 0, and -infinity for the others
+ *   lengths     int32[B]: tokens of the hypotheses, the one chosen now among
+ *               them (less than 1 counts as 1)
+ *   end         the end token, or -1: none; then lengths, alpha and the ended_*
+ *               arrays are ignored
+ *   tokens, parents  int32[B, beams], written: the token, and the row b * beams
+ *               + k that it continues (as attn_cache_fork takes it)
+ *   new_scores  fp32[B, beams], written: totals; may be `scores` itself.
+ *               A beam without a candidate: -infinity, the end token (0 without
+ *               one) and its own row
+ *   ended_scores, ended_rows, ended_lengths  fp32, int32, int32 [B, beams], in
+ *               place: score, the row that the end token continued, and n. The
+ *               caller starts with scores of -infinity; a place without a
+ *               hypothesis has that and keeps the other two as they were
+ *   1 <= beams <= 16, vocab <= 2^20, and B * beams * ceil(vocab / 1024) < 2^31 -
+ *               64, else ATTN_ERR_UNSUPPORTED
+ *   workspace   device, 16-byte aligned, >= beam_select_workspace_bytes(...)
+ *               bytes of scratch (0 for sizes that the call refuses)
+ * Logits of -infinity are tokens that are never chosen. A beam whose logits or
+ * score hold a NaN or +infinity has no candidates, and attn_get_device_status
+ * answers ATTN_ERR_DEVICE_VALUE once. Totals are formed and compared in 64 bits
+ * from exponentials and partial sums in 32. beams = 1 is greedy decoding.
+ * Errors as attn_forward. Two launches.
+ */
+size_t beam_select_workspace_bytes(int B, int beams, int vocab);
+attn_status beam_select(const void *logits, int64_t row_stride, const float *scores,
+                        const int32_t *lengths, int B, int beams, int vocab, int end, float alpha,
+                        int32_t *tokens, int32_t *parents, float *new_scores, float *ended_scores,
+                        int32_t *ended_rows, int32_t *ended_lengths, void *workspace,
+                        size_t workspace_bytes, tsd_stream_t stream);
+
+/* beam_select_f32 -- beam_select of fp32 logits (4-byte aligned). */
+attn_status beam_select_f32(const float *logits, int64_t row_stride, const float *scores,
+                            const int32_t *lengths, int B, int beams, int vocab, int end,
+                            float alpha, int32_t *tokens, int32_t *parents, float *new_scores,
+                            float *ended_scores, int32_t *ended_rows, int32_t *ended_lengths,
+                            void *workspace, size_t workspace_bytes, tsd_stream_t stream);
+
+/*
  * attn_get_device_status -- synchronises `stream`, then reads and clears the
- * device error words the kernels set when a bounded wait runs out or a page
- * index or position is out of range. Returns ATTN_OK,
- * ATTN_ERR_DEVICE_TIMEOUT (also where both happened), ATTN_ERR_DEVICE_INDEX,
- * or ATTN_ERR_CUDA if the synchronisation itself failed.
+ * device error words the kernels set when a bounded wait runs out, a page
+ * index or position is out of range, or a beam's logits are no numbers. Returns
+ * ATTN_OK, ATTN_ERR_DEVICE_TIMEOUT, ATTN_ERR_DEVICE_INDEX, ATTN_ERR_DEVICE_VALUE
+ * (the first of them that happened, in this order), or ATTN_ERR_CUDA if the
+ * synchronisation itself failed.
  */
 attn_status attn_get_device_status(tsd_stream_t stream);
 

@@ -18,7 +18,8 @@ from . import build as _build
 
 __all__ = [
     "ATTN_OK", "ATTN_ERR_INVALID", "ATTN_ERR_UNSUPPORTED", "ATTN_ERR_CUDA",
-    "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_ERR_DEVICE_INDEX", "ATTN_MASK_NONE", "ATTN_MASK_CAUSAL", "ATTN_MASK_KEY_PADDING",
+    "ATTN_ERR_DEVICE_TIMEOUT", "ATTN_ERR_DEVICE_INDEX", "ATTN_ERR_DEVICE_VALUE",
+    "ATTN_MASK_NONE", "ATTN_MASK_CAUSAL", "ATTN_MASK_KEY_PADDING",
     "AttnError", "library", "library_path", "EXPORTED_SYMBOLS",
     "attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_workspace_bytes",
     "mha_forward", "attn_get_device_status", "attn_last_cuda_error", "attn_status_string",
@@ -32,11 +33,13 @@ __all__ = [
     "attn_decode_host_async", "encoder_layer_forward_host_async",
     "ATTN_ROPE_NONE", "ATTN_ROPE_HALVES", "ATTN_ROPE_PAIRS", "attn_cache_append",
     "attn_cache_append_q4", "attn_decode_paged_workspace_bytes", "attn_decode_paged",
-    "attn_decode_paged_q4",
+    "attn_decode_paged_q4", "attn_cache_fork", "attn_cache_release", "attn_cache_pages_workspace_bytes",
+    "attn_cache_reserve", "attn_cache_compact", "attn_cache_copy", "attn_cache_copy_q4",
+    "beam_select_workspace_bytes", "beam_select", "beam_select_f32",
 ]
 
 ATTN_OK, ATTN_ERR_INVALID, ATTN_ERR_UNSUPPORTED, ATTN_ERR_CUDA, ATTN_ERR_DEVICE_TIMEOUT, \
-    ATTN_ERR_DEVICE_INDEX = range(6)
+    ATTN_ERR_DEVICE_INDEX, ATTN_ERR_DEVICE_VALUE = range(7)
 ATTN_MASK_NONE, ATTN_MASK_CAUSAL, ATTN_MASK_KEY_PADDING = 0, 1, 2
 ATTN_ROPE_NONE, ATTN_ROPE_HALVES, ATTN_ROPE_PAIRS = 0, 1, 2
 
@@ -52,6 +55,9 @@ EXPORTED_SYMBOLS = (
     "mha_forward_host_async", "attn_host_join", "attn_decode_host_async",
     "encoder_layer_forward_host_async", "attn_cache_append", "attn_cache_append_q4",
     "attn_decode_paged_workspace_bytes", "attn_decode_paged", "attn_decode_paged_q4",
+    "attn_cache_fork", "attn_cache_release", "attn_cache_pages_workspace_bytes",
+    "attn_cache_reserve", "attn_cache_compact", "attn_cache_copy", "attn_cache_copy_q4",
+    "beam_select_workspace_bytes", "beam_select", "beam_select_f32",
 )
 
 # TSD_MHA_NOALLOC_SCRATCH_BYTES of the header: the fixed scratch of mha_forward_noalloc
@@ -136,7 +142,22 @@ def library():
     lib.attn_decode_paged_workspace_bytes.restype = sz
     lib.attn_decode_paged.argtypes = [vp] * 7 + [i] * 9 + [f, vp, sz, st]
     lib.attn_decode_paged_q4.argtypes = [vp] * 5 + [f, f] + [vp] * 4 + [i] * 9 + [f, vp, sz, st]
-    for name in ("attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_forward",
+    lib.attn_cache_fork.argtypes = [vp] * 4 + [i] * 3 + [st]
+    lib.attn_cache_release.argtypes = [vp] * 3 + [i] * 4 + [st]
+    lib.attn_cache_pages_workspace_bytes.argtypes = [i, i]
+    lib.attn_cache_pages_workspace_bytes.restype = sz
+    lib.attn_cache_reserve.argtypes = [vp] * 7 + [i] * 5 + [vp, sz, st]
+    lib.attn_cache_compact.argtypes = [vp] * 7 + [i] * 5 + [vp, sz, st]
+    lib.attn_cache_copy.argtypes = [vp] * 4 + [i, i, i64] + [i] * 4 + [st]
+    lib.attn_cache_copy_q4.argtypes = [vp] * 6 + [i, i, i64] + [i] * 4 + [st]
+    lib.beam_select_workspace_bytes.argtypes = [i] * 3
+    lib.beam_select_workspace_bytes.restype = sz
+    for name in ("beam_select", "beam_select_f32"):
+        getattr(lib, name).argtypes = [vp, i64, vp, vp, i, i, i, i, f] + [vp] * 7 + [sz, st]
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("attn_cache_fork", "attn_cache_release", "attn_cache_reserve",
+                 "attn_cache_compact", "attn_cache_copy", "attn_cache_copy_q4",
+                 "attn_forward", "attn_forward_strided", "attn_forward_f32", "mha_forward",
                  "attn_cache_append", "attn_cache_append_q4", "attn_decode_paged",
                  "attn_decode_paged_q4", "attn_get_device_status", "attn_last_cuda_error", "attn_selftest_wait_timeout",
                  "mha_project_qkv", "mha_project_out", "mha_forward_noalloc", "mha_concat_heads",
@@ -267,6 +288,91 @@ def attn_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, k_factor, v_fa
         _stream(stream)), "attn_decode_paged_q4")
 
 
+def attn_cache_fork(page_table, cache_lens, ref_counts, parents, B, n_pages, max_pages,
+                    stream=None):
+    """Row r of the page table becomes row parents[r] (-1: empty), all at once and in place;
+    ref_counts, and cache_lens unless None, follow."""
+    _check(library().attn_cache_fork(_ptr(page_table), _ptr(cache_lens), _ptr(ref_counts),
+                                     _ptr(parents), B, n_pages, max_pages, _stream(stream)),
+           "attn_cache_fork")
+
+
+def attn_cache_release(page_table, ref_counts, keep_lens, B, n_pages, page_size, max_pages,
+                       stream=None):
+    """Row b gives back the pages past its first keep_lens[b] rows (None: all; negative: none)."""
+    _check(library().attn_cache_release(_ptr(page_table), _ptr(ref_counts), _ptr(keep_lens), B,
+                                        n_pages, page_size, max_pages, _stream(stream)),
+           "attn_cache_release")
+
+
+def attn_cache_pages_workspace_bytes(B, n_pages) -> int:
+    return int(library().attn_cache_pages_workspace_bytes(B, n_pages))
+
+
+def attn_cache_reserve(page_table, ref_counts, cache_lens, new_lens, copies, n_copies, n_missing,
+                       B, n_new, n_pages, page_size, max_pages, workspace=None, workspace_bytes=0,
+                       stream=None):
+    """Pages of their own for the new tokens of every row, the lowest free ones first; the copies
+    that attn_cache_copy has to make of pages that were shared go into `copies`."""
+    _check(library().attn_cache_reserve(
+        _ptr(page_table), _ptr(ref_counts), _ptr(cache_lens), _ptr(new_lens), _ptr(copies),
+        _ptr(n_copies), _ptr(n_missing), B, n_new, n_pages, page_size, max_pages, _ptr(workspace),
+        workspace_bytes, _stream(stream)), "attn_cache_reserve")
+
+
+def attn_cache_compact(page_table, ref_counts, table_out, counts_out, copies, n_copies, n_used, B,
+                       n_pages, page_size, max_pages, max_copies, workspace=None,
+                       workspace_bytes=0, stream=None):
+    """The table and counts with the used pages at the front of the pool, and the copies that
+    attn_cache_copy has to make for it."""
+    _check(library().attn_cache_compact(
+        _ptr(page_table), _ptr(ref_counts), _ptr(table_out), _ptr(counts_out), _ptr(copies),
+        _ptr(n_copies), _ptr(n_used), B, n_pages, page_size, max_pages, max_copies,
+        _ptr(workspace), workspace_bytes, _stream(stream)), "attn_cache_compact")
+
+
+def attn_cache_copy(k_cache, v_cache, copies, n_copies, max_copies, n_layers, layer_rows, h_kv, d,
+                    n_pages, page_size, stream=None):
+    """Copies rows of pages by a list [max_copies, 3] of (from, to, rows), in all layers."""
+    _check(library().attn_cache_copy(_ptr(k_cache), _ptr(v_cache), _ptr(copies), _ptr(n_copies),
+                                     max_copies, n_layers, layer_rows, h_kv, d, n_pages,
+                                     page_size, _stream(stream)), "attn_cache_copy")
+
+
+def attn_cache_copy_q4(k_codes, k_scales, v_codes, v_scales, copies, n_copies, max_copies,
+                       n_layers, layer_rows, h_kv, d, n_pages, page_size, stream=None):
+    """attn_cache_copy of a 4-bit cache's codes and scales."""
+    _check(library().attn_cache_copy_q4(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes),
+                                        _ptr(v_scales), _ptr(copies), _ptr(n_copies), max_copies,
+                                        n_layers, layer_rows, h_kv, d, n_pages, page_size,
+                                        _stream(stream)), "attn_cache_copy_q4")
+
+
+def beam_select_workspace_bytes(B, beams, vocab) -> int:
+    return int(library().beam_select_workspace_bytes(B, beams, vocab))
+
+
+def beam_select(logits, row_stride, scores, lengths, B, beams, vocab, end, alpha, tokens, parents,
+                new_scores, ended_scores=None, ended_rows=None, ended_lengths=None,
+                workspace=None, workspace_bytes=0, stream=None):
+    """One step of beam search: the next beams of each sentence from its beams' bf16 logits, and
+    the hypotheses that ended (end = -1: no end token)."""
+    _check(library().beam_select(
+        _ptr(logits), row_stride, _ptr(scores), _ptr(lengths), B, beams, vocab, end, alpha,
+        _ptr(tokens), _ptr(parents), _ptr(new_scores), _ptr(ended_scores), _ptr(ended_rows),
+        _ptr(ended_lengths), _ptr(workspace), workspace_bytes, _stream(stream)), "beam_select")
+
+
+def beam_select_f32(logits, row_stride, scores, lengths, B, beams, vocab, end, alpha, tokens,
+                    parents, new_scores, ended_scores=None, ended_rows=None, ended_lengths=None,
+                    workspace=None, workspace_bytes=0, stream=None):
+    """beam_select of fp32 logits."""
+    _check(library().beam_select_f32(
+        _ptr(logits), row_stride, _ptr(scores), _ptr(lengths), B, beams, vocab, end, alpha,
+        _ptr(tokens), _ptr(parents), _ptr(new_scores), _ptr(ended_scores), _ptr(ended_rows),
+        _ptr(ended_lengths), _ptr(workspace), workspace_bytes, _stream(stream)), "beam_select_f32")
+
+
 def encoder_layer_workspace_bytes(B, n, d_model, h, d_k, d_ff) -> int:
     return int(library().encoder_layer_workspace_bytes(B, n, d_model, h, d_k, d_ff))
 
@@ -352,7 +458,7 @@ def mha_forward_noalloc(x_q, x_kv, w_q, w_k, w_v, w_o, out, B, n_q, n_k, d_model
 
 
 def attn_get_device_status(stream=None) -> int:
-    """Returns the status code (does not raise on ATTN_ERR_DEVICE_TIMEOUT)."""
+    """Returns the status code (does not raise on ATTN_ERR_DEVICE_*)."""
     return int(library().attn_get_device_status(_stream(stream)))
 
 

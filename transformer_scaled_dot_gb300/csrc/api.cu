@@ -24,6 +24,7 @@ attn_status cuda_fail(cudaError_t e) {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point, so the
 // library does not link libcuda directly.
@@ -738,6 +739,91 @@ attn_status run_decode_paged(const void* q, const void* k_cache, const void* k_s
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
+// Sizes and state of the entry points that keep a paged cache's pages.
+attn_status pages_check(int B, int n_pages, int page_size, int max_pages, const int32_t* table,
+                        const int32_t* counts) {
+  if (B < 0 || n_pages < 1 || max_pages < 1 || B > 65535) return ATTN_ERR_INVALID;
+  if (page_size < 1 || (page_size & (page_size - 1)) != 0) return ATTN_ERR_INVALID;
+  if (page_size < 16 || page_size > 256) return ATTN_ERR_UNSUPPORTED;
+  if (int64_t(max_pages) * page_size > tsd::kPagedMaxRows) return ATTN_ERR_UNSUPPORTED;
+  if (n_pages > tsd::kPagesMost) return ATTN_ERR_UNSUPPORTED;
+  if (!table || !counts || !aligned4(table) || !aligned4(counts)) return ATTN_ERR_INVALID;
+  return ATTN_OK;
+}
+
+attn_status run_cache_copy(void* k, void* k_scales, void* v, void* v_scales, bool q4,
+                           const int32_t* copies, const int32_t* n_copies, int max_copies,
+                           int n_layers, int64_t layer_rows, int h_kv, int d, int n_pages,
+                           int page_size, cudaStream_t stream) {
+  static const int32_t table = 0;
+  attn_status s = paged_check(0, h_kv, h_kv, 0, d, n_pages, page_size, 1, &table, nullptr, nullptr);
+  if (s != ATTN_OK) return s;
+  if (int64_t(h_kv) * page_size * d * 2 > tsd::kCopyMostPageBytes) return ATTN_ERR_UNSUPPORTED;
+  if (max_copies < 0 || n_layers < 0 || n_layers > 65535) return ATTN_ERR_INVALID;
+  const int64_t rows = int64_t(n_pages) * h_kv * page_size;
+  if (n_layers > 1 && (layer_rows < rows || layer_rows % 16 != 0 ||
+                       layer_rows > (int64_t(1) << 50) / n_layers))
+    return ATTN_ERR_INVALID;
+  s = pool_check(k, v, k_scales, v_scales, q4, 1.f, 1.f);
+  if (s != ATTN_OK) return s;
+  if (!copies || !aligned4(copies) || !aligned4(n_copies)) return ATTN_ERR_INVALID;
+  if (max_copies == 0 || n_layers == 0) return ATTN_OK;
+  tsd::CopyProblem p;
+  std::memset(&p, 0, sizeof(p));
+  void* const pools[4] = {k, v, k_scales, v_scales};
+  p.n_pools = q4 ? 4 : 2;
+  for (int i = 0; i < p.n_pools; ++i) {
+    p.pool[i] = pools[i];
+    p.row_bytes[i] = !q4 ? 2 * d : i < 2 ? d / 2 : d / 16;
+  }
+  p.n_layers = n_layers;
+  p.layer_rows = n_layers > 1 ? layer_rows : 0;
+  p.copies = copies;
+  p.n_copies = n_copies;
+  p.max_copies = max_copies;
+  p.h_kv = h_kv;
+  p.n_pages = n_pages;
+  p.page_shift = log2_int(page_size);
+  cudaError_t e = tsd::launch_cache_copy(p, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+// Sizes of a beam selection.
+attn_status beam_size_check(int B, int beams, int vocab) {
+  if (B < 0 || beams < 1 || vocab < 1) return ATTN_ERR_INVALID;
+  if (beams > tsd::kBeamMaxBeams || vocab > tsd::kBeamMaxVocab) return ATTN_ERR_UNSUPPORTED;
+  const int64_t tiles = (int64_t(vocab) + tsd::kBeamTile - 1) / tsd::kBeamTile;
+  if (int64_t(B) * beams * tiles > INT32_MAX - 64) return ATTN_ERR_UNSUPPORTED;
+  return ATTN_OK;
+}
+
+attn_status run_beam_select(const void* logits, bool f32, int64_t row_stride, const float* scores,
+                            const int32_t* lengths, int B, int beams, int vocab, int end,
+                            float alpha, int32_t* tokens, int32_t* parents, float* new_scores,
+                            float* ended_scores, int32_t* ended_rows, int32_t* ended_lengths,
+                            void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  attn_status s = beam_size_check(B, beams, vocab);
+  if (s != ATTN_OK) return s;
+  if (row_stride < vocab || row_stride > INT64_MAX / 8 / (int64_t(B) * beams + 1)) return ATTN_ERR_INVALID;
+  if (end < -1 || !std::isfinite(alpha)) return ATTN_ERR_INVALID;
+  if (!logits || (reinterpret_cast<uintptr_t>(logits) & (f32 ? 3u : 1u))) return ATTN_ERR_INVALID;
+  for (const void* p : {static_cast<const void*>(scores), static_cast<const void*>(tokens),
+                        static_cast<const void*>(parents), static_cast<const void*>(new_scores)})
+    if (!p || !aligned4(p)) return ATTN_ERR_INVALID;
+  if (end >= 0)
+    for (const void* p : {static_cast<const void*>(lengths), static_cast<const void*>(ended_scores),
+                          static_cast<const void*>(ended_rows), static_cast<const void*>(ended_lengths)})
+      if (!p || !aligned4(p)) return ATTN_ERR_INVALID;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < beam_select_workspace_bytes(B, beams, vocab))
+    return ATTN_ERR_INVALID;
+  if (B == 0) return ATTN_OK;
+  const tsd::BeamProblem p = {logits, f32, row_stride, scores, lengths, B, beams, vocab, end, alpha,
+                              tokens, parents, new_scores, ended_scores, ended_rows, ended_lengths,
+                              workspace};
+  cudaError_t e = tsd::launch_beam_select(p, stream);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
 // Staging regions of the host-buffer entry points, 256-byte aligned, in
 // order; the device entry point's own workspace follows them.
 struct StageLayout {
@@ -1159,6 +1245,121 @@ attn_status attn_decode_paged_q4(const void* q, const void* k_codes, const void*
                           reinterpret_cast<cudaStream_t>(stream));
 }
 
+size_t attn_cache_pages_workspace_bytes(int B, int n_pages) {
+  if (B < 0 || B > 65535 || n_pages < 1 || n_pages > tsd::kPagesMost) return 0;
+  return align256(size_t(n_pages) * 4) * 2;
+}
+
+attn_status attn_cache_fork(int32_t* page_table, int32_t* cache_lens, int32_t* ref_counts,
+                            const int32_t* parents, int B, int n_pages, int max_pages,
+                            tsd_stream_t stream) {
+  attn_status s = pages_check(B, n_pages, 16, max_pages, page_table, ref_counts);
+  if (s != ATTN_OK) return s;
+  if (!parents || !aligned4(parents) || !aligned4(cache_lens)) return ATTN_ERR_INVALID;
+  if (B > tsd::kForkMaxRows) return ATTN_ERR_UNSUPPORTED;
+  if (B == 0) return ATTN_OK;
+  cudaError_t e = tsd::launch_cache_fork({page_table, ref_counts, B, n_pages, 4, max_pages}, cache_lens,
+                                         parents, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status attn_cache_release(int32_t* page_table, int32_t* ref_counts, const int32_t* keep_lens,
+                               int B, int n_pages, int page_size, int max_pages,
+                               tsd_stream_t stream) {
+  attn_status s = pages_check(B, n_pages, page_size, max_pages, page_table, ref_counts);
+  if (s != ATTN_OK) return s;
+  if (!aligned4(keep_lens)) return ATTN_ERR_INVALID;
+  if (B == 0) return ATTN_OK;
+  cudaError_t e = tsd::launch_cache_release({page_table, ref_counts, B, n_pages, log2_int(page_size), max_pages},
+                                            keep_lens, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status attn_cache_reserve(int32_t* page_table, int32_t* ref_counts, const int32_t* cache_lens,
+                               const int32_t* new_lens, int32_t* copies, int32_t* n_copies,
+                               int32_t* n_missing, int B, int n_new, int n_pages, int page_size,
+                               int max_pages, void* workspace, size_t workspace_bytes,
+                               tsd_stream_t stream) {
+  attn_status s = pages_check(B, n_pages, page_size, max_pages, page_table, ref_counts);
+  if (s != ATTN_OK) return s;
+  if (n_new < 0 || !cache_lens || !aligned4(cache_lens) || !aligned4(new_lens)) return ATTN_ERR_INVALID;
+  for (const int32_t* p : {copies, n_copies, n_missing})
+    if (!p || !aligned4(p)) return ATTN_ERR_INVALID;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < attn_cache_pages_workspace_bytes(B, n_pages))
+    return ATTN_ERR_INVALID;
+  if (B == 0) return ATTN_OK;
+  const tsd::ReserveProblem p = {{page_table, ref_counts, B, n_pages, log2_int(page_size), max_pages},
+                                 cache_lens, new_lens, n_new, copies, n_copies, n_missing,
+                                 static_cast<int32_t*>(workspace)};
+  cudaError_t e = tsd::launch_cache_reserve(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status attn_cache_compact(const int32_t* page_table, const int32_t* ref_counts,
+                               int32_t* table_out, int32_t* counts_out, int32_t* copies,
+                               int32_t* n_copies, int32_t* n_used, int B, int n_pages,
+                               int page_size, int max_pages, int max_copies, void* workspace,
+                               size_t workspace_bytes, tsd_stream_t stream) {
+  attn_status s = pages_check(B, n_pages, page_size, max_pages, page_table, ref_counts);
+  if (s != ATTN_OK) return s;
+  if (max_copies < 0) return ATTN_ERR_INVALID;
+  for (const int32_t* p : {table_out, counts_out, copies, n_copies, n_used})
+    if (!p || !aligned4(p)) return ATTN_ERR_INVALID;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < attn_cache_pages_workspace_bytes(B, n_pages))
+    return ATTN_ERR_INVALID;
+  int32_t* ws = static_cast<int32_t*>(workspace);
+  const tsd::CompactProblem p = {{const_cast<int32_t*>(page_table), const_cast<int32_t*>(ref_counts), B, n_pages,
+                                  log2_int(page_size), max_pages},
+                                 table_out, counts_out, copies, n_copies, n_used, max_copies, ws,
+                                 ws + align256(size_t(n_pages) * 4) / 4};
+  cudaError_t e = tsd::launch_cache_compact(p, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
+}
+
+attn_status attn_cache_copy(void* k_cache, void* v_cache, const int32_t* copies,
+                            const int32_t* n_copies, int max_copies, int n_layers,
+                            int64_t layer_rows, int h_kv, int d, int n_pages, int page_size,
+                            tsd_stream_t stream) {
+  return run_cache_copy(k_cache, nullptr, v_cache, nullptr, false, copies, n_copies, max_copies,
+                        n_layers, layer_rows, h_kv, d, n_pages, page_size,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status attn_cache_copy_q4(void* k_codes, void* k_scales, void* v_codes, void* v_scales,
+                               const int32_t* copies, const int32_t* n_copies, int max_copies,
+                               int n_layers, int64_t layer_rows, int h_kv, int d, int n_pages,
+                               int page_size, tsd_stream_t stream) {
+  return run_cache_copy(k_codes, k_scales, v_codes, v_scales, true, copies, n_copies, max_copies,
+                        n_layers, layer_rows, h_kv, d, n_pages, page_size,
+                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+size_t beam_select_workspace_bytes(int B, int beams, int vocab) {
+  if (beam_size_check(B, beams, vocab) != ATTN_OK) return 0;
+  const size_t tiles = (size_t(vocab) + tsd::kBeamTile - 1) / tsd::kBeamTile;
+  return align256(size_t(B) * beams * tiles * 8 + 1);
+}
+
+attn_status beam_select(const void* logits, int64_t row_stride, const float* scores,
+                        const int32_t* lengths, int B, int beams, int vocab, int end, float alpha,
+                        int32_t* tokens, int32_t* parents, float* new_scores, float* ended_scores,
+                        int32_t* ended_rows, int32_t* ended_lengths, void* workspace,
+                        size_t workspace_bytes, tsd_stream_t stream) {
+  return run_beam_select(logits, false, row_stride, scores, lengths, B, beams, vocab, end, alpha,
+                         tokens, parents, new_scores, ended_scores, ended_rows, ended_lengths,
+                         workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
+attn_status beam_select_f32(const float* logits, int64_t row_stride, const float* scores,
+                            const int32_t* lengths, int B, int beams, int vocab, int end,
+                            float alpha, int32_t* tokens, int32_t* parents, float* new_scores,
+                            float* ended_scores, int32_t* ended_rows, int32_t* ended_lengths,
+                            void* workspace, size_t workspace_bytes, tsd_stream_t stream) {
+  return run_beam_select(logits, true, row_stride, scores, lengths, B, beams, vocab, end, alpha,
+                         tokens, parents, new_scores, ended_scores, ended_rows, ended_lengths,
+                         workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
+}
+
 attn_status attn_get_device_status(tsd_stream_t stream) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e);
@@ -1173,15 +1374,17 @@ attn_status attn_get_device_status(tsd_stream_t stream) {
   unsigned int dec = 0;
   if (e == cudaSuccess) e = tsd::take_device_error_decode(&dec);
   m |= dec;
-  for (auto take : {tsd::take_device_error_append, tsd::take_device_error_paged}) {
+  for (auto take : {tsd::take_device_error_append, tsd::take_device_error_paged, tsd::take_device_error_beam,
+                    tsd::take_device_error_pages, tsd::take_device_error_copy}) {
     unsigned int w = 0;
     if (e == cudaSuccess) e = take(&w);
     m |= w;
   }
   if (e != cudaSuccess) return cuda_fail(e);
   m |= a | g | f;
-  if (m & ~tsd::kDeviceErrIndex) return ATTN_ERR_DEVICE_TIMEOUT;
-  return m ? ATTN_ERR_DEVICE_INDEX : ATTN_OK;
+  if (m & ~(tsd::kDeviceErrIndex | tsd::kDeviceErrValue)) return ATTN_ERR_DEVICE_TIMEOUT;
+  if (m & tsd::kDeviceErrIndex) return ATTN_ERR_DEVICE_INDEX;
+  return m ? ATTN_ERR_DEVICE_VALUE : ATTN_OK;
 }
 
 int attn_last_cuda_error(void) { return g_last_cuda_error; }
@@ -1194,6 +1397,7 @@ const char* attn_status_string(attn_status s) {
     case ATTN_ERR_CUDA: return "ATTN_ERR_CUDA";
     case ATTN_ERR_DEVICE_TIMEOUT: return "ATTN_ERR_DEVICE_TIMEOUT";
     case ATTN_ERR_DEVICE_INDEX: return "ATTN_ERR_DEVICE_INDEX";
+    case ATTN_ERR_DEVICE_VALUE: return "ATTN_ERR_DEVICE_VALUE";
   }
   return "ATTN_STATUS_UNKNOWN";
 }

@@ -250,9 +250,84 @@ cudaError_t launch_add_layernorm(const void* x, bool x_f32, const uint16_t* r,
                                  float* out32, int rows, int d_model, float eps,
                                  cudaStream_t stream);
 
+// One step of beam search over B sentences of `beams` hypotheses.
+constexpr int kBeamMaxBeams = 16;
+constexpr int kBeamMaxVocab = 1 << 20;
+constexpr int kBeamTile = 1024;  // logits to a record of the workspace (8 bytes)
+struct BeamProblem {
+  const void* logits;   // row b * beams + k, row_stride elements apart
+  bool f32;             // fp32 logits, else bf16
+  int64_t row_stride;
+  const float* scores;  // [B, beams]; -infinity: no live hypothesis
+  const int32_t* lengths;  // [B], with an end token
+  int B, beams, vocab;
+  int end;              // the end token, or -1
+  float alpha;
+  int32_t* tokens;      // [B, beams]
+  int32_t* parents;
+  float* new_scores;
+  float* ended_scores;  // [B, beams], with an end token
+  int32_t* ended_rows;
+  int32_t* ended_lengths;
+  void* workspace;
+};
+cudaError_t launch_beam_select(const BeamProblem& p, cudaStream_t stream);
+
+// Keeping a paged cache's pages: a table [B, max_pages] of page numbers (-1:
+// none) and how many entries of tables name each page (0: free).
+struct PagesProblem {
+  int32_t* table;
+  int32_t* counts;  // [n_pages]
+  int B, n_pages, page_shift, max_pages;
+};
+constexpr int kForkMaxRows = 32768;
+constexpr int kPagesMost = 1 << 30;
+cudaError_t launch_cache_fork(const PagesProblem& p, int32_t* lens, const int32_t* parents,
+                              cudaStream_t stream);
+cudaError_t launch_cache_release(const PagesProblem& p, const int32_t* keep_lens,
+                                 cudaStream_t stream);
+struct ReserveProblem {
+  PagesProblem pages;
+  const int32_t* lens;
+  const int32_t* new_lens;  // or null: n_new each
+  int n_new;
+  int32_t* copies;    // [B, 3]: from page, to page, rows
+  int32_t* n_copies;
+  int32_t* n_missing;
+  int32_t* free_ids;  // workspace [n_pages]
+};
+cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream);
+struct CompactProblem {
+  PagesProblem pages;  // read
+  int32_t* table_out;  // may be the table
+  int32_t* counts_out; // may be the counts
+  int32_t* copies;     // [max_copies, 3]
+  int32_t* n_copies;
+  int32_t* n_used;
+  int max_copies;
+  int32_t* moves;      // workspace [n_pages]: from and to of each move
+  int32_t* map;        // workspace [n_pages]
+};
+cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream);
+
+// Copies rows of pages of up to four pools (K and V rows, or codes and scales).
+struct CopyProblem {
+  void* pool[4];
+  int row_bytes[4];
+  int n_pools, n_layers;
+  int64_t layer_rows;  // rows from one layer's pool to the next
+  const int32_t* copies;
+  const int32_t* n_copies;  // or null: max_copies
+  int max_copies, h_kv, n_pages, page_shift;
+};
+constexpr int64_t kCopyMostPageBytes = 1ll << 30;  // of one pool's page
+cudaError_t launch_cache_copy(const CopyProblem& p, cudaStream_t stream);
+
 // Per-file device error words (read and cleared; see sm103.cuh). kDeviceErrIndex
-// is the bit of an index out of range; any other bit is a wait that ran out.
+// is the bit of an index out of range, kDeviceErrValue that of a NaN or
+// infinity; any other bit is a wait that ran out.
 constexpr unsigned int kDeviceErrIndex = 2u;
+constexpr unsigned int kDeviceErrValue = 4u;
 cudaError_t take_device_error_attn(unsigned int* value);
 cudaError_t take_device_error_decode(unsigned int* value);
 cudaError_t take_device_error_gemm(unsigned int* value);
@@ -261,6 +336,9 @@ cudaError_t take_device_error_fused(unsigned int* value);
 cudaError_t take_device_error_cross(unsigned int* value);
 cudaError_t take_device_error_append(unsigned int* value);
 cudaError_t take_device_error_paged(unsigned int* value);
+cudaError_t take_device_error_beam(unsigned int* value);
+cudaError_t take_device_error_pages(unsigned int* value);
+cudaError_t take_device_error_copy(unsigned int* value);
 
 // Failure-detection self test: a bounded wait on a barrier nobody arrives on.
 cudaError_t launch_wait_timeout_selftest(unsigned long long limit_ns, cudaStream_t stream);

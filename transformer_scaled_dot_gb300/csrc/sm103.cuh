@@ -24,8 +24,10 @@ static __device__ unsigned int g_device_error = 0u;
 enum : unsigned int {
   kErrWaitTimeout = 1u,
   kErrIndex = 2u,  // a page index or a position outside its table; the row was left out
+  kErrValue = 4u,  // a NaN or +infinity where none can be used; its row was left out
 };
-static_assert(kErrIndex == kDeviceErrIndex, "the word's bit that the API layer tells apart");
+static_assert(kErrIndex == kDeviceErrIndex && kErrValue == kDeviceErrValue,
+              "the word's bits that the API layer tells apart");
 
 // A wait that has not completed after this long is treated as a hang.
 // Legitimate waits in these kernels last microseconds.
@@ -267,6 +269,11 @@ __device__ __forceinline__ void st_async_f32x2(uint32_t cluster_addr, float a, f
           cluster_addr),
       "f"(a), "f"(b), "r"(cluster_bar)
       : "memory");
+}
+// A plain 8-byte store into another CTA's shared memory (`cluster_addr`, from
+// cluster_map), visible there after a cluster_sync().
+__device__ __forceinline__ void st_cluster_u64(uint32_t cluster_addr, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(cluster_addr), "l"(v) : "memory");
 }
 // Whole-cluster barrier (every thread of every CTA of the cluster), with
 // release / acquire ordering of shared and global memory.
@@ -515,6 +522,11 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
 // max(a, b, c) in one instruction
