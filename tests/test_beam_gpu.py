@@ -150,6 +150,28 @@ def test_largest_vocabulary(tsd, f32):
     check(s, x)
 
 
+@pytest.mark.parametrize("kind", ["one group", "five groups", "few tokens", "all alike"])
+def test_best_tokens_close_together(tsd, kind):
+    """The likely tokens all in tiles that lie 8 (of 1024 tokens) apart in one beam, which is how the
+    search for them is split: many more tiles pass its first look than have to."""
+    rng = np.random.default_rng(6)
+    K, V = 16, 1 << 20
+    s = Step(tsd, 1, K, V, True, 3 * 1024)
+    x = rng.standard_normal((1, K, V)).astype(np.float32) - 20
+    tile = np.arange(V) // 1024
+    if kind == "one group":
+        x[0, 2, tile % 8 == 5] += 25
+    elif kind == "five groups":
+        x[0, 9, tile % 8 < 5] += 25
+    elif kind == "few tokens":
+        x[0, :] = -np.inf
+        x[0, 3, (tile % 8 == 1) & (np.arange(V) % 1024 > 1021)] = 1 + rng.random(256)
+    else:
+        x[0, :] = 1.5
+    s.scores.copy_(dev_f32(-2 - 1e-3 * np.arange(K)[None]))
+    check(s, s.fill(x))
+
+
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("V,pad", [(700, 0), (5001, 0), (5000, 8), (40960, 0)])
 def test_ties_go_to_the_lowest_place(tsd, f32, V, pad):

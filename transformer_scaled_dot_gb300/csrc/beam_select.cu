@@ -19,8 +19,9 @@
 // and then the M pairs in them.
 // Totals that lie next to one another decide which token a beam takes: they
 // are formed and compared in 64 bits. Exponentials and a tile's sum are in 32,
-// relative to the tile's own maximum; tiles are joined in 64.
-#include <cuda_bf16.h>
+// relative to the tile's own maximum, as are the few tiles of a lane that joins
+// them; lanes are joined in 64.
+#include <cfloat>
 
 #include "kernels.h"
 #include "sm103.cuh"
@@ -44,6 +45,11 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
 // 32 logits of a lane. Aligned: 16-byte loads, lane l of load j holds the
 // consecutive ones from (32 j + l) * (16 / size); otherwise one logit to a
 // load, number 32 j + l. Past the row's end -infinity.
+template <bool F32, bool ALIGNED>
+__device__ __forceinline__ int tile_place(int t, int i, int lane) {
+  constexpr int kPer = F32 ? 4 : 8;
+  return t * kTile + (ALIGNED ? (i / kPer * 32 + lane) * kPer + i % kPer : i * 32 + lane);
+}
 template <bool F32, bool ALIGNED>
 __device__ __forceinline__ void load_tile(const void* row, int t, int vocab, int lane, float (&x)[32]) {
   const int base = t * kTile;
@@ -128,49 +134,57 @@ __global__ void __launch_bounds__(32 * kTileWarps)
   if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = make_float2(top, s);
 }
 
-struct Best {
-  double total;
-  int at;
-};
-// Whether a is ahead of b: by total, then by place. Neither is a NaN.
-__device__ __forceinline__ bool ahead(const Best& a, const Best& b) {
-  return a.total > b.total || (a.total == b.total && a.at < b.at);
+// Totals of 64 bits as whole numbers in the same order; 0: none.
+__device__ __forceinline__ uint64_t order_key(double total) {
+  const int64_t bits = __double_as_longlong(total + 0.0);  // -0 is 0
+  return static_cast<uint64_t>(bits < 0 ? ~bits : bits | INT64_MIN);
 }
+__device__ __forceinline__ double key_total(uint64_t key) {
+  const int64_t bits = static_cast<int64_t>(key);
+  return __longlong_as_double(bits < 0 ? bits & INT64_MAX : ~bits);
+}
+// Whether a is ahead of b: by total, then by place.
+__device__ __forceinline__ bool ahead(uint64_t a_key, int a_at, uint64_t b_key, int b_at) {
+  return a_key > b_key || (a_key == b_key && a_at < b_at);
+}
+
+constexpr int kGroups = 128;    // of a sentence's tiles, each within a row
+constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
+constexpr int kTileList = 64;   // chosen tiles that are looked through
+constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
 
 struct PickSmem {
   // total = base + (logit - top): no digits are lost where logits are large
   double base[kBeamMaxBeams];  // s_k - log sum exp(x - top); -infinity: no live hypothesis
   double top[kBeamMaxBeams];   // the row's largest logit
-  Best warp_best[kPickWarps];
-  Best tiles[2 * kBeamMaxBeams];
-  Best pairs[2 * kBeamMaxBeams];
+  float least[kBeamMaxBeams];  // logits of this beam below it are not among the best
+  float group_top[kGroups];
+  int group_tile[kGroups];
+  uint64_t group_key[kGroups];
+  uint64_t last_key;           // the M-th best group's largest total, and its tile
+  int last_tile;
+  int n_tiles, n_pairs;
+  int tile[2 * kPickThreads];  // chosen tiles
+  uint64_t tile_key[2 * kPickThreads];
+  uint64_t pair_key[kPairList];
+  int pair_at[kPairList];
+  uint64_t best_key[2 * kBeamMaxBeams];
+  int best_at[2 * kBeamMaxBeams];
   float end_score[2 * kBeamMaxBeams];
   int end_row[kBeamMaxBeams];
 };
 
-// The best of all threads' `mine`, in every thread.
-__device__ __forceinline__ Best block_best(Best mine, PickSmem& sm) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Best other;
-    other.total = __shfl_xor_sync(0xffffffffu, mine.total, o);
-    other.at = __shfl_xor_sync(0xffffffffu, mine.at, o);
-    if (ahead(other, mine)) mine = other;
-  }
-  __syncthreads();
-  if (lane_id() == 0) sm.warp_best[warp_id()] = mine;
-  __syncthreads();
-  Best best = sm.warp_best[0];
-  for (int w = 1; w < kPickWarps; ++w)
-    if (ahead(sm.warp_best[w], best)) best = sm.warp_best[w];
-  return best;
+// Of n entries how many are ahead of entry i, by a warp.
+__device__ __forceinline__ int rank_of(const uint64_t* key, const int* at, int n, int i, int lane) {
+  int before = 0;
+  for (int j = lane; j < n; j += 32) before += ahead(key[j], at[j], key[i], at[i]);
+  return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
 }
 
-constexpr Best kNone = {-INFINITY, INT32_MAX};
-
-template <bool F32>
+template <bool F32, bool ALIGNED>
 __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProblem p, int tiles) {
-  __shared__ PickSmem sm;
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  PickSmem& sm = *reinterpret_cast<PickSmem*>(smem_raw);
   griddep_wait();
   griddep_launch_dependents();
   const int b = static_cast<int>(blockIdx.x), K = p.beams;
@@ -178,27 +192,83 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   const int M = p.end >= 0 ? 2 * K : K;
   const float2* tile_stats = reinterpret_cast<const float2*>(p.workspace) + static_cast<int64_t>(b) * K * tiles;
 
+  // The largest logit of each group of tiles (of its lowest tile among equal
+  // ones): beam group / per_beam, every per_beam-th tile of its row. The loads
+  // do not wait for the log-sums.
+  const int per_beam = kGroups / K;
+  const int group = tid / kSubs, sub = tid % kSubs;
+  const int group_beam = group / per_beam;
+  float group_top = -INFINITY;
+  int group_tile = INT32_MAX;
+  if (group_beam < K && __ldcg(p.scores + b * K + group_beam) != -INFINITY) {
+    const float2* st = tile_stats + static_cast<int64_t>(group_beam) * tiles;
+#pragma unroll 4
+    for (int t = group % per_beam + per_beam * sub; t < tiles; t += per_beam * kSubs) {
+      const float x = __ldcg(&st[t].x);
+      if (x > group_top) {
+        group_top = x;
+        group_tile = group_beam * tiles + t;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < kSubs; o <<= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, group_top, o);
+    const int t = __shfl_xor_sync(0xffffffffu, group_tile, o);
+    if (x > group_top || (x == group_top && t < group_tile)) {
+      group_top = x;
+      group_tile = t;
+    }
+  }
+  if (sub == 0) {
+    sm.group_top[group] = group_top;
+    sm.group_tile[group] = group_tile;
+  }
+  if (tid == 0) {
+    sm.n_tiles = sm.n_pairs = 0;
+    sm.last_key = 0;
+    sm.last_tile = INT32_MAX;
+  }
+
+  // a row's log-sum, by a warp: eight tiles to a lane at a time
   if (warp < K) {
     const float score = __ldcg(p.scores + b * K + warp);
     double base = -INFINITY;
     if (score != -INFINITY) {
       const float2* st = tile_stats + static_cast<int64_t>(warp) * tiles;
-      float top = -INFINITY;
-      for (int t = lane; t < tiles; t += 32) top = max_nan(top, __ldcg(&st[t]).x);
+      float top = -INFINITY, sum = 0.f;
+      for (int t0 = 0; t0 < tiles; t0 += 256) {
+        float2 r[8];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        for (int j = 0; j < 8; ++j) {
+          const int t = t0 + j * 32 + lane;
+          r[j] = t < tiles ? __ldcg(&st[t]) : make_float2(-INFINITY, 0.f);
+        }
+        float now = top;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) now = max_nan(now, r[j].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) now = max_nan(now, __shfl_xor_sync(0xffffffffu, now, o));
+        if (!(now > -INFINITY && now < INFINITY)) {  // nothing yet, or no numbers
+          top = now;
+          continue;
+        }
+        auto weight = [&](float x) {
+          const float d = x - now;
+          return ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo));
+        };
+        sum *= weight(top);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[j].y, weight(r[j].x), sum);
+        top = now;
+      }
       if (!(top < INFINITY) || !(score < INFINITY)) {
         if (lane == 0) atomicOr(&g_device_error, kErrValue);
       } else if (top > -INFINITY) {
-        double sum = 0.0;
-        for (int t = lane; t < tiles; t += 32) {
-          const float2 r = __ldcg(&st[t]);
-          const float d = r.x - top;
-          sum += static_cast<double>(r.y * ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo)));
-        }
+        double all = sum;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        base = static_cast<double>(score) - log(sum);
+        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        base = static_cast<double>(score) - log(all);
         if (lane == 0) sm.top[warp] = top;
       }
     }
@@ -206,67 +276,151 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   }
   __syncthreads();
 
-  // the M tiles with the best maxima
-  const int n = K * tiles;  // at most 32 to a thread
-  uint32_t gone = 0u;
-  auto best_tile = [&]() {
-    Best best = kNone;
-    for (int j = 0, i = tid; i < n; ++j, i += kPickThreads) {
-      const int k = i / tiles;
-      if (sm.base[k] == -INFINITY || (gone >> j & 1u)) continue;
-      const Best one = {sm.base[k] + (__ldcg(&tile_stats[i]).x - sm.top[k]), i};
-      if (one.total > -INFINITY && ahead(one, best)) best = one;
+  // the groups' totals, and the M-th of them: the pairs that are ahead of it
+  // or are it include the M best, and lie in tiles of which the same holds
+  if (tid < kGroups) {
+    const int tile = sm.group_tile[tid];
+    uint64_t key = 0;
+    if (tile != INT32_MAX) {
+      const int k = tid / per_beam;
+      if (sm.base[k] > -INFINITY) key = order_key(sm.base[k] + (sm.group_top[tid] - sm.top[k]));
     }
-    return best;
+    sm.group_key[tid] = key;
+  }
+  __syncthreads();
+  for (int i = warp; i < kGroups; i += kPickWarps) {
+    if (sm.group_key[i] == 0) continue;
+    if (rank_of(sm.group_key, sm.group_tile, kGroups, i, lane) == M - 1) {
+      if (lane == 0) {
+        sm.last_key = sm.group_key[i];
+        sm.last_tile = sm.group_tile[i];
+      }
+      // lowered by what the sums may be off in 64 bits, and rounded down
+      if (lane < K) {
+        const double last = key_total(sm.group_key[i]), base = sm.base[lane], top = sm.top[lane];
+        sm.least[lane] = __double2float_rd(fma(-0x1p-49, fabs(last) + fabs(base) + fabs(top), last - base + top));
+      }
+    }
+  }
+  __syncthreads();
+  const uint64_t last_key = sm.last_key;
+  const int last_tile = sm.last_tile;
+
+  // those tiles. More than the list holds (the best ones in few groups): the
+  // best M of it are kept and it is filled again.
+  const int n = K * tiles;
+  auto keep_best_tiles = [&]() {
+    const int listed = sm.n_tiles;
+    for (int i = warp; i < listed; i += kPickWarps) {
+      const int rank = rank_of(sm.tile_key, sm.tile, listed, i, lane);
+      if (lane == 0 && rank < M) {
+        sm.best_key[rank] = sm.tile_key[i];
+        sm.best_at[rank] = sm.tile[i];
+      }
+    }
+    __syncthreads();
+    if (tid < M) {
+      sm.tile_key[tid] = sm.best_key[tid];
+      sm.tile[tid] = sm.best_at[tid];
+    }
+    if (tid == 0) sm.n_tiles = M;
+    __syncthreads();
   };
-  Best mine = best_tile();
-  for (int r = 0; r < M; ++r) {
-    const Best best = block_best(mine, sm);
-    if (tid == 0) sm.tiles[r] = best;
-    if (best.at != INT32_MAX && best.at % kPickThreads == tid) {
-      gone |= 1u << (best.at / kPickThreads);
-      mine = best_tile();
+  for (int i0 = 0; i0 < n; i0 += kPickThreads) {
+    const int i = i0 + tid, k = i / tiles;
+    if (i < n && sm.base[k] > -INFINITY) {
+      const float x = __ldcg(&tile_stats[i].x);
+      if (x > -INFINITY && (last_key == 0 || x >= sm.least[k])) {
+        const uint64_t key = order_key(sm.base[k] + (x - sm.top[k]));
+        if (!ahead(last_key, last_tile, key, i)) {
+          const int at = atomicAdd(&sm.n_tiles, 1);
+          sm.tile[at] = i;
+          sm.tile_key[at] = key;
+        }
+      }
+    }
+    if (i0 + kPickThreads < n || n > kTileList) {
+      __syncthreads();
+      const int listed = sm.n_tiles;
+      __syncthreads();
+      if (listed > (i0 + kPickThreads < n ? kPickThreads : kTileList)) keep_best_tiles();
     }
   }
   __syncthreads();
 
-  // the M best pairs in them: 2 M pairs to a thread
-  uint64_t taken = 0ull;
-  auto best_pair = [&]() {
-    Best best = kNone;
-    for (int j = 0; j < M * (kTile / kPickThreads); ++j) {
-      const int i = j * kPickThreads + tid;
-      const int tile = sm.tiles[i / kTile].at;
-      if (tile == INT32_MAX || (taken >> j & 1ull)) continue;
-      const int k = tile / tiles, v = tile % tiles * kTile + i % kTile;
-      if (v >= p.vocab) continue;
-      const int64_t at = (static_cast<int64_t>(b) * K + k) * p.row_stride + v;
-      const Best one = {sm.base[k] + (load_logit<F32>(p.logits, at) - sm.top[k]), k * p.vocab + v};
-      if (one.total > -INFINITY && ahead(one, best)) best = one;
-    }
-    return best;
-  };
-  mine = best_pair();
-  for (int r = 0; r < M; ++r) {
-    const Best best = block_best(mine, sm);
-    if (tid == 0) sm.pairs[r] = best;
-    if (best.at != INT32_MAX && best.at == mine.at) {
-      // its place among this thread's pairs
-      for (int j = 0; j < M * (kTile / kPickThreads); ++j) {
-        const int i = j * kPickThreads + tid;
-        const int tile = sm.tiles[i / kTile].at;
-        if (tile != INT32_MAX && tile / tiles * p.vocab + tile % tiles * kTile + i % kTile == best.at) taken |= 1ull << j;
+  // their pairs, a warp to a tile
+  const int listed = sm.n_tiles;
+  for (int i = warp; i < listed; i += kPickWarps) {
+    const int tile = sm.tile[i], k = tile / tiles, t = tile % tiles;
+    const uint8_t* row = static_cast<const uint8_t*>(p.logits) +
+                         (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
+    const float least = last_key == 0 ? -FLT_MAX : sm.least[k];
+    float x[32];
+    load_tile<F32, ALIGNED>(row, t, p.vocab, lane, x);
+    uint32_t in = 0u;  // of this lane's logits
+#pragma unroll
+    for (int j = 0; j < 32; ++j) in |= (x[j] >= least ? 1u : 0u) << j;
+    auto push = [&](int j) {
+      const int v = tile_place<F32, ALIGNED>(t, j, lane);
+      const int at = atomicAdd(&sm.n_pairs, 1);
+      sm.pair_key[at] = order_key(sm.base[k] + (load_logit<F32>(row, v) - sm.top[k]));
+      sm.pair_at[at] = k * p.vocab + v;
+    };
+    if (__reduce_add_sync(0xffffffffu, __popc(in)) <= static_cast<unsigned>(M)) {
+      for (; in != 0u; in &= in - 1u) push(__ffs(in) - 1);
+    } else {
+      // more than M, as with many equal logits: the best M one by one
+      for (int r = 0; r < M; ++r) {
+        float best = -INFINITY;
+        int best_j = 0, best_v = INT32_MAX;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const int v = tile_place<F32, ALIGNED>(t, j, lane);
+          if ((in >> j & 1u) && (x[j] > best || (x[j] == best && v < best_v))) {
+            best = x[j];
+            best_j = j;
+            best_v = v;
+          }
+        }
+        float top = best;
+        int top_v = best_v;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const float other = __shfl_xor_sync(0xffffffffu, top, o);
+          const int other_v = __shfl_xor_sync(0xffffffffu, top_v, o);
+          if (other > top || (other == top && other_v < top_v)) {
+            top = other;
+            top_v = other_v;
+          }
+        }
+        if (best_v == top_v) {
+          push(best_j);
+          in &= ~(1u << best_j);
+        }
       }
-      mine = best_pair();
+    }
+  }
+  __syncthreads();
+
+  // the best M in order
+  const int pairs = sm.n_pairs;
+  if (tid < 2 * kBeamMaxBeams) sm.best_at[tid] = INT32_MAX;
+  __syncthreads();
+  for (int i = warp; i < pairs; i += kPickWarps) {
+    const int rank = rank_of(sm.pair_key, sm.pair_at, pairs, i, lane);
+    if (lane == 0 && rank < M) {
+      sm.best_key[rank] = sm.pair_key[i];
+      sm.best_at[rank] = sm.pair_at[i];
     }
   }
   __syncthreads();
   if (warp != 0) return;
 
   // a lane to a candidate: the next beams
-  const Best mine_pair = lane < M ? sm.pairs[lane] : kNone;
-  const bool real = mine_pair.at != INT32_MAX;
-  const int beam = real ? mine_pair.at / p.vocab : 0, token = real ? mine_pair.at % p.vocab : 0;
+  const int pair = lane < M ? sm.best_at[lane] : INT32_MAX;
+  const bool real = pair != INT32_MAX;
+  const double pair_total = real ? key_total(sm.best_key[lane]) : 0.0;
+  const int beam = real ? pair / p.vocab : 0, token = real ? pair % p.vocab : 0;
   const bool ends = real && token == p.end;
   const uint32_t before = (1u << lane) - 1u;
   const uint32_t going = __ballot_sync(0xffffffffu, real && !ends), ending = __ballot_sync(0xffffffffu, ends);
@@ -274,7 +428,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (real && !ends && rank < K) {
     p.tokens[b * K + rank] = token;
     p.parents[b * K + rank] = b * K + beam;
-    p.new_scores[b * K + rank] = static_cast<float>(mine_pair.total);
+    p.new_scores[b * K + rank] = static_cast<float>(pair_total);
   }
   if (lane < K && lane >= __popc(going)) {  // no pair for this beam
     p.tokens[b * K + lane] = p.end >= 0 ? p.end : 0;
@@ -288,7 +442,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (ends) {
     const double norm = pow((5.0 + length) / 6.0, static_cast<double>(p.alpha));
     const int e = __popc(ending & before);  // below K: a beam ends once
-    sm.end_score[e] = static_cast<float>(mine_pair.total / norm);
+    sm.end_score[e] = static_cast<float>(pair_total / norm);
     sm.end_row[e] = b * K + beam;
   }
   __syncwarp();
@@ -319,23 +473,26 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (lane < K && lane >= held) p.ended_scores[b * K + lane] = -INFINITY;
 }
 
-template <bool F32>
-cudaError_t launch_type(const BeamProblem& p, cudaStream_t stream) {
+template <bool F32, bool ALIGNED>
+cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   const int tiles = (p.vocab + kTile - 1) / kTile;
   const int total = p.B * p.beams * tiles;
-  const int per = F32 ? 4 : 8;
-  const bool aligned = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.row_stride % per == 0;
-  const dim3 grid(static_cast<unsigned>((total + kTileWarps - 1) / kTileWarps));
-  cudaError_t e = launch_pdl(aligned ? beam_tiles_kernel<F32, true> : beam_tiles_kernel<F32, false>, grid,
-                             dim3(32 * kTileWarps), 0, stream, p, tiles, total);
+  static unsigned long long configured = 0;
+  cudaError_t e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, sizeof(PickSmem), &configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(beam_pick_kernel<F32>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), 0, stream, p, tiles);
+  const dim3 grid(static_cast<unsigned>((total + kTileWarps - 1) / kTileWarps));
+  e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, grid, dim3(32 * kTileWarps), 0, stream, p, tiles, total);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), sizeof(PickSmem),
+                    stream, p, tiles);
 }
 
 }  // namespace
 
 cudaError_t launch_beam_select(const BeamProblem& p, cudaStream_t stream) {
-  return p.f32 ? launch_type<true>(p, stream) : launch_type<false>(p, stream);
+  const bool aligned = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && p.row_stride % (p.f32 ? 4 : 8) == 0;
+  if (p.f32) return aligned ? launch_variant<true, true>(p, stream) : launch_variant<true, false>(p, stream);
+  return aligned ? launch_variant<false, true>(p, stream) : launch_variant<false, false>(p, stream);
 }
 
 TSD_DEFINE_ERROR_READER(take_device_error_beam)
