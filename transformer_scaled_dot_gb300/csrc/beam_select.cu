@@ -18,9 +18,9 @@
 // block to a sentence, joins a row's tiles to its log-sum, picks those M tiles
 // and then the M pairs in them.
 // Totals that lie next to one another decide which token a beam takes: they
-// are formed and compared in 64 bits. Exponentials and a tile's sum are in 32,
-// relative to the tile's own maximum, as are the few tiles of a lane that joins
-// them; lanes are joined in 64.
+// are formed and compared as pairs of fp32, 48 bits. Exponentials and a tile's
+// sum are in 32, relative to the tile's own maximum, as are the few tiles of a
+// lane that joins them; lanes are joined in 48.
 #include <cfloat>
 
 #include "kernels.h"
@@ -134,33 +134,131 @@ __global__ void __launch_bounds__(32 * kTileWarps)
   if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = make_float2(top, s);
 }
 
-// Totals of 64 bits as whole numbers in the same order; 0: none.
-__device__ __forceinline__ uint64_t order_key(double total) {
-  const int64_t bits = __double_as_longlong(total + 0.0);  // -0 is 0
-  return static_cast<uint64_t>(bits < 0 ? ~bits : bits | INT64_MIN);
+// ---------------------------------------------------------------- pairs of fp32
+// A number as the unevaluated sum of two of 32 bits, the second at most half a
+// step of the first: 48 bits. Totals are kept so: 64-bit arithmetic has a
+// sixtieth of the rate here and many times the latency (with it a sentence's
+// choice took 13 us, 5 of them one logarithm and one power).
+
+struct Pair {
+  float h, l;
+};
+// a + b, exactly
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
 }
-__device__ __forceinline__ double key_total(uint64_t key) {
-  const int64_t bits = static_cast<int64_t>(key);
-  return __longlong_as_double(bits < 0 ? bits & INT64_MAX : ~bits);
+// h + l again with l at most half a step; |h| >= |l|, or h = 0
+__device__ __forceinline__ Pair settled(float h, float l) {
+  const float s = __fadd_rn(h, l);
+  return {s, __fsub_rn(l, __fsub_rn(s, h))};
+}
+__device__ __forceinline__ Pair add(Pair a, Pair b) {
+  const Pair s = two_sum(a.h, b.h);
+  return settled(s.h, s.l + (a.l + b.l));
+}
+
+// ln 2 in two parts, the first of 14 bits, so that its products with exponents are exact
+constexpr float kLn2Hi = 0x1.62e4p-1f, kLn2Lo = 1.4286068e-06f;
+
+// ln(x) for a normal x.h, off by less than 2^-28: with x = 2^e m, m within
+// sqrt(2) of 1, ln m = 2 atanh(z) = 2 (z + z^3 / 3 + z^5 / 5 + ..), z = (m - 1) / (m + 1),
+// whose first term is carried as a pair.
+__device__ __forceinline__ Pair log_pair(Pair x) {
+  const int bits = __float_as_int(x.h);
+  const int e = (bits - 0x3f3504f3) >> 23;  // sqrt(1/2) is 0x3f3504f3
+  const float m = __int_as_float(bits - (e << 23));
+  const float f = m - 1.f, d = 1.f + m, d_rest = m - (d - 1.f);
+  const float inverse = __frcp_rn(d);
+  const float z = f * inverse;
+  const float z_rest = (__fmaf_rn(-z, d, f) - z * d_rest) * inverse;
+  const float z2 = z * z;
+  float series = 1.f / 13.f;
+  series = __fmaf_rn(series, z2, 1.f / 11.f);
+  series = __fmaf_rn(series, z2, 1.f / 9.f);
+  series = __fmaf_rn(series, z2, 1.f / 7.f);
+  series = __fmaf_rn(series, z2, 1.f / 5.f);
+  series = __fmaf_rn(series, z2, 1.f / 3.f);
+  const float ef = static_cast<float>(e);
+  const Pair s = two_sum(ef * kLn2Hi, 2.f * z);
+  const float rest = 2.f * (z_rest + z * (z2 * series)) + __fdividef(x.l, x.h);
+  return settled(s.h, s.l + (rest + ef * kLn2Lo));
+}
+
+// exp(x) = value * 2^exponent, to 2^-25 of it, |x| <= 300: the Taylor series over
+// half of ln 2, its first two terms as a pair
+__device__ __forceinline__ Pair exp_pair(Pair x, int* exponent) {
+  const float k = rintf(x.h * kLog2eHi);
+  *exponent = static_cast<int>(k);
+  const Pair r = two_sum(__fmaf_rn(-k, kLn2Hi, x.h), x.l - k * kLn2Lo);
+  float series = 1.f / 40320.f;
+  series = __fmaf_rn(series, r.h, 1.f / 5040.f);
+  series = __fmaf_rn(series, r.h, 1.f / 720.f);
+  series = __fmaf_rn(series, r.h, 1.f / 120.f);
+  series = __fmaf_rn(series, r.h, 1.f / 24.f);
+  series = __fmaf_rn(series, r.h, 1.f / 6.f);
+  series = __fmaf_rn(series, r.h, 0.5f);
+  const Pair s = two_sum(1.f, r.h);
+  return settled(s.h, s.l + (r.l + r.h * r.h * series));
+}
+
+// The length penalty ((5 + n) / 6)^alpha as value * 2^exponent.
+__device__ __forceinline__ Pair length_penalty(int n, float alpha, int* exponent) {
+  const int64_t top = static_cast<int64_t>(n) + 5;
+  const float h = static_cast<float>(top);
+  constexpr float kLn6Hi = 0x1.cab0cp+0f, kLn6Lo = -2.1738742e-08f;
+  const Pair base = add(log_pair({h, static_cast<float>(top - static_cast<int64_t>(h))}), {-kLn6Hi, -kLn6Lo});
+  float x = alpha * base.h;
+  float rest = __fmaf_rn(alpha, base.h, -x) + alpha * base.l;
+  // e^300 and e^-300 take every score to 0 or beyond fp32 already
+  if (!(fabsf(x) < 300.f)) {
+    x = copysignf(300.f, x);
+    rest = 0.f;
+  }
+  return exp_pair(settled(x, rest), exponent);
+}
+
+// Pairs as whole numbers in the same order; 0: none.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 is 0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float from_order_bits(uint32_t u) {
+  return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u);
+}
+__device__ __forceinline__ Pair key_total(uint64_t key) {
+  return {from_order_bits(static_cast<uint32_t>(key >> 32)), from_order_bits(static_cast<uint32_t>(key))};
 }
 // Whether a is ahead of b: by total, then by place.
 __device__ __forceinline__ bool ahead(uint64_t a_key, int a_at, uint64_t b_key, int b_at) {
   return a_key > b_key || (a_key == b_key && a_at < b_at);
 }
 
-constexpr int kGroups = 128;    // of a sentence's tiles, each within a row
+// A beam: total = base + (logit - top), so that no digits are lost where
+// logits are large.
+struct Beam {
+  Pair base;  // s_k - log sum exp(x - top); h = -infinity: no live hypothesis
+  float top;  // the row's largest logit
+};
+// The key of a logit's total; 0 where it is no candidate.
+__device__ __forceinline__ uint64_t total_key(const Beam& beam, float x) {
+  const Pair d = two_sum(x, -beam.top);
+  const Pair s = two_sum(beam.base.h, d.h);
+  if (!(s.h > -INFINITY)) return 0;
+  const Pair t = settled(s.h, s.l + (beam.base.l + d.l));
+  return static_cast<uint64_t>(order_bits(t.h)) << 32 | order_bits(t.l);
+}
+
+constexpr int kGroups = 64;     // of a sentence's tiles
 constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
+constexpr int kHeld = 4;        // tiles that a thread keeps in registers
 constexpr int kTileList = 64;   // chosen tiles that are looked through
 constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
 
 struct PickSmem {
-  // total = base + (logit - top): no digits are lost where logits are large
-  double base[kBeamMaxBeams];  // s_k - log sum exp(x - top); -infinity: no live hypothesis
-  double top[kBeamMaxBeams];   // the row's largest logit
-  float least[kBeamMaxBeams];  // logits of this beam below it are not among the best
-  float group_top[kGroups];
-  int group_tile[kGroups];
+  Beam beam[kBeamMaxBeams];
   uint64_t group_key[kGroups];
+  int group_tile[kGroups];
   uint64_t last_key;           // the M-th best group's largest total, and its tile
   int last_tile;
   int n_tiles, n_pairs;
@@ -170,6 +268,8 @@ struct PickSmem {
   int pair_at[kPairList];
   uint64_t best_key[2 * kBeamMaxBeams];
   int best_at[2 * kBeamMaxBeams];
+  Pair penalty;
+  int penalty_exponent;
   float end_score[2 * kBeamMaxBeams];
   int end_row[kBeamMaxBeams];
 };
@@ -190,39 +290,18 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   const int b = static_cast<int>(blockIdx.x), K = p.beams;
   const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = static_cast<int>(lane_id());
   const int M = p.end >= 0 ? 2 * K : K;
-  const float2* tile_stats = reinterpret_cast<const float2*>(p.workspace) + static_cast<int64_t>(b) * K * tiles;
+  const int n = K * tiles;
+  const float2* tile_stats = reinterpret_cast<const float2*>(p.workspace) + static_cast<int64_t>(b) * n;
 
-  // The largest logit of each group of tiles (of its lowest tile among equal
-  // ones): beam group / per_beam, every per_beam-th tile of its row. The loads
-  // do not wait for the log-sums.
-  const int per_beam = kGroups / K;
-  const int group = tid / kSubs, sub = tid % kSubs;
-  const int group_beam = group / per_beam;
-  float group_top = -INFINITY;
-  int group_tile = INT32_MAX;
-  if (group_beam < K && __ldcg(p.scores + b * K + group_beam) != -INFINITY) {
-    const float2* st = tile_stats + static_cast<int64_t>(group_beam) * tiles;
-#pragma unroll 4
-    for (int t = group % per_beam + per_beam * sub; t < tiles; t += per_beam * kSubs) {
-      const float x = __ldcg(&st[t].x);
-      if (x > group_top) {
-        group_top = x;
-        group_tile = group_beam * tiles + t;
-      }
-    }
-  }
+  // This thread's tiles: a group's eight threads take every 64th tile, so that
+  // likely tokens that lie close together fall into different groups. The
+  // first loads do not wait for the log-sums.
+  const int first = tid % kSubs * kGroups + tid / kSubs;
+  float tile_top[kHeld];
 #pragma unroll
-  for (int o = 1; o < kSubs; o <<= 1) {
-    const float x = __shfl_xor_sync(0xffffffffu, group_top, o);
-    const int t = __shfl_xor_sync(0xffffffffu, group_tile, o);
-    if (x > group_top || (x == group_top && t < group_tile)) {
-      group_top = x;
-      group_tile = t;
-    }
-  }
-  if (sub == 0) {
-    sm.group_top[group] = group_top;
-    sm.group_tile[group] = group_tile;
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = first + j * kPickThreads;
+    tile_top[j] = i < n ? __ldcg(&tile_stats[i].x) : -INFINITY;
   }
   if (tid == 0) {
     sm.n_tiles = sm.n_pairs = 0;
@@ -233,73 +312,111 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   // a row's log-sum, by a warp: eight tiles to a lane at a time
   if (warp < K) {
     const float score = __ldcg(p.scores + b * K + warp);
-    double base = -INFINITY;
-    if (score != -INFINITY) {
-      const float2* st = tile_stats + static_cast<int64_t>(warp) * tiles;
-      float top = -INFINITY, sum = 0.f;
-      for (int t0 = 0; t0 < tiles; t0 += 256) {
-        float2 r[8];
+    const float2* st = tile_stats + static_cast<int64_t>(warp) * tiles;
+    float top = -INFINITY, sum = 0.f;
+    for (int t0 = 0; t0 < tiles; t0 += 256) {
+      float2 r[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = t0 + j * 32 + lane;
-          r[j] = t < tiles ? __ldcg(&st[t]) : make_float2(-INFINITY, 0.f);
-        }
-        float now = top;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) now = max_nan(now, r[j].x);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) now = max_nan(now, __shfl_xor_sync(0xffffffffu, now, o));
-        if (!(now > -INFINITY && now < INFINITY)) {  // nothing yet, or no numbers
-          top = now;
-          continue;
-        }
-        auto weight = [&](float x) {
-          const float d = x - now;
-          return ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo));
-        };
-        sum *= weight(top);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[j].y, weight(r[j].x), sum);
-        top = now;
+      for (int j = 0; j < 8; ++j) {
+        const int t = t0 + j * 32 + lane;
+        r[j] = t < tiles ? __ldcg(&st[t]) : make_float2(-INFINITY, 0.f);
       }
+      if (score == -INFINITY) break;  // what was loaded is no record
+      float now = top;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) now = max_nan(now, r[j].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) now = max_nan(now, __shfl_xor_sync(0xffffffffu, now, o));
+      if (!(now > -INFINITY && now < INFINITY)) {  // nothing yet, or no numbers
+        top = now;
+        continue;
+      }
+      auto weight = [&](float x) {
+        const float d = x - now;
+        return ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo));
+      };
+      sum *= weight(top);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[j].y, weight(r[j].x), sum);
+      top = now;
+    }
+    Beam beam = {{-INFINITY, 0.f}, 0.f};
+    if (score != -INFINITY) {
       if (!(top < INFINITY) || !(score < INFINITY)) {
         if (lane == 0) atomicOr(&g_device_error, kErrValue);
       } else if (top > -INFINITY) {
-        double all = sum;
+        Pair all = {sum, 0.f};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-        base = static_cast<double>(score) - log(all);
-        if (lane == 0) sm.top[warp] = top;
+        for (int o = 16; o > 0; o >>= 1)
+          all = add(all, {__shfl_xor_sync(0xffffffffu, all.h, o), __shfl_xor_sync(0xffffffffu, all.l, o)});
+        const Pair log_sum = log_pair(all);
+        beam = {add({score, 0.f}, {-log_sum.h, -log_sum.l}), top};
       }
     }
-    if (lane == 0) sm.base[warp] = base;
+    if (lane == 0) sm.beam[warp] = beam;
+  }
+  if (warp == kPickWarps - 1 && p.end >= 0) {
+    int exponent;
+    const Pair penalty = length_penalty(max(__ldcg(p.lengths + b), 1), p.alpha, &exponent);
+    if (lane == 0) {
+      sm.penalty = penalty;
+      sm.penalty_exponent = exponent;
+    }
   }
   __syncthreads();
 
-  // the groups' totals, and the M-th of them: the pairs that are ahead of it
-  // or are it include the M best, and lie in tiles of which the same holds
-  if (tid < kGroups) {
-    const int tile = sm.group_tile[tid];
-    uint64_t key = 0;
-    if (tile != INT32_MAX) {
-      const int k = tid / per_beam;
-      if (sm.base[k] > -INFINITY) key = order_key(sm.base[k] + (sm.group_top[tid] - sm.top[k]));
+  // The groups' best tiles, and the M-th of them: the tiles that are ahead of
+  // it, or are it, hold the M best pairs, and no pair behind it is one.
+  auto tile_key = [&](int i, float x) -> uint64_t {
+    if (!(x > -INFINITY)) return 0;
+    const Beam& beam = sm.beam[i / tiles];
+    return beam.base.h > -INFINITY ? total_key(beam, x) : 0;
+  };
+  uint64_t held_key[kHeld];
+  uint64_t group_key = 0;
+  int group_tile = INT32_MAX;
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    const int i = first + j * kPickThreads;
+    held_key[j] = i < n ? tile_key(i, tile_top[j]) : 0;
+    if (held_key[j] > group_key) {
+      group_key = held_key[j];
+      group_tile = i;
     }
-    sm.group_key[tid] = key;
+  }
+  for (int i = first + kHeld * kPickThreads; i < n; i += kPickThreads) {
+    const uint64_t key = tile_key(i, __ldcg(&tile_stats[i].x));
+    if (key > group_key) {
+      group_key = key;
+      group_tile = i;
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < kSubs; o <<= 1) {
+    const uint64_t key = __shfl_xor_sync(0xffffffffu, group_key, o);
+    const int tile = __shfl_xor_sync(0xffffffffu, group_tile, o);
+    if (ahead(key, tile, group_key, group_tile)) {
+      group_key = key;
+      group_tile = tile;
+    }
+  }
+  if (tid % kSubs == 0) {
+    sm.group_key[tid / kSubs] = group_key;
+    sm.group_tile[tid / kSubs] = group_tile;
   }
   __syncthreads();
-  for (int i = warp; i < kGroups; i += kPickWarps) {
-    if (sm.group_key[i] == 0) continue;
-    if (rank_of(sm.group_key, sm.group_tile, kGroups, i, lane) == M - 1) {
-      if (lane == 0) {
-        sm.last_key = sm.group_key[i];
-        sm.last_tile = sm.group_tile[i];
-      }
-      // lowered by what the sums may be off in 64 bits, and rounded down
-      if (lane < K) {
-        const double last = key_total(sm.group_key[i]), base = sm.base[lane], top = sm.top[lane];
-        sm.least[lane] = __double2float_rd(fma(-0x1p-49, fabs(last) + fabs(base) + fabs(top), last - base + top));
-      }
+  {
+    int before = 0;
+#pragma unroll
+    for (int j = 0; j < kGroups / kSubs; ++j) {
+      const int g = j * kSubs + tid % kSubs;
+      before += ahead(sm.group_key[g], sm.group_tile[g], group_key, group_tile);
+    }
+#pragma unroll
+    for (int o = 1; o < kSubs; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    if (before == M - 1 && group_key != 0 && tid % kSubs == 0) {
+      sm.last_key = group_key;
+      sm.last_tile = group_tile;
     }
   }
   __syncthreads();
@@ -308,7 +425,6 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 
   // those tiles. More than the list holds (the best ones in few groups): the
   // best M of it are kept and it is filled again.
-  const int n = K * tiles;
   auto keep_best_tiles = [&]() {
     const int listed = sm.n_tiles;
     for (int i = warp; i < listed; i += kPickWarps) {
@@ -326,27 +442,30 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     if (tid == 0) sm.n_tiles = M;
     __syncthreads();
   };
-  for (int i0 = 0; i0 < n; i0 += kPickThreads) {
-    const int i = i0 + tid, k = i / tiles;
-    if (i < n && sm.base[k] > -INFINITY) {
-      const float x = __ldcg(&tile_stats[i].x);
-      if (x > -INFINITY && (last_key == 0 || x >= sm.least[k])) {
-        const uint64_t key = order_key(sm.base[k] + (x - sm.top[k]));
-        if (!ahead(last_key, last_tile, key, i)) {
-          const int at = atomicAdd(&sm.n_tiles, 1);
-          sm.tile[at] = i;
-          sm.tile_key[at] = key;
-        }
-      }
-    }
-    if (i0 + kPickThreads < n || n > kTileList) {
-      __syncthreads();
-      const int listed = sm.n_tiles;
-      __syncthreads();
-      if (listed > (i0 + kPickThreads < n ? kPickThreads : kTileList)) keep_best_tiles();
-    }
+  auto list_tile = [&](int i, uint64_t key) {
+    if (key == 0 || ahead(last_key, last_tile, key, i)) return;
+    const int at = atomicAdd(&sm.n_tiles, 1);
+    sm.tile[at] = i;
+    sm.tile_key[at] = key;
+  };
+  auto shorten = [&](int most) {
+    __syncthreads();
+    const int listed = sm.n_tiles;
+    __syncthreads();
+    if (listed > most) keep_best_tiles();
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) {
+    if (j * kPickThreads >= n) break;
+    if (j > 0) shorten(kPickThreads);
+    list_tile(first + j * kPickThreads, held_key[j]);
   }
-  __syncthreads();
+  for (int i0 = kHeld * kPickThreads; i0 < n; i0 += kPickThreads) {
+    shorten(kPickThreads);
+    const int i = i0 + first;
+    if (i < n) list_tile(i, tile_key(i, __ldcg(&tile_stats[i].x)));
+  }
+  shorten(kTileList);
 
   // their pairs, a warp to a tile
   const int listed = sm.n_tiles;
@@ -354,7 +473,13 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     const int tile = sm.tile[i], k = tile / tiles, t = tile % tiles;
     const uint8_t* row = static_cast<const uint8_t*>(p.logits) +
                          (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
-    const float least = last_key == 0 ? -FLT_MAX : sm.least[k];
+    const Beam beam = sm.beam[k];
+    // Logits below `least` are not among the best: the logit at which the last
+    // group's total is reached, less what this sum of 32 bits may be off.
+    const float last = key_total(last_key).h;
+    const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
+    float least = (last - beam.base.h) + beam.top - slack;
+    if (last_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
     float x[32];
     load_tile<F32, ALIGNED>(row, t, p.vocab, lane, x);
     uint32_t in = 0u;  // of this lane's logits
@@ -362,8 +487,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     for (int j = 0; j < 32; ++j) in |= (x[j] >= least ? 1u : 0u) << j;
     auto push = [&](int j) {
       const int v = tile_place<F32, ALIGNED>(t, j, lane);
+      const uint64_t key = total_key(beam, load_logit<F32>(row, v));
+      if (key == 0) return;
       const int at = atomicAdd(&sm.n_pairs, 1);
-      sm.pair_key[at] = order_key(sm.base[k] + (load_logit<F32>(row, v) - sm.top[k]));
+      sm.pair_key[at] = key;
       sm.pair_at[at] = k * p.vocab + v;
     };
     if (__reduce_add_sync(0xffffffffu, __popc(in)) <= static_cast<unsigned>(M)) {
@@ -419,7 +546,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   // a lane to a candidate: the next beams
   const int pair = lane < M ? sm.best_at[lane] : INT32_MAX;
   const bool real = pair != INT32_MAX;
-  const double pair_total = real ? key_total(sm.best_key[lane]) : 0.0;
+  const Pair pair_total = real ? key_total(sm.best_key[lane]) : Pair{0.f, 0.f};
   const int beam = real ? pair / p.vocab : 0, token = real ? pair % p.vocab : 0;
   const bool ends = real && token == p.end;
   const uint32_t before = (1u << lane) - 1u;
@@ -428,7 +555,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (real && !ends && rank < K) {
     p.tokens[b * K + rank] = token;
     p.parents[b * K + rank] = b * K + beam;
-    p.new_scores[b * K + rank] = static_cast<float>(pair_total);
+    p.new_scores[b * K + rank] = pair_total.h;
   }
   if (lane < K && lane >= __popc(going)) {  // no pair for this beam
     p.tokens[b * K + lane] = p.end >= 0 ? p.end : 0;
@@ -440,9 +567,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   // the ended hypotheses: lanes below 16 hold the earlier ones, the others this step's
   const int length = max(__ldcg(p.lengths + b), 1);
   if (ends) {
-    const double norm = pow((5.0 + length) / 6.0, static_cast<double>(p.alpha));
+    // the quotient of two pairs, rounded once
+    const Pair by = sm.penalty;
+    const float q = __fdiv_rn(pair_total.h, by.h);
+    const float rest = __fmaf_rn(-q, by.h, pair_total.h) + (pair_total.l - q * by.l);
     const int e = __popc(ending & before);  // below K: a beam ends once
-    sm.end_score[e] = static_cast<float>(pair_total / norm);
+    sm.end_score[e] = ldexpf(q + __fdividef(rest, by.h), -sm.penalty_exponent);
     sm.end_row[e] = b * K + beam;
   }
   __syncwarp();
