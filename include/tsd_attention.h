@@ -767,8 +767,8 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  *
  *   logits      bf16, 2-byte aligned; element (row, v) at row * row_stride + v,
  *               row_stride >= vocab (16-byte aligned rows are faster)
- *   scores      fp32[B, beams]; -infinity: no hypothesis (its logits are not
- *               read). At a sentence's start: 0, and -infinity for the others
+ *   scores      fp32[B, beams]; -infinity: no hypothesis (whatever its logits
+ *               are). At a sentence's start: 0, and -infinity for the others
  *   lengths     int32[B]: tokens of the hypotheses, the one chosen now among
  *               them (less than 1 counts as 1)
  *   end         the end token, or -1: none; then lengths, alpha and the ended_*
@@ -782,13 +782,13 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  *               place: score, the row that the end token continued, and n. The
  *               caller starts with scores of -infinity; a place without a
  *               hypothesis has that and keeps the other two as they were
- *   1 <= beams <= 16, vocab <= 2^20, and B * beams * ceil(vocab / 1024) < 2^31 -
- *               64, else ATTN_ERR_UNSUPPORTED
+ *   1 <= beams <= 16, vocab <= 2^20, and B * beams * ceil(vocab / 1024) <= 2^31 -
+ *               2^20, else ATTN_ERR_UNSUPPORTED
  *   workspace   device, 16-byte aligned, >= beam_select_workspace_bytes(...)
  *               bytes of scratch (0 for sizes that the call refuses)
  * Logits of -infinity are tokens that are never chosen. A beam whose logits or
  * score hold a NaN or +infinity has no candidates, and attn_get_device_status
- * answers ATTN_ERR_DEVICE_VALUE once. Totals are formed and compared in 64 bits
+ * answers ATTN_ERR_DEVICE_VALUE once. Totals are formed and compared in 48 bits
  * from exponentials and partial sums in 32. beams = 1 is greedy decoding.
  * Errors as attn_forward. Two launches.
  */

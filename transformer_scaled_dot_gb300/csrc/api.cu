@@ -793,7 +793,7 @@ attn_status beam_size_check(int B, int beams, int vocab) {
   if (B < 0 || beams < 1 || vocab < 1) return ATTN_ERR_INVALID;
   if (beams > tsd::kBeamMaxBeams || vocab > tsd::kBeamMaxVocab) return ATTN_ERR_UNSUPPORTED;
   const int64_t tiles = (int64_t(vocab) + tsd::kBeamTile - 1) / tsd::kBeamTile;
-  if (int64_t(B) * beams * tiles > INT32_MAX - 64) return ATTN_ERR_UNSUPPORTED;
+  if (int64_t(B) * beams * tiles > tsd::kBeamMostTiles) return ATTN_ERR_UNSUPPORTED;
   return ATTN_OK;
 }
 

@@ -31,7 +31,7 @@ namespace tsd {
 namespace {
 
 constexpr int kTile = kBeamTile;          // logits of a warp's tile
-constexpr int kTileWarps = 8;             // warps of a beam_tiles block
+constexpr int kTileWarps = 4;             // warps of a beam_tiles block
 constexpr int kPickThreads = 512;
 constexpr int kPickWarps = kPickThreads / 32;
 static_assert(kPickWarps >= kBeamMaxBeams, "a warp joins a row's tiles");
@@ -42,47 +42,62 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at]) << 16);
 }
 
-// 32 logits of a lane. Aligned: 16-byte loads, lane l of load j holds the
-// consecutive ones from (32 j + l) * (16 / size); otherwise one logit to a
-// load, number 32 j + l. Past the row's end -infinity.
+// A lane's 32 logits of a tile. Aligned: 16-byte loads, lane l of load j holds
+// the consecutive ones from (32 j + l) * (16 / size); otherwise one logit to a
+// load, number 32 j + l. Past the row's end -infinity. They are loaded as they
+// lie in memory and unpacked when they are used, so that a warp has its next
+// tile under way.
 template <bool F32, bool ALIGNED>
-__device__ __forceinline__ int tile_place(int t, int i, int lane) {
-  constexpr int kPer = F32 ? 4 : 8;
-  return t * kTile + (ALIGNED ? (i / kPer * 32 + lane) * kPer + i % kPer : i * 32 + lane);
-}
-template <bool F32, bool ALIGNED>
-__device__ __forceinline__ void load_tile(const void* row, int t, int vocab, int lane, float (&x)[32]) {
-  const int base = t * kTile;
-  if constexpr (!ALIGNED) {
+struct Tile {
+  static constexpr int kPer = F32 ? 4 : 8;
+  static constexpr int kWords = F32 || !ALIGNED ? 32 : 16;
+  uint32_t w[kWords];
+
+  static __device__ __forceinline__ int place(int t, int i, int lane) {
+    return t * kTile + (ALIGNED ? (i / kPer * 32 + lane) * kPer + i % kPer : i * 32 + lane);
+  }
+  static __device__ __forceinline__ uint32_t one(const void* row, int v) {
+    return F32 ? static_cast<const uint32_t*>(row)[v] : static_cast<const uint16_t*>(row)[v];
+  }
+  __device__ __forceinline__ void load(const void* row, int t, int vocab, int lane) {
+    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80u;
+    if constexpr (!ALIGNED) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int v = base + j * 32 + lane;
-      x[j] = v < vocab ? load_logit<F32>(row, v) : -INFINITY;
-    }
-  } else {
-    constexpr int kPer = F32 ? 4 : 8;
+      for (int i = 0; i < 32; ++i) {
+        const int v = place(t, i, lane);
+        w[i] = v < vocab ? one(row, v) : kNone;
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < 32 / kPer; ++j) {
-      const int v = base + (j * 32 + lane) * kPer;
-      if (v + kPer <= vocab) {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(v) * (16 / kPer));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+      for (int j = 0; j < 32 / kPer; ++j) {
+        const int v = place(t, j * kPer, lane);
+        if (v + kPer <= vocab) {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(v) * (16 / kPer));
+          w[4 * j] = q.x;
+          w[4 * j + 1] = q.y;
+          w[4 * j + 2] = q.z;
+          w[4 * j + 3] = q.w;
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (F32) {
-            x[j * kPer + i] = __uint_as_float(u[i]);
-          } else {
-            x[j * kPer + 2 * i] = __uint_as_float(u[i] << 16);
-            x[j * kPer + 2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (F32) {
+              w[4 * j + i] = v + i < vocab ? one(row, v + i) : kNone;
+            } else {
+              const uint32_t lo = v + 2 * i < vocab ? one(row, v + 2 * i) : kNone;
+              const uint32_t hi = v + 2 * i + 1 < vocab ? one(row, v + 2 * i + 1) : kNone;
+              w[4 * j + i] = lo | hi << 16;
+            }
           }
         }
-      } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) x[j * kPer + i] = v + i < vocab ? load_logit<F32>(row, v + i) : -INFINITY;
       }
     }
   }
-}
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i]);
+    if constexpr (!ALIGNED) return __uint_as_float(w[i] << 16);
+    return __uint_as_float(i & 1 ? w[i / 2 % kWords] & 0xffff0000u : w[i / 2 % kWords] << 16);
+  }
+};
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
@@ -96,42 +111,62 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // log2(e) as two numbers of 32 bits
 constexpr float kLog2eHi = 1.4426950216293335f, kLog2eLo = 1.9259629911266175e-8f;
 
+// Persistent warps, each a tile at a time with the next one's loads in flight.
+// Of a beam without a hypothesis nothing is loaded but the first tile of a
+// warp, which does not wait for the score.
 template <bool F32, bool ALIGNED>
 __global__ void __launch_bounds__(32 * kTileWarps)
     beam_tiles_kernel(const BeamProblem p, int tiles, int total) {
   griddep_wait();
   griddep_launch_dependents();
-  const int id = static_cast<int>(blockIdx.x) * kTileWarps + warp_id();
-  if (id >= total) return;
   const int lane = static_cast<int>(lane_id());
-  const int row = id / tiles, t = id % tiles;
-  if (__ldcg(p.scores + row) == -INFINITY) return;  // no live hypothesis: beam_pick does not look here
-  const uint8_t* x_row = static_cast<const uint8_t*>(p.logits) + row * p.row_stride * (F32 ? 4 : 2);
-  float x[32];
-  load_tile<F32, ALIGNED>(x_row, t, p.vocab, lane, x);
-  float top = x[0];
+  const int step = static_cast<int>(gridDim.x) * kTileWarps;
+  int id = static_cast<int>(blockIdx.x) * kTileWarps + warp_id();
+  if (id >= total) return;
+  const int64_t row_bytes = p.row_stride * (F32 ? 4 : 2);
+  Tile<F32, ALIGNED> next;
+  auto load = [&](int i) {
+    const int row = i / tiles;
+    next.load(static_cast<const uint8_t*>(p.logits) + row * row_bytes, i - row * tiles, p.vocab, lane);
+  };
+  auto score = [&](int i) { return i < total ? __ldcg(p.scores + i / tiles) : -INFINITY; };
+  load(id);
+  float score0 = score(id), score1 = score(id + step);
+  while (id < total) {
+    const Tile<F32, ALIGNED> x = next;
+    const bool live = score0 != -INFINITY;
+    score0 = score1;
+    if (id + step < total) {  // no overflow: kBeamMostTiles
+      if (score0 != -INFINITY) load(id + step);
+      score1 = score(id + 2 * step);
+    }
+    if (live) {
+      float top = x.at(0);
 #pragma unroll
-  for (int i = 1; i < 31; i += 2) top = max3_nan(top, x[i], x[i + 1]);
-  top = max_nan(top, x[31]);
+      for (int i = 1; i < 31; i += 2) top = max3_nan(top, x.at(i), x.at(i + 1));
+      top = max_nan(top, x.at(31));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-  // the difference first, so that its rounding is its own (none for bf16 near the maximum)
-  const float m = top == -INFINITY ? 0.f : top;
-  const uint64_t neg = f2_pack(-m, -m), hi = f2_pack(kLog2eHi, kLog2eHi), lo = f2_pack(kLog2eLo, kLog2eLo);
-  uint64_t sum[2] = {0ull, 0ull};
+      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+      // the difference first, so that its rounding is its own (none for bf16 near the maximum)
+      const float m = top == -INFINITY ? 0.f : top;
+      const uint64_t neg = f2_pack(-m, -m), hi = f2_pack(kLog2eHi, kLog2eHi), lo = f2_pack(kLog2eLo, kLog2eLo);
+      uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const uint64_t d = fadd2(f2_pack(x[2 * i], x[2 * i + 1]), neg);
-    float a, b;
-    f2_unpack(ffma2(d, hi, fmul2(d, lo)), a, b);
-    sum[i & 1] = fadd2(sum[i & 1], f2_pack(ex2(a), ex2(b)));
+      for (int i = 0; i < 16; ++i) {
+        const uint64_t d = fadd2(f2_pack(x.at(2 * i), x.at(2 * i + 1)), neg);
+        float a, b;
+        f2_unpack(ffma2(d, hi, fmul2(d, lo)), a, b);
+        sum[i & 1] = fadd2(sum[i & 1], f2_pack(ex2(a), ex2(b)));
+      }
+      float a, b;
+      f2_unpack(fadd2(sum[0], sum[1]), a, b);
+      float s = a + b;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = make_float2(top, s);
+    }
+    id += step;
   }
-  float a, b;
-  f2_unpack(fadd2(sum[0], sum[1]), a, b);
-  float s = a + b;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = make_float2(top, s);
 }
 
 // ---------------------------------------------------------------- pairs of fp32
@@ -269,7 +304,7 @@ struct PickSmem {
   uint64_t best_key[2 * kBeamMaxBeams];
   int best_at[2 * kBeamMaxBeams];
   Pair penalty;
-  int penalty_exponent;
+  int penalty_exponent, length;
   float end_score[2 * kBeamMaxBeams];
   int end_row[kBeamMaxBeams];
 };
@@ -302,6 +337,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   for (int j = 0; j < kHeld; ++j) {
     const int i = first + j * kPickThreads;
     tile_top[j] = i < n ? __ldcg(&tile_stats[i].x) : -INFINITY;
+  }
+  // the hypotheses that ended before, for the last step
+  float ended = -INFINITY;
+  int end_row = 0, end_length = 0;
+  if (p.end >= 0 && tid < K) {
+    ended = __ldcg(p.ended_scores + b * K + tid);
+    end_row = __ldcg(p.ended_rows + b * K + tid);
+    end_length = __ldcg(p.ended_lengths + b * K + tid);
   }
   if (tid == 0) {
     sm.n_tiles = sm.n_pairs = 0;
@@ -357,8 +400,10 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   }
   if (warp == kPickWarps - 1 && p.end >= 0) {
     int exponent;
-    const Pair penalty = length_penalty(max(__ldcg(p.lengths + b), 1), p.alpha, &exponent);
+    const int length = max(__ldcg(p.lengths + b), 1);
+    const Pair penalty = length_penalty(length, p.alpha, &exponent);
     if (lane == 0) {
+      sm.length = length;
       sm.penalty = penalty;
       sm.penalty_exponent = exponent;
     }
@@ -367,9 +412,11 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 
   // The groups' best tiles, and the M-th of them: the tiles that are ahead of
   // it, or are it, hold the M best pairs, and no pair behind it is one.
+  // i / tiles: i is below 2^14, and (i + 1/2) / tiles at least 2^-11 off a whole number
+  const float per_tile = 1.f / static_cast<float>(tiles);
   auto tile_key = [&](int i, float x) -> uint64_t {
     if (!(x > -INFINITY)) return 0;
-    const Beam& beam = sm.beam[i / tiles];
+    const Beam& beam = sm.beam[static_cast<int>((static_cast<float>(i) + 0.5f) * per_tile)];
     return beam.base.h > -INFINITY ? total_key(beam, x) : 0;
   };
   uint64_t held_key[kHeld];
@@ -378,7 +425,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     const int i = first + j * kPickThreads;
-    held_key[j] = i < n ? tile_key(i, tile_top[j]) : 0;
+    held_key[j] = 0;
+    if (j * kPickThreads >= n) continue;
+    if (i < n) held_key[j] = tile_key(i, tile_top[j]);
     if (held_key[j] > group_key) {
       group_key = held_key[j];
       group_tile = i;
@@ -480,13 +529,13 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
     float least = (last - beam.base.h) + beam.top - slack;
     if (last_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
-    float x[32];
-    load_tile<F32, ALIGNED>(row, t, p.vocab, lane, x);
+    Tile<F32, ALIGNED> x;
+    x.load(row, t, p.vocab, lane);
     uint32_t in = 0u;  // of this lane's logits
 #pragma unroll
-    for (int j = 0; j < 32; ++j) in |= (x[j] >= least ? 1u : 0u) << j;
+    for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
     auto push = [&](int j) {
-      const int v = tile_place<F32, ALIGNED>(t, j, lane);
+      const int v = Tile<F32, ALIGNED>::place(t, j, lane);
       const uint64_t key = total_key(beam, load_logit<F32>(row, v));
       if (key == 0) return;
       const int at = atomicAdd(&sm.n_pairs, 1);
@@ -502,9 +551,9 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
         int best_j = 0, best_v = INT32_MAX;
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const int v = tile_place<F32, ALIGNED>(t, j, lane);
-          if ((in >> j & 1u) && (x[j] > best || (x[j] == best && v < best_v))) {
-            best = x[j];
+          const int v = Tile<F32, ALIGNED>::place(t, j, lane);
+          if ((in >> j & 1u) && (x.at(j) > best || (x.at(j) == best && v < best_v))) {
+            best = x.at(j);
             best_j = j;
             best_v = v;
           }
@@ -565,7 +614,6 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (p.end < 0) return;
 
   // the ended hypotheses: lanes below 16 hold the earlier ones, the others this step's
-  const int length = max(__ldcg(p.lengths + b), 1);
   if (ends) {
     // the quotient of two pairs, rounded once
     const Pair by = sm.penalty;
@@ -576,20 +624,15 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     sm.end_row[e] = b * K + beam;
   }
   __syncwarp();
-  float value = -INFINITY;
-  int end_row = 0, end_length = length;
-  if (lane < kBeamMaxBeams) {
-    if (lane < K) {
-      value = __ldcg(p.ended_scores + b * K + lane);
-      end_row = __ldcg(p.ended_rows + b * K + lane);
-      end_length = __ldcg(p.ended_lengths + b * K + lane);
-    }
-  } else if (lane - kBeamMaxBeams < __popc(ending)) {
+  float value = ended;
+  if (lane >= kBeamMaxBeams && lane - kBeamMaxBeams < __popc(ending)) {
     value = sm.end_score[lane - kBeamMaxBeams];
     end_row = sm.end_row[lane - kBeamMaxBeams];
+    end_length = sm.length;
   }
   if (!(value > -INFINITY)) value = -INFINITY;  // a NaN is no hypothesis
   int place = 0;
+#pragma unroll
   for (int j = 0; j < 32; ++j) {
     const float other = __shfl_sync(0xffffffffu, value, j);
     place += other > value || (other == value && j < lane);
@@ -610,7 +653,21 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   static unsigned long long configured = 0;
   cudaError_t e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, sizeof(PickSmem), &configured);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((total + kTileWarps - 1) / kTileWarps));
+  static int resident = 0;  // blocks on the device
+  int fit = __atomic_load_n(&resident, __ATOMIC_RELAXED);
+  if (fit == 0) {
+    int dev = 0, sms = 0, per_sm = 0;
+    e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess)
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, beam_tiles_kernel<F32, ALIGNED>, 32 * kTileWarps, 0);
+    if (e != cudaSuccess) return e;
+    fit = sms * per_sm;
+    __atomic_store_n(&resident, fit, __ATOMIC_RELAXED);
+  }
+  const int blocks = (total + kTileWarps - 1) / kTileWarps;
+  const dim3 grid(static_cast<unsigned>(blocks < fit ? blocks : fit));
+  static_assert(kBeamMostTiles <= INT32_MAX - 2 * 4 * 32768, "two rounds of any grid");
   e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, grid, dim3(32 * kTileWarps), 0, stream, p, tiles, total);
   if (e != cudaSuccess) return e;
   return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), sizeof(PickSmem),

@@ -254,6 +254,7 @@ cudaError_t launch_add_layernorm(const void* x, bool x_f32, const uint16_t* r,
 constexpr int kBeamMaxBeams = 16;
 constexpr int kBeamMaxVocab = 1 << 20;
 constexpr int kBeamTile = 1024;  // logits to a record of the workspace (8 bytes)
+constexpr int64_t kBeamMostTiles = (1ll << 31) - (1 << 20);  // two rounds of a grid further are whole numbers of 32 bits
 struct BeamProblem {
   const void* logits;   // row b * beams + k, row_stride elements apart
   bool f32;             // fp32 logits, else bf16
