@@ -68,10 +68,11 @@ struct Tile {
         w[i] = v < vocab ? one(row, v) : kNone;
       }
     } else {
+      const bool whole = (t + 1) * kTile <= vocab;
 #pragma unroll
       for (int j = 0; j < 32 / kPer; ++j) {
         const int v = place(t, j * kPer, lane);
-        if (v + kPer <= vocab) {
+        if (whole || v + kPer <= vocab) {
           const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(v) * (16 / kPer));
           w[4 * j] = q.x;
           w[4 * j + 1] = q.y;
@@ -108,8 +109,48 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
   return a;
 }
 
+// Over a warp: one instruction in place of five exchanges.
+__device__ __forceinline__ float warp_max_nan(float x) {
+  asm("redux.sync.max.NaN.f32 %0, %0, 0xffffffff;" : "+f"(x));
+  return x;
+}
+
 // log2(e) as two numbers of 32 bits
 constexpr float kLog2eHi = 1.4426950216293335f, kLog2eLo = 1.9259629911266175e-8f;
+
+// The largest logit of a warp's tile and the sum of exponentials relative to it.
+// 2^(x log2(e) - r), r = top log2(e) as fp32 has it, is one multiply-add; what r
+// is off by is made good in the sum. What is left is the constant's own
+// rounding, 2^-26 (x - top).
+template <bool F32, bool ALIGNED>
+__device__ __forceinline__ float2 tile_record(const Tile<F32, ALIGNED>& x) {
+  float top = x.at(0);
+#pragma unroll
+  for (int i = 1; i < 31; i += 2) top = max3_nan(top, x.at(i), x.at(i + 1));
+  top = warp_max_nan(max_nan(top, x.at(31)));
+  float s = 0.f, off = 0.f;
+  if (fabsf(top) < 1024.f) {  // r is off by 2^-14 at most
+    const float r = top * kLog2eHi;
+    const uint64_t neg = f2_pack(-r, -r), scale = f2_pack(kLog2eHi, kLog2eHi);
+    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float a, b;
+      f2_unpack(ffma2(f2_pack(x.at(2 * i), x.at(2 * i + 1)), scale, neg), a, b);
+      sum[i & 1] = fadd2(sum[i & 1], f2_pack(ex2(a), ex2(b)));
+    }
+    float a, b;
+    f2_unpack(fadd2(sum[0], sum[1]), a, b);
+    s = a + b;
+    off = __fmaf_rn(top, kLog2eHi, -r);  // the largest one's exponent
+  } else if (top > -INFINITY) {  // the differences first; a NaN or infinity among them
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += ex2((x.at(i) - top) * kLog2eHi);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return make_float2(top, __fmaf_rn(s, off * -0.693147181f, s));
+}
 
 // Persistent warps, each a tile at a time with the next one's loads in flight.
 // Of a beam without a hypothesis nothing is loaded but the first tile of a
@@ -124,48 +165,43 @@ __global__ void __launch_bounds__(32 * kTileWarps)
   int id = static_cast<int>(blockIdx.x) * kTileWarps + warp_id();
   if (id >= total) return;
   const int64_t row_bytes = p.row_stride * (F32 ? 4 : 2);
-  Tile<F32, ALIGNED> next;
-  auto load = [&](int i) {
-    const int row = i / tiles;
-    next.load(static_cast<const uint8_t*>(p.logits) + row * row_bytes, i - row * tiles, p.vocab, lane);
-  };
-  auto score = [&](int i) { return i < total ? __ldcg(p.scores + i / tiles) : -INFINITY; };
-  load(id);
-  float score0 = score(id), score1 = score(id + step);
-  while (id < total) {
-    const Tile<F32, ALIGNED> x = next;
-    const bool live = score0 != -INFINITY;
-    score0 = score1;
-    if (id + step < total) {  // no overflow: kBeamMostTiles
-      if (score0 != -INFINITY) load(id + step);
-      score1 = score(id + 2 * step);
+  const int step_rows = step / tiles, step_tiles = step - step_rows * tiles;
+  int row = id / tiles, t = id - row * tiles;  // of the tile to load next
+  auto advance = [&]() {
+    row += step_rows;
+    t += step_tiles;
+    if (t >= tiles) {
+      t -= tiles;
+      ++row;
     }
-    if (live) {
-      float top = x.at(0);
-#pragma unroll
-      for (int i = 1; i < 31; i += 2) top = max3_nan(top, x.at(i), x.at(i + 1));
-      top = max_nan(top, x.at(31));
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // the difference first, so that its rounding is its own (none for bf16 near the maximum)
-      const float m = top == -INFINITY ? 0.f : top;
-      const uint64_t neg = f2_pack(-m, -m), hi = f2_pack(kLog2eHi, kLog2eHi), lo = f2_pack(kLog2eLo, kLog2eLo);
-      uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint64_t d = fadd2(f2_pack(x.at(2 * i), x.at(2 * i + 1)), neg);
-        float a, b;
-        f2_unpack(ffma2(d, hi, fmul2(d, lo)), a, b);
-        sum[i & 1] = fadd2(sum[i & 1], f2_pack(ex2(a), ex2(b)));
-      }
-      float a, b;
-      f2_unpack(fadd2(sum[0], sum[1]), a, b);
-      float s = a + b;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = make_float2(top, s);
+  };
+  auto load = [&](Tile<F32, ALIGNED>& x) {
+    x.load(static_cast<const uint8_t*>(p.logits) + row * row_bytes, t, p.vocab, lane);
+  };
+  const int rows = p.B * p.beams;
+  // the scores of the tile at hand and of the next one
+  Tile<F32, ALIGNED> x, y;
+  load(x);
+  bool live = __ldcg(p.scores + row) != -INFINITY, next_live = false;
+  advance();
+  if (row < rows) next_live = __ldcg(p.scores + row) != -INFINITY;
+  // one tile: the next one's loads, this one's record; false at the end
+  auto turn = [&](Tile<F32, ALIGNED>& now, Tile<F32, ALIGNED>& then) {
+    const bool was_live = live;
+    live = next_live;
+    if (row < rows) {
+      if (live) load(then);
+      advance();
+      next_live = row < rows && __ldcg(p.scores + row) != -INFINITY;
+    }
+    if (was_live) {
+      const float2 record = tile_record(now);
+      if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = record;
     }
     id += step;
+    return id < total;
+  };
+  while (turn(x, y) && turn(y, x)) {
   }
 }
 
@@ -368,8 +404,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
       float now = top;
 #pragma unroll
       for (int j = 0; j < 8; ++j) now = max_nan(now, r[j].x);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) now = max_nan(now, __shfl_xor_sync(0xffffffffu, now, o));
+      now = warp_max_nan(now);
       if (!(now > -INFINITY && now < INFINITY)) {  // nothing yet, or no numbers
         top = now;
         continue;
