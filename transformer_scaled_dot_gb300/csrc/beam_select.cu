@@ -22,6 +22,7 @@
 // sum are in 32, relative to the tile's own maximum, as are the few tiles of a
 // lane that joins them; lanes are joined in 48.
 #include <cfloat>
+#include <cstddef>
 
 #include "kernels.h"
 #include "sm103.cuh"
@@ -33,6 +34,7 @@ namespace {
 constexpr int kTile = kBeamTile;          // logits of a warp's tile
 constexpr int kTileWarps = 4;             // warps of a beam_tiles block
 constexpr int kPickThreads = 512;
+constexpr unsigned long long kDrainLimitNs = 100ull * 1000ull * 1000ull;  // 0.1 s
 constexpr int kPickWarps = kPickThreads / 32;
 static_assert(kPickWarps >= kBeamMaxBeams, "a warp joins a row's tiles");
 
@@ -42,61 +44,122 @@ __device__ __forceinline__ float load_logit(const void* p, int64_t at) {
   return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[at]) << 16);
 }
 
-// A lane's 32 logits of a tile. Aligned: 16-byte loads, lane l of load j holds
-// the consecutive ones from (32 j + l) * (16 / size); otherwise one logit to a
-// load, number 32 j + l. Past the row's end -infinity. They are loaded as they
-// lie in memory and unpacked when they are used, so that a warp has its next
-// tile under way.
+// A lane's 32 logits of a tile, as they lie in memory, two of bf16 to a word.
+// ALIGNED: every row of the call starts on 16 bytes, and a lane's vector j holds
+// the consecutive logits from (32 j + l) * (16 / size); otherwise a word j those
+// from (32 j + l) * (4 / size). Which lane adds up a logit follows from its
+// number alone, so that equal rows have equal sums wherever they start. Past the
+// row's end -infinity.
 template <bool F32, bool ALIGNED>
 struct Tile {
-  static constexpr int kPer = F32 ? 4 : 8;
-  static constexpr int kWords = F32 || !ALIGNED ? 32 : 16;
+  static constexpr int kSize = F32 ? 4 : 2;
+  static constexpr int kPer = (ALIGNED ? 16 : 4) / kSize;  // consecutive logits of a lane
+  static constexpr int kWords = 32 * kSize / 4;
   uint32_t w[kWords];
 
   static __device__ __forceinline__ int place(int t, int i, int lane) {
-    return t * kTile + (ALIGNED ? (i / kPer * 32 + lane) * kPer + i % kPer : i * 32 + lane);
+    return t * kTile + (i / kPer * 32 + lane) * kPer + i % kPer;
   }
   static __device__ __forceinline__ uint32_t one(const void* row, int v) {
     return F32 ? static_cast<const uint32_t*>(row)[v] : static_cast<const uint16_t*>(row)[v];
   }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (F32) return __uint_as_float(w[i]);
+    return __uint_as_float(i & 1 ? w[i / 2 % kWords] & 0xffff0000u : w[i / 2 % kWords] << 16);
+  }
+  // what lies past the row's end
+  __device__ __forceinline__ void cut(int t, int vocab, int lane) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const bool past = place(t, i, lane) >= vocab;
+      uint32_t& word = w[F32 ? i : i / 2 % kWords];
+      if constexpr (F32) word = past ? 0xff800000u : word;
+      else if (i & 1) word = past ? (word & 0xffffu) | 0xff800000u : word;
+      else word = past ? (word & 0xffff0000u) | 0xff80u : word;
+    }
+  }
+  // straight from memory
   __device__ __forceinline__ void load(const void* row, int t, int vocab, int lane) {
-    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80u;
-    if constexpr (!ALIGNED) {
+    if constexpr (ALIGNED) {
+      if ((t + 1) * kTile <= vocab) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const int v = place(t, i, lane);
-        w[i] = v < vocab ? one(row, v) : kNone;
-      }
-    } else {
-      const bool whole = (t + 1) * kTile <= vocab;
-#pragma unroll
-      for (int j = 0; j < 32 / kPer; ++j) {
-        const int v = place(t, j * kPer, lane);
-        if (whole || v + kPer <= vocab) {
-          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(v) * (16 / kPer));
+        for (int j = 0; j < kWords / 4; ++j) {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) +
+                                                          static_cast<int64_t>(place(t, j * kPer, lane)) * kSize);
           w[4 * j] = q.x;
           w[4 * j + 1] = q.y;
           w[4 * j + 2] = q.z;
           w[4 * j + 3] = q.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (F32) {
-              w[4 * j + i] = v + i < vocab ? one(row, v + i) : kNone;
-            } else {
-              const uint32_t lo = v + 2 * i < vocab ? one(row, v + 2 * i) : kNone;
-              const uint32_t hi = v + 2 * i + 1 < vocab ? one(row, v + 2 * i + 1) : kNone;
-              w[4 * j + i] = lo | hi << 16;
-            }
-          }
         }
+        return;
       }
     }
+    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80u;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const int v = place(t, i, lane);
+      const uint32_t x = v < vocab ? one(row, v) : kNone;
+      if constexpr (F32) w[i] = x;
+      else w[i / 2 % kWords] = i & 1 ? w[i / 2 % kWords] | x << 16 : x;
+    }
   }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (F32) return __uint_as_float(w[i]);
-    if constexpr (!ALIGNED) return __uint_as_float(w[i] << 16);
-    return __uint_as_float(i & 1 ? w[i / 2 % kWords] & 0xffff0000u : w[i / 2 % kWords] << 16);
+};
+
+// A warp's ring of units of U tiles in shared memory, filled by bulk copies: one
+// thread starts 2 or 4 KB. They move 16-byte blocks of memory; a row that starts
+// `skew` bytes into one has one block more to a unit.
+template <bool F32, bool ALIGNED>
+struct Ring {
+  using T = Tile<F32, ALIGNED>;
+  static constexpr int kStages = 2;
+  static constexpr int U = F32 ? 1 : 2;
+  static constexpr int kUnit = U * kTile;
+  static constexpr int kUnitBytes = kUnit * T::kSize;
+  static constexpr int kStageBytes = kUnitBytes + 16;
+  alignas(16) uint8_t stage[kStages][kStageBytes];
+  uint64_t full[kStages];
+
+  static __device__ __forceinline__ int skew_of(const uint8_t* row) {
+    return ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) & 15u);
+  }
+  // Bytes of the copy of unit u, from `skew` bytes ahead of it; its first and
+  // last blocks may hold logits of other rows. 0, no copy, where they would lie
+  // outside of [begin, end), all rows' logits.
+  static __device__ __forceinline__ int bytes(const uint8_t* row, int u, int vocab, const uint8_t* begin, const uint8_t* end) {
+    const int skew = skew_of(row);
+    const int there = (vocab - u * kUnit) * T::kSize + skew;
+    const int n = min(kUnitBytes + (skew != 0 ? 16 : 0), (there + 15) & ~15);
+    const uint8_t* from = row + static_cast<int64_t>(u) * kUnitBytes - skew;
+    return from < begin || from + n > end ? 0 : n;
+  }
+  __device__ __forceinline__ void copy(int s, const uint8_t* row, int u, int n) {
+    mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(n));
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(stage[s])),
+                 "l"(row + static_cast<int64_t>(u) * kUnitBytes - skew_of(row)), "r"(n), "r"(smem_u32(&full[s]))
+                 : "memory");
+  }
+  static __device__ __forceinline__ void read(T& x, const uint8_t* stage, const uint8_t* row, int lane) {
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int j = 0; j < T::kWords / 4; ++j) {
+        const uint4 q = *reinterpret_cast<const uint4*>(stage + (j * 32 + lane) * 16);
+        x.w[4 * j] = q.x;
+        x.w[4 * j + 1] = q.y;
+        x.w[4 * j + 2] = q.z;
+        x.w[4 * j + 3] = q.w;
+      }
+    } else {
+      const int skew = skew_of(row);
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(stage + (skew & ~3)) + lane;
+      if (F32 || (skew & 3) == 0) {
+#pragma unroll
+        for (int j = 0; j < T::kWords; ++j) x.w[j] = words[j * 32];
+      } else {  // each pair from two words
+#pragma unroll
+        for (int j = 0; j < T::kWords; ++j) x.w[j] = __funnelshift_r(words[j * 32], words[j * 32 + 1], 16);
+      }
+    }
   }
 };
 
@@ -152,56 +215,124 @@ __device__ __forceinline__ float2 tile_record(const Tile<F32, ALIGNED>& x) {
   return make_float2(top, __fmaf_rn(s, off * -0.693147181f, s));
 }
 
-// Persistent warps, each a tile at a time with the next one's loads in flight.
-// Of a beam without a hypothesis nothing is loaded but the first tile of a
+// Persistent warps, each with a ring of two units of 4 KB, 24 warps to an SM.
+// 134 MB of bf16 in 25 to 26 us, of fp32 in 22, launch included (5.2 and 6.1 TB/s;
+// exponentials and all but the copies left out, 24 and 22). Loads by the lanes
+// instead: 29 us, 40 where rows are not aligned, and for fp32 25; 2 KB to a copy
+// and 4 stages 29; 8 KB 25, and slower where there are few tiles.
+// Of a beam without a hypothesis nothing is loaded but the first unit of a
 // warp, which does not wait for the score.
 template <bool F32, bool ALIGNED>
-__global__ void __launch_bounds__(32 * kTileWarps)
+__global__ void __launch_bounds__(32 * kTileWarps, 6)
     beam_tiles_kernel(const BeamProblem p, int tiles, int total) {
+  using R = Ring<F32, ALIGNED>;
+  constexpr int U = R::U;
+  using T = Tile<F32, ALIGNED>;
+  static_assert(sizeof(R) % 16 == 0 && R::kStageBytes % 16 == 0, "copies into shared memory start on 16 bytes");
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  R& ring = reinterpret_cast<R*>(smem_raw)[warp_id()];
+  __shared__ uint32_t abort_word;
+  volatile uint32_t* abort_flag = &abort_word;
+  const int lane = static_cast<int>(lane_id());
+  if (lane == 0) {
+    for (int i = 0; i < R::kStages; ++i) mbar_init(&ring.full[i], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) abort_word = 0;
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = static_cast<int>(lane_id());
   const int step = static_cast<int>(gridDim.x) * kTileWarps;
   int id = static_cast<int>(blockIdx.x) * kTileWarps + warp_id();
   if (id >= total) return;
-  const int64_t row_bytes = p.row_stride * (F32 ? 4 : 2);
-  const int step_rows = step / tiles, step_tiles = step - step_rows * tiles;
-  int row = id / tiles, t = id - row * tiles;  // of the tile to load next
-  auto advance = [&]() {
-    row += step_rows;
-    t += step_tiles;
-    if (t >= tiles) {
-      t -= tiles;
-      ++row;
-    }
-  };
-  auto load = [&](Tile<F32, ALIGNED>& x) {
-    x.load(static_cast<const uint8_t*>(p.logits) + row * row_bytes, t, p.vocab, lane);
-  };
   const int rows = p.B * p.beams;
-  // the scores of the tile at hand and of the next one
-  Tile<F32, ALIGNED> x, y;
-  load(x);
-  bool live = __ldcg(p.scores + row) != -INFINITY, next_live = false;
-  advance();
-  if (row < rows) next_live = __ldcg(p.scores + row) != -INFINITY;
-  // one tile: the next one's loads, this one's record; false at the end
-  auto turn = [&](Tile<F32, ALIGNED>& now, Tile<F32, ALIGNED>& then) {
-    const bool was_live = live;
-    live = next_live;
-    if (row < rows) {
-      if (live) load(then);
-      advance();
-      next_live = row < rows && __ldcg(p.scores + row) != -INFINITY;
-    }
-    if (was_live) {
-      const float2 record = tile_record(now);
-      if (lane == 0) reinterpret_cast<float2*>(p.workspace)[id] = record;
-    }
-    id += step;
-    return id < total;
+  const uint8_t* logits = static_cast<const uint8_t*>(p.logits);
+  const int64_t row_bytes = p.row_stride * (F32 ? 4 : 2);
+  const uint8_t* logits_end = logits + (rows - 1) * row_bytes + p.vocab * T::kSize;
+  const int units = (tiles + U - 1) / U;  // of a row
+  const int step_rows = step / units, step_units = step - step_rows * units;
+  struct At {
+    int row, u;
   };
-  while (turn(x, y) && turn(y, x)) {
+  auto next = [&](At at) {
+    at.row += step_rows;
+    at.u += step_units;
+    if (at.u >= units) {
+      at.u -= units;
+      ++at.row;
+    }
+    return at;
+  };
+  auto score = [&](const At& at) { return at.row < rows ? __ldcg(p.scores + at.row) : -INFINITY; };
+  At now = {id / units, id % units}, ahead = now;  // the unit at hand, and the next to copy
+  uint32_t under_way = 0u;  // bit s: a copy into stage s
+  auto copy = [&](int s, bool wanted) {
+    if (wanted) {
+      const uint8_t* row = logits + ahead.row * row_bytes;
+      const int n = R::bytes(row, ahead.u, p.vocab, logits, logits_end);
+      if (n > 0) {
+        under_way |= 1u << s;
+        if (lane == 0) ring.copy(s, row, ahead.u, n);
+      }
+    }
+    ahead = next(ahead);
+  };
+  copy(0, true);
+  At look = now;
+  float scores[R::kStages];
+#pragma unroll
+  for (int i = 0; i < R::kStages; ++i) {
+    scores[i] = score(look);
+    look = next(look);
+  }
+  float pending = score(look);  // of the unit after them; looked at a round later
+  look = next(look);
+  uint32_t live = 0u;  // bit i: the unit i after the one at hand has a hypothesis
+#pragma unroll
+  for (int i = 0; i < R::kStages; ++i) live |= (scores[i] != -INFINITY ? 1u : 0u) << i;
+#pragma unroll
+  for (int i = 1; i < R::kStages - 1; ++i) copy(i, live >> i & 1u);
+  uint32_t parity = 0u;  // bit s: of stage s
+  bool ok = true;
+  for (int s = 0; id < total; id += step) {
+    __syncwarp();  // the previous unit has been read
+    copy(s == 0 ? R::kStages - 1 : s - 1, live >> (R::kStages - 1) & 1u);
+    const bool wanted = live & 1u;
+    live = live >> 1 | (pending != -INFINITY ? 1u : 0u) << (R::kStages - 1);
+    pending = score(look);
+    look = next(look);
+    const uint8_t* row = logits + now.row * row_bytes;
+    const bool copied = under_way >> s & 1u;
+    if (copied) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ring.full[s], parity >> s & 1u, abort_flag));
+      if (!ok) break;
+      parity ^= 1u << s;
+      under_way &= ~(1u << s);
+    }
+    if (wanted) {
+#pragma unroll
+      for (int h = 0; h < U; ++h) {
+        const int t = now.u * U + h;
+        if (t >= tiles) break;
+        Tile<F32, ALIGNED> x;
+        if (copied) {
+          R::read(x, ring.stage[s] + h * kTile * T::kSize, row, lane);
+          if ((t + 1) * kTile > p.vocab) x.cut(t, p.vocab, lane);
+        } else {
+          x.load(row, t, p.vocab, lane);
+        }
+        const float2 record = tile_record(x);
+        if (lane == 0) reinterpret_cast<float2*>(p.workspace)[static_cast<int64_t>(now.row) * tiles + t] = record;
+      }
+    }
+    now = next(now);
+    s = s + 1 == R::kStages ? 0 : s + 1;
+  }
+  if (!ok) {
+    // this warp's copies still under way, a limited time
+    volatile uint32_t never = 0;
+    for (int s = 0; s < R::kStages; ++s)
+      if (under_way >> s & 1u) mbar_wait(&ring.full[s], parity >> s & 1u, &never, kDrainLimitNs);
   }
 }
 
@@ -683,10 +814,12 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 
 template <bool F32, bool ALIGNED>
 cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
+  using R = Ring<F32, ALIGNED>;
+  constexpr int kRingBytes = kTileWarps * static_cast<int>(sizeof(R));
   const int tiles = (p.vocab + kTile - 1) / kTile;
-  const int total = p.B * p.beams * tiles;
-  static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, sizeof(PickSmem), &configured);
+  static unsigned long long tiles_configured = 0, pick_configured = 0;
+  cudaError_t e = set_smem_once(beam_tiles_kernel<F32, ALIGNED>, kRingBytes, &tiles_configured);
+  if (e == cudaSuccess) e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, sizeof(PickSmem), &pick_configured);
   if (e != cudaSuccess) return e;
   static int resident = 0;  // blocks on the device
   int fit = __atomic_load_n(&resident, __ATOMIC_RELAXED);
@@ -695,15 +828,16 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
     e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, beam_tiles_kernel<F32, ALIGNED>, 32 * kTileWarps, 0);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, beam_tiles_kernel<F32, ALIGNED>, 32 * kTileWarps, kRingBytes);
     if (e != cudaSuccess) return e;
-    fit = sms * per_sm;
+    fit = sms * (per_sm > 0 ? per_sm : 1);
     __atomic_store_n(&resident, fit, __ATOMIC_RELAXED);
   }
+  const int total = p.B * p.beams * ((tiles + R::U - 1) / R::U);
   const int blocks = (total + kTileWarps - 1) / kTileWarps;
-  const dim3 grid(static_cast<unsigned>(blocks < fit ? blocks : fit));
-  static_assert(kBeamMostTiles <= INT32_MAX - 2 * 4 * 32768, "two rounds of any grid");
-  e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, grid, dim3(32 * kTileWarps), 0, stream, p, tiles, total);
+  static_assert(kBeamMostTiles <= INT32_MAX - 2 * kTileWarps * 32768, "two rounds of any grid");
+  e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(blocks < fit ? blocks : fit)),
+                 dim3(32 * kTileWarps), kRingBytes, stream, p, tiles, total);
   if (e != cudaSuccess) return e;
   return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), sizeof(PickSmem),
                     stream, p, tiles);
