@@ -453,7 +453,6 @@ __device__ __forceinline__ uint64_t total_key(const Beam& beam, float x) {
 
 constexpr int kGroups = 64;     // of a sentence's tiles
 constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
-constexpr int kHeld = 4;        // tiles that a thread keeps in registers
 constexpr int kTileList = 64;   // chosen tiles that are looked through
 constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
 
@@ -474,13 +473,47 @@ struct PickSmem {
   int penalty_exponent, length;
   float end_score[2 * kBeamMaxBeams];
   int end_row[kBeamMaxBeams];
+  // of every tile of the sentence first its record, then its largest total
+  uint64_t key[1];
 };
 
 // Of n entries how many are ahead of entry i, by a warp.
 __device__ __forceinline__ int rank_of(const uint64_t* key, const int* at, int n, int i, int lane) {
   int before = 0;
+#pragma unroll 1
   for (int j = lane; j < n; j += 32) before += ahead(key[j], at[j], key[i], at[i]);
   return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(before)));
+}
+
+// The M best of the listed tiles, at the list's front.
+__device__ __noinline__ void keep_best_tiles(PickSmem& sm, int M) {
+  const int warp = warp_id(), lane = static_cast<int>(lane_id()), tid = static_cast<int>(threadIdx.x);
+  const int listed = sm.n_tiles;
+#pragma unroll 1
+  for (int i = warp; i < listed; i += kPickWarps) {
+    const int rank = rank_of(sm.tile_key, sm.tile, listed, i, lane);
+    if (lane == 0 && rank < M) {
+      sm.best_key[rank] = sm.tile_key[i];
+      sm.best_at[rank] = sm.tile[i];
+    }
+  }
+  __syncthreads();
+  if (tid < M) {
+    sm.tile_key[tid] = sm.best_key[tid];
+    sm.tile[tid] = sm.best_at[tid];
+  }
+  if (tid == 0) sm.n_tiles = M;
+  __syncthreads();
+}
+
+// A sum of numbers of 0 .. 2^20 in all over a warp, off by 2^-25 at most: their parts
+// above and below 2^-6 as whole numbers, for which a warp has an instruction.
+__device__ __forceinline__ Pair warp_sum(float x) {
+  const float scaled = x * 64.f, whole = truncf(scaled);
+  const unsigned high = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(whole));
+  const unsigned low = __reduce_add_sync(0xffffffffu, static_cast<unsigned>((scaled - whole) * 0x1p24f));
+  const float h = static_cast<float>(high & 0xffffff00u);  // exact
+  return settled(h * 0x1p-6f, static_cast<float>(high & 0xffu) * 0x1p-6f + static_cast<float>(low) * 0x1p-30f);
 }
 
 template <bool F32, bool ALIGNED>
@@ -492,22 +525,15 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   const int b = static_cast<int>(blockIdx.x), K = p.beams;
   const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = static_cast<int>(lane_id());
   const int M = p.end >= 0 ? 2 * K : K;
-  const int n = K * tiles;
-  const float2* tile_stats = reinterpret_cast<const float2*>(p.workspace) + static_cast<int64_t>(b) * n;
+  const int n = K * tiles;  // below 2^14
+  const uint64_t* records = static_cast<const uint64_t*>(p.workspace) + static_cast<int64_t>(b) * n;
 
-  // This thread's tiles: a group's eight threads take every 64th tile, so that
-  // likely tokens that lie close together fall into different groups. The
-  // first loads do not wait for the log-sums.
-  const int first = tid % kSubs * kGroups + tid / kSubs;
-  float tile_top[kHeld];
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int i = first + j * kPickThreads;
-    tile_top[j] = i < n ? __ldcg(&tile_stats[i].x) : -INFINITY;
-  }
-  // the hypotheses that ended before, for the last step
-  float ended = -INFINITY;
+#pragma unroll 4
+  for (int i = tid; i < n; i += kPickThreads) sm.key[i] = __ldcg(reinterpret_cast<const unsigned long long*>(records) + i);
+  // what the last step needs
+  float score = -INFINITY, ended = -INFINITY;
   int end_row = 0, end_length = 0;
+  if (warp < K) score = __ldcg(p.scores + b * K + warp);
   if (p.end >= 0 && tid < K) {
     ended = __ldcg(p.ended_scores + b * K + tid);
     end_row = __ldcg(p.ended_rows + b * K + tid);
@@ -518,52 +544,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     sm.last_key = 0;
     sm.last_tile = INT32_MAX;
   }
-
-  // a row's log-sum, by a warp: eight tiles to a lane at a time
-  if (warp < K) {
-    const float score = __ldcg(p.scores + b * K + warp);
-    const float2* st = tile_stats + static_cast<int64_t>(warp) * tiles;
-    float top = -INFINITY, sum = 0.f;
-    for (int t0 = 0; t0 < tiles; t0 += 256) {
-      float2 r[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int t = t0 + j * 32 + lane;
-        r[j] = t < tiles ? __ldcg(&st[t]) : make_float2(-INFINITY, 0.f);
-      }
-      if (score == -INFINITY) break;  // what was loaded is no record
-      float now = top;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) now = max_nan(now, r[j].x);
-      now = warp_max_nan(now);
-      if (!(now > -INFINITY && now < INFINITY)) {  // nothing yet, or no numbers
-        top = now;
-        continue;
-      }
-      auto weight = [&](float x) {
-        const float d = x - now;
-        return ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo));
-      };
-      sum *= weight(top);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum = __fmaf_rn(r[j].y, weight(r[j].x), sum);
-      top = now;
-    }
-    Beam beam = {{-INFINITY, 0.f}, 0.f};
-    if (score != -INFINITY) {
-      if (!(top < INFINITY) || !(score < INFINITY)) {
-        if (lane == 0) atomicOr(&g_device_error, kErrValue);
-      } else if (top > -INFINITY) {
-        Pair all = {sum, 0.f};
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          all = add(all, {__shfl_xor_sync(0xffffffffu, all.h, o), __shfl_xor_sync(0xffffffffu, all.l, o)});
-        const Pair log_sum = log_pair(all);
-        beam = {add({score, 0.f}, {-log_sum.h, -log_sum.l}), top};
-      }
-    }
-    if (lane == 0) sm.beam[warp] = beam;
-  }
+  if (tid < 2 * kBeamMaxBeams) sm.best_at[tid] = INT32_MAX;
   if (warp == kPickWarps - 1 && p.end >= 0) {
     int exponent;
     const int length = max(__ldcg(p.lengths + b), 1);
@@ -576,31 +557,47 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   }
   __syncthreads();
 
-  // The groups' best tiles, and the M-th of them: the tiles that are ahead of
-  // it, or are it, hold the M best pairs, and no pair behind it is one.
+  // a row's log-sum, by a warp
+  if (warp < K) {
+    Beam beam = {{-INFINITY, 0.f}, 0.f};
+    if (score != -INFINITY) {
+      const float2* st = reinterpret_cast<const float2*>(sm.key) + warp * tiles;
+      float top = -INFINITY;
+      for (int t = lane; t < tiles; t += 32) top = max_nan(top, st[t].x);
+      top = warp_max_nan(top);
+      if (!(top < INFINITY) || !(score < INFINITY)) {
+        if (lane == 0) atomicOr(&g_device_error, kErrValue);
+      } else if (top > -INFINITY) {
+        float sum = 0.f;
+        for (int t = lane; t < tiles; t += 32) {
+          const float2 r = st[t];
+          const float d = r.x - top;
+          sum = __fmaf_rn(r.y, ex2(__fmaf_rn(d, kLog2eHi, d * kLog2eLo)), sum);
+        }
+        const Pair log_sum = log_pair(warp_sum(sum));
+        beam = {add({score, 0.f}, {-log_sum.h, -log_sum.l}), top};
+      }
+    }
+    if (lane == 0) sm.beam[warp] = beam;
+  }
+  __syncthreads();
+
+  // The tiles' largest totals, and the best of each group's: its eight threads
+  // take every 64th tile, so that likely tokens that lie close together fall into
+  // different groups.
   // i / tiles: i is below 2^14, and (i + 1/2) / tiles at least 2^-11 off a whole number
-  const float per_tile = 1.f / static_cast<float>(tiles);
-  auto tile_key = [&](int i, float x) -> uint64_t {
-    if (!(x > -INFINITY)) return 0;
-    const Beam& beam = sm.beam[static_cast<int>((static_cast<float>(i) + 0.5f) * per_tile)];
-    return beam.base.h > -INFINITY ? total_key(beam, x) : 0;
-  };
-  uint64_t held_key[kHeld];
+  const float per_tile = __fdividef(1.f, static_cast<float>(tiles));
   uint64_t group_key = 0;
   int group_tile = INT32_MAX;
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    const int i = first + j * kPickThreads;
-    held_key[j] = 0;
-    if (j * kPickThreads >= n) continue;
-    if (i < n) held_key[j] = tile_key(i, tile_top[j]);
-    if (held_key[j] > group_key) {
-      group_key = held_key[j];
-      group_tile = i;
+#pragma unroll 1
+  for (int i = tid % kSubs * kGroups + tid / kSubs; i < n; i += kPickThreads) {
+    const Beam& beam = sm.beam[static_cast<int>((static_cast<float>(i) + 0.5f) * per_tile)];
+    uint64_t key = 0;
+    if (beam.base.h > -INFINITY) {
+      const float x = reinterpret_cast<const float2*>(sm.key)[i].x;
+      if (x > -INFINITY) key = total_key(beam, x);
     }
-  }
-  for (int i = first + kHeld * kPickThreads; i < n; i += kPickThreads) {
-    const uint64_t key = tile_key(i, __ldcg(&tile_stats[i].x));
+    sm.key[i] = key;
     if (key > group_key) {
       group_key = key;
       group_tile = i;
@@ -620,6 +617,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     sm.group_tile[tid / kSubs] = group_tile;
   }
   __syncthreads();
+  // The M-th of them: the tiles that are ahead of it, or are it, hold the M best
+  // pairs, and no pair behind it is one.
   {
     int before = 0;
 #pragma unroll
@@ -640,54 +639,31 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 
   // those tiles. More than the list holds (the best ones in few groups): the
   // best M of it are kept and it is filled again.
-  auto keep_best_tiles = [&]() {
-    const int listed = sm.n_tiles;
-    for (int i = warp; i < listed; i += kPickWarps) {
-      const int rank = rank_of(sm.tile_key, sm.tile, listed, i, lane);
-      if (lane == 0 && rank < M) {
-        sm.best_key[rank] = sm.tile_key[i];
-        sm.best_at[rank] = sm.tile[i];
+#pragma unroll 1
+  for (int i = tid, left = n; left > 0; left -= kPickThreads, i += kPickThreads) {
+    if (i < n) {
+      const uint64_t key = sm.key[i];
+      if (key != 0 && !ahead(last_key, last_tile, key, i)) {
+        const int at = atomicAdd(&sm.n_tiles, 1);
+        sm.tile[at] = i;
+        sm.tile_key[at] = key;
       }
     }
     __syncthreads();
-    if (tid < M) {
-      sm.tile_key[tid] = sm.best_key[tid];
-      sm.tile[tid] = sm.best_at[tid];
-    }
-    if (tid == 0) sm.n_tiles = M;
-    __syncthreads();
-  };
-  auto list_tile = [&](int i, uint64_t key) {
-    if (key == 0 || ahead(last_key, last_tile, key, i)) return;
-    const int at = atomicAdd(&sm.n_tiles, 1);
-    sm.tile[at] = i;
-    sm.tile_key[at] = key;
-  };
-  auto shorten = [&](int most) {
-    __syncthreads();
-    const int listed = sm.n_tiles;
-    __syncthreads();
-    if (listed > most) keep_best_tiles();
-  };
-#pragma unroll
-  for (int j = 0; j < kHeld; ++j) {
-    if (j * kPickThreads >= n) break;
-    if (j > 0) shorten(kPickThreads);
-    list_tile(first + j * kPickThreads, held_key[j]);
+    const bool more = left > kPickThreads;
+    if (sm.n_tiles > (more ? kPickThreads : kTileList)) keep_best_tiles(sm, M);
+    if (more) __syncthreads();  // all have seen the count before it grows
   }
-  for (int i0 = kHeld * kPickThreads; i0 < n; i0 += kPickThreads) {
-    shorten(kPickThreads);
-    const int i = i0 + first;
-    if (i < n) list_tile(i, tile_key(i, __ldcg(&tile_stats[i].x)));
-  }
-  shorten(kTileList);
 
   // their pairs, a warp to a tile
   const int listed = sm.n_tiles;
+#pragma unroll 1
   for (int i = warp; i < listed; i += kPickWarps) {
     const int tile = sm.tile[i], k = tile / tiles, t = tile % tiles;
     const uint8_t* row = static_cast<const uint8_t*>(p.logits) +
                          (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
+    Tile<F32, ALIGNED> x;
+    x.load(row, t, p.vocab, lane);
     const Beam beam = sm.beam[k];
     // Logits below `least` are not among the best: the logit at which the last
     // group's total is reached, less what this sum of 32 bits may be off.
@@ -695,23 +671,14 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
     float least = (last - beam.base.h) + beam.top - slack;
     if (last_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
-    Tile<F32, ALIGNED> x;
-    x.load(row, t, p.vocab, lane);
     uint32_t in = 0u;  // of this lane's logits
 #pragma unroll
     for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
-    auto push = [&](int j) {
-      const int v = Tile<F32, ALIGNED>::place(t, j, lane);
-      const uint64_t key = total_key(beam, load_logit<F32>(row, v));
-      if (key == 0) return;
-      const int at = atomicAdd(&sm.n_pairs, 1);
-      sm.pair_key[at] = key;
-      sm.pair_at[at] = k * p.vocab + v;
-    };
-    if (__reduce_add_sync(0xffffffffu, __popc(in)) <= static_cast<unsigned>(M)) {
-      for (; in != 0u; in &= in - 1u) push(__ffs(in) - 1);
-    } else {
-      // more than M, as with many equal logits: the best M one by one
+    // more than M, as with many equal logits: the best M one by one
+    const bool crowded = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))) > static_cast<unsigned>(M);
+    if (crowded) {
+      uint32_t best_ones = 0u;
+#pragma unroll 1
       for (int r = 0; r < M; ++r) {
         float best = -INFINITY;
         int best_j = 0, best_v = INT32_MAX;
@@ -724,30 +691,30 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
             best_v = v;
           }
         }
-        float top = best;
-        int top_v = best_v;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          const float other = __shfl_xor_sync(0xffffffffu, top, o);
-          const int other_v = __shfl_xor_sync(0xffffffffu, top_v, o);
-          if (other > top || (other == top && other_v < top_v)) {
-            top = other;
-            top_v = other_v;
-          }
-        }
+        const float top = warp_max_nan(best);
+        const int top_v = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(best_v) : 0x7fffffffu));
         if (best_v == top_v) {
-          push(best_j);
+          best_ones |= 1u << best_j;
           in &= ~(1u << best_j);
         }
       }
+      in = best_ones;
+    }
+#pragma unroll 1
+    for (; in != 0u; in &= in - 1u) {
+      const int v = Tile<F32, ALIGNED>::place(t, __ffs(in) - 1, lane);
+      const uint64_t key = total_key(beam, load_logit<F32>(row, v));
+      if (key == 0) continue;
+      const int at = atomicAdd(&sm.n_pairs, 1);
+      sm.pair_key[at] = key;
+      sm.pair_at[at] = k * p.vocab + v;
     }
   }
   __syncthreads();
 
   // the best M in order
   const int pairs = sm.n_pairs;
-  if (tid < 2 * kBeamMaxBeams) sm.best_at[tid] = INT32_MAX;
-  __syncthreads();
+#pragma unroll 1
   for (int i = warp; i < pairs; i += kPickWarps) {
     const int rank = rank_of(sm.pair_key, sm.pair_at, pairs, i, lane);
     if (lane == 0 && rank < M) {
@@ -761,8 +728,8 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   // a lane to a candidate: the next beams
   const int pair = lane < M ? sm.best_at[lane] : INT32_MAX;
   const bool real = pair != INT32_MAX;
-  const Pair pair_total = real ? key_total(sm.best_key[lane]) : Pair{0.f, 0.f};
-  const int beam = real ? pair / p.vocab : 0, token = real ? pair % p.vocab : 0;
+  const Pair total = real ? key_total(sm.best_key[lane]) : Pair{0.f, 0.f};
+  const int beam = real ? pair / p.vocab : 0, token = real ? pair - beam * p.vocab : 0;
   const bool ends = real && token == p.end;
   const uint32_t before = (1u << lane) - 1u;
   const uint32_t going = __ballot_sync(0xffffffffu, real && !ends), ending = __ballot_sync(0xffffffffu, ends);
@@ -770,7 +737,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (real && !ends && rank < K) {
     p.tokens[b * K + rank] = token;
     p.parents[b * K + rank] = b * K + beam;
-    p.new_scores[b * K + rank] = pair_total.h;
+    p.new_scores[b * K + rank] = total.h;
   }
   if (lane < K && lane >= __popc(going)) {  // no pair for this beam
     p.tokens[b * K + lane] = p.end >= 0 ? p.end : 0;
@@ -781,12 +748,20 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 
   // the ended hypotheses: lanes below 16 hold the earlier ones, the others this step's
   if (ends) {
-    // the quotient of two pairs, rounded once
+    // the quotient of two pairs, rounded once, and the exponent in four steps
     const Pair by = sm.penalty;
-    const float q = __fdiv_rn(pair_total.h, by.h);
-    const float rest = __fmaf_rn(-q, by.h, pair_total.h) + (pair_total.l - q * by.l);
+    const float q = __fdividef(total.h, by.h);
+    const float rest = __fmaf_rn(-q, by.h, total.h) + (total.l - q * by.l);
+    float value = q + __fdividef(rest, by.h);
+    int exponent = -sm.penalty_exponent;  // within 433
+#pragma unroll
+    for (int j = 4; j > 0; --j) {
+      const int part = exponent / j;
+      value *= __int_as_float((127 + part) << 23);
+      exponent -= part;
+    }
     const int e = __popc(ending & before);  // below K: a beam ends once
-    sm.end_score[e] = ldexpf(q + __fdividef(rest, by.h), -sm.penalty_exponent);
+    sm.end_score[e] = value;
     sm.end_row[e] = b * K + beam;
   }
   __syncwarp();
@@ -817,9 +792,12 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   using R = Ring<F32, ALIGNED>;
   constexpr int kRingBytes = kTileWarps * static_cast<int>(sizeof(R));
   const int tiles = (p.vocab + kTile - 1) / kTile;
+  // the largest call's tiles
+  constexpr int kPickMost = static_cast<int>(sizeof(PickSmem)) + kBeamMaxBeams * (kBeamMaxVocab / kTile) * 8;
+  static_assert(kPickMost <= 227 * 1024, "shared memory of a block");
   static unsigned long long tiles_configured = 0, pick_configured = 0;
   cudaError_t e = set_smem_once(beam_tiles_kernel<F32, ALIGNED>, kRingBytes, &tiles_configured);
-  if (e == cudaSuccess) e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, sizeof(PickSmem), &pick_configured);
+  if (e == cudaSuccess) e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, kPickMost, &pick_configured);
   if (e != cudaSuccess) return e;
   static int resident = 0;  // blocks on the device
   int fit = __atomic_load_n(&resident, __ATOMIC_RELAXED);
@@ -839,8 +817,8 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(blocks < fit ? blocks : fit)),
                  dim3(32 * kTileWarps), kRingBytes, stream, p, tiles, total);
   if (e != cudaSuccess) return e;
-  return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), sizeof(PickSmem),
-                    stream, p, tiles);
+  return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads),
+                    sizeof(PickSmem) + static_cast<size_t>(p.beams) * tiles * sizeof(uint64_t), stream, p, tiles);
 }
 
 }  // namespace
