@@ -15,6 +15,8 @@
 // over all rows or pages (which page is the j-th free one, which row the j-th
 // to need one) runs in one thread-block cluster, whose barrier costs less than
 // a second launch.
+#include <type_traits>
+
 #include "kernels.h"
 #include "sm103.cuh"
 
@@ -105,77 +107,120 @@ constexpr int kMaxCtas = 8;  // of the cluster (the portable size)
 constexpr int kWarps = kClusterThreads / 32;
 
 struct ClusterSmem {
-  uint64_t warp_sum[kWarps];
-  uint64_t cta_sum[2][kMaxCtas];  // written by the cluster's CTAs; used in turn
+  uint64_t warp_sum[2][kWarps];
+  uint64_t cta_sum[4][kMaxCtas];  // written by the cluster's CTAs, each row once
 };
 
-// The sum of `v` over the threads before this one, CTAs in order of rank;
-// *total over all. Threads of every CTA call it together. Which of the two
-// rows of cta_sum it uses alternates, so that a CTA that is ahead does not
-// overwrite what another still reads (between two uses of a row lies the
-// barrier of the other).
-__device__ __forceinline__ uint64_t cluster_scan(uint64_t v, ClusterSmem& sm, int row, uint32_t rank,
-                                                 uint32_t ctas, uint64_t* total) {
+// The sums of `v` and `w` over the threads before this one, CTAs in order of
+// rank (returned, and in *w_before), and over all. Threads of every CTA call it
+// together; row_v and row_w of cta_sum belong to this call.
+__device__ __forceinline__ uint64_t cluster_scan(uint64_t v, ClusterSmem& sm, int row_v, uint32_t rank, uint32_t ctas,
+                                                 uint64_t* v_total, uint64_t w, int row_w, uint64_t* w_total,
+                                                 uint64_t* w_before) {
   const int lane = static_cast<int>(lane_id()), warp = warp_id();
-  uint64_t sum = v;
+  uint64_t sum_v = v, sum_w = w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t other = __shfl_up_sync(kAll, sum, o);
-    if (lane >= o) sum += other;
+    const uint64_t other_v = __shfl_up_sync(kAll, sum_v, o), other_w = __shfl_up_sync(kAll, sum_w, o);
+    if (lane >= o) {
+      sum_v += other_v;
+      sum_w += other_w;
+    }
   }
   __syncthreads();  // warp_sum's previous use is over
-  if (lane == 31) sm.warp_sum[warp] = sum;
+  if (lane == 31) {
+    sm.warp_sum[0][warp] = sum_v;
+    sm.warp_sum[1][warp] = sum_w;
+  }
   __syncthreads();
-  uint64_t before = sum - v;
-  uint64_t mine = sm.warp_sum[lane];
+  uint64_t warp_v = sm.warp_sum[0][lane], warp_w = sm.warp_sum[1][lane];
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t other = __shfl_up_sync(kAll, mine, o);
-    if (lane >= o) mine += other;
+    const uint64_t other_v = __shfl_up_sync(kAll, warp_v, o), other_w = __shfl_up_sync(kAll, warp_w, o);
+    if (lane >= o) {
+      warp_v += other_v;
+      warp_w += other_w;
+    }
   }
-  const uint64_t cta_total = __shfl_sync(kAll, mine, 31);
-  const uint64_t warps_before = __shfl_sync(kAll, mine, (warp + 31) & 31);
-  if (warp > 0) before += warps_before;
-  if (threadIdx.x < ctas) st_cluster_u64(cluster_map(&sm.cta_sum[row][rank], threadIdx.x), cta_total);
+  uint64_t before_v = sum_v - v, before_w = sum_w - w;
+  const uint64_t cta_v = __shfl_sync(kAll, warp_v, 31), cta_w = __shfl_sync(kAll, warp_w, 31);
+  const uint64_t warps_v = __shfl_sync(kAll, warp_v, (warp + 31) & 31), warps_w = __shfl_sync(kAll, warp_w, (warp + 31) & 31);
+  if (warp > 0) {
+    before_v += warps_v;
+    before_w += warps_w;
+  }
+  if (threadIdx.x < ctas) {
+    st_cluster_u64(cluster_map(&sm.cta_sum[row_v][rank], threadIdx.x), cta_v);
+    st_cluster_u64(cluster_map(&sm.cta_sum[row_w][rank], threadIdx.x), cta_w);
+  }
   cluster_sync();
-  uint64_t all = 0;
+  uint64_t all_v = 0, all_w = 0;
   for (uint32_t c = 0; c < ctas; ++c) {
-    const uint64_t t = sm.cta_sum[row][c];
-    if (c < rank) before += t;
-    all += t;
+    const uint64_t t_v = sm.cta_sum[row_v][c], t_w = sm.cta_sum[row_w][c];
+    if (c < rank) {
+      before_v += t_v;
+      before_w += t_w;
+    }
+    all_v += t_v;
+    all_w += t_w;
   }
-  *total = all;
-  return before;
+  *v_total = all_v;
+  *w_total = all_w;
+  *w_before = before_w;
+  return before_v;
 }
 
-// Pages of one warp: [begin, end), in steps of 128.
+// Pages of one warp: [begin, end), in steps of 256: eight counts to a lane are
+// loaded at a time.
+constexpr int kBatch = 8;
 struct Slice {
   int begin, end;
 };
 __device__ __forceinline__ Slice warp_slice(int n_pages, uint32_t rank, uint32_t ctas) {
   const int warps = static_cast<int>(ctas) * kWarps;
-  const int64_t len = ((static_cast<int64_t>(n_pages) + warps - 1) / warps + 127) / 128 * 128;
+  const int64_t len = ((static_cast<int64_t>(n_pages) + warps - 1) / warps + 32 * kBatch - 1) / (32 * kBatch) * (32 * kBatch);
   const int64_t begin = len * (static_cast<int64_t>(rank) * kWarps + warp_id());
   return {static_cast<int>(begin < n_pages ? begin : n_pages),
           static_cast<int>(begin + len < n_pages ? begin + len : n_pages)};
 }
-
+// f(page, its count, whether it is one) for a warp's pages 32 at a time, while
+// f returns true; all lanes call it together.
+template <typename F>
+__device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, F f) {
+  const int lane = static_cast<int>(lane_id());
+  bool go = true;
+#pragma unroll 1
+  for (int i = s.begin; go && i < s.end; i += 32 * kBatch) {
+    int c[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int page = i + 32 * j + lane;
+      c[j] = page < s.end ? __ldcg(counts + page) : 0;
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int page = i + 32 * j + lane;
+      go = go && f(page, c[j], page < s.end);
+    }
+  }
+}
 // How many of a warp's pages are free, in every lane.
 __device__ __forceinline__ int free_pages(const int32_t* counts, const Slice& s) {
   int n = 0;
-  const int lane = static_cast<int>(lane_id());
-#pragma unroll 8
-  for (int i = s.begin + lane; i < s.end; i += 32) n += __ldcg(counts + i) == 0;
+  for_slice(counts, s, [&](int, int count, bool in) {
+    n += in && count == 0;
+    return true;
+  });
   return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
 }
 
 // ---------------------------------------------------------------- reserve
 
-// Row b's new tokens lie at the positions before .. len - 1; the pages of
-// those positions are looked at, by 2^lanes_log2 lanes to a row.
+// Row b's new tokens lie at the positions before .. len - 1: the pages
+// [first, last) of the row.
 struct RowRange {
-  int first, last;  // pages
-  int rows;         // rows of the first page that hold earlier tokens
+  int first, last;
+  int rows;  // rows of the first page that hold earlier tokens
 };
 
 __device__ __forceinline__ RowRange row_range(const ReserveProblem& p, int b) {
@@ -198,7 +243,15 @@ __device__ __forceinline__ RowRange row_range(const ReserveProblem& p, int b) {
 __device__ __forceinline__ bool marked(int entry) { return entry < -1; }
 __device__ __forceinline__ int marked_page(int entry) { return -2 - entry; }
 
-__global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const ReserveProblem p, int lanes_log2) {
+// The pages of a row are cut into units of 2^lanes_log2, `units` of them to a row; a
+// group of lanes takes consecutive units, so that the groups' order is the rows'
+// and pages'. A call without shared pages, as most are, has two barriers: one
+// that adds up what the rows need, with the free pages, and one after the free
+// pages' numbers are written down. Pages that several rows name take three more.
+// 256 rows of a token, 65536 pages: 5 us; 64 prompts of up to 8192 tokens, 33000
+// pages of 262144: 10 us (with a row to a group, its pages one after the other,
+// and the counts read 32 at a time: 11 and 38).
+__global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const ReserveProblem p, int lanes_log2, int units) {
   __shared__ ClusterSmem sm;
   griddep_wait();
   griddep_launch_dependents();
@@ -206,73 +259,91 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
   const int lane = static_cast<int>(lane_id());
   const int lanes = 1 << lanes_log2;
-  // this group of lanes takes the rows [b0, b1), the groups in order
   const int groups = static_cast<int>(ctas) * (kClusterThreads >> lanes_log2);
   const int group = (static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x)) >> lanes_log2;
-  const int per = (p.pages.B + groups - 1) / groups;
-  const int b0 = min(group * per, pg.B), b1 = min(b0 + per, pg.B);
+  const int64_t all_units = static_cast<int64_t>(pg.B) * units;
+  const int64_t per = (all_units + groups - 1) / groups;
   const int sub = lane & (lanes - 1);
   const uint32_t group_mask = (lanes == 32 ? kAll : ((1u << lanes) - 1u) << (lane & ~(lanes - 1)));
   const uint32_t before_mask = group_mask & ((1u << lane) - 1u);
 
-  // f(row, its range, page number in the row, entry) for every page of the
-  // group's rows; all lanes of a warp take the same number of rounds, so that
-  // f may vote (k >= last: no page)
-  auto for_pages = [&](auto f) {
-    for (int i = 0; i < per; ++i) {
-      const int b = b0 + i;
-      const RowRange r = b < b1 ? row_range(p, b) : RowRange{0, 0, 0};
-      for (int k = r.first + sub; __any_sync(kAll, k - sub < r.last); k += lanes)
-        f(b, r, k, k < r.last ? pg.table + static_cast<int64_t>(b) * pg.max_pages + k : nullptr);
+  // f(row, its range, page number in the row, address of the entry or null, the
+  // entry) for every page of the group's units, U of them loaded at a time; all
+  // lanes of a warp call f together, so that it may vote
+  auto for_pages = [&](auto unroll, auto f) {
+    constexpr int U = decltype(unroll)::value;
+#pragma unroll 1
+    for (int64_t i = 0; i < per; i += U) {
+      int row[U], k[U], entry[U];
+      RowRange r[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int64_t u = group * per + i + j;
+        const bool is = i + j < per && u < all_units;
+        row[j] = is ? units == 1 ? static_cast<int>(u) : static_cast<int>(u / units) : 0;
+        r[j] = is ? row_range(p, row[j]) : RowRange{0, 0, 0};
+        k[j] = is ? r[j].first + ((static_cast<int>(u - static_cast<int64_t>(row[j]) * units) << lanes_log2) | sub) : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        entry[j] = k[j] < r[j].last ? __ldcg(pg.table + static_cast<int64_t>(row[j]) * pg.max_pages + k[j]) : 0;
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        f(row[j], r[j], k[j], k[j] < r[j].last ? pg.table + static_cast<int64_t>(row[j]) * pg.max_pages + k[j] : nullptr,
+          entry[j]);
     }
   };
+  using One = std::integral_constant<int, 1>;
+  using Four = std::integral_constant<int, 4>;
 
-  // which entries name shared pages
-  int any = 0;
-  for_pages([&](int, const RowRange&, int, int32_t* e) {
+  const Slice slice = warp_slice(pg.n_pages, rank, ctas);
+  const int free_here = free_pages(pg.counts, slice);
+
+  // what the rows need: pages, in the high half, and copies; and which entries
+  // name shared pages
+  uint64_t need = 0;
+  bool any = false;
+  for_pages(Four{}, [&](int, const RowRange&, int, int32_t* e, int page) {
     if (!e) return;
-    int page = *e;
     if (page >= pg.n_pages) atomicOr(&g_device_error, kErrIndex);
     if (page < 0 || page >= pg.n_pages) {
       if (page != -1) *e = -1;
+      need += 1ull << 32;
     } else if (__ldcg(pg.counts + page) > 1) {
       *e = -2 - page;
-      any = 1;
+      any = true;
     }
   });
-  uint64_t sharing;
-  cluster_scan(static_cast<uint64_t>(any), sm, 0, rank, ctas, &sharing);
+  uint64_t totals, more;  // more: free pages in the low half, threads with shared ones
+  uint64_t at = cluster_scan((any ? 1ull << 32 : 0ull) + (lane == 0 ? static_cast<uint64_t>(free_here) : 0ull), sm, 1, rank,
+                             ctas, &more, need, 0, &totals, &need);
+  at = __shfl_sync(kAll, at & kAll, 0);
+  const uint64_t n_free = more & kAll;
+  const bool sharing = (more >> 32) != 0;
+  uint64_t place = need;  // of this lane's group among the pages and copies
+  auto keeps = [&](int b, int entry) { return __ldcg(pg.counts + marked_page(entry)) == INT32_MIN + b; };
   if (sharing) {
     // Every row leaves the shared pages that it writes. Where that takes a
     // page's count to 0, the first of them keeps it after all: its number is
     // left in the count.
-    for_pages([&](int, const RowRange&, int, int32_t* e) {
-      if (e && marked(*e)) atomicSub(pg.counts + marked_page(*e), 1);
+    for_pages(One{}, [&](int, const RowRange&, int, int32_t* e, int entry) {
+      if (e && marked(entry)) atomicSub(pg.counts + marked_page(entry), 1);
     });
     cluster_sync();
-    for_pages([&](int b, const RowRange&, int, int32_t* e) {
-      if (e && marked(*e) && __ldcg(pg.counts + marked_page(*e)) <= 0) atomicMin(pg.counts + marked_page(*e), INT32_MIN + b);
+    for_pages(One{}, [&](int b, const RowRange&, int, int32_t* e, int entry) {
+      if (e && marked(entry) && __ldcg(pg.counts + marked_page(entry)) <= 0)
+        atomicMin(pg.counts + marked_page(entry), INT32_MIN + b);
     });
     cluster_sync();
+    uint64_t now = 0, unused;
+    for_pages(One{}, [&](int b, const RowRange& r, int k, int32_t* e, int entry) {
+      if (e && (entry == -1 || (marked(entry) && !keeps(b, entry))))
+        now += (1ull << 32) + (marked(entry) && k == r.first && r.rows > 0 ? 1ull : 0ull);
+    });
+    cluster_scan(0ull, sm, 3, rank, ctas, &unused, now, 2, &totals, &place);
   }
-  auto keeps = [&](int b, int entry) { return __ldcg(pg.counts + marked_page(entry)) == INT32_MIN + b; };
-
-  // what the rows need: pages, and copies of what pages held before
-  uint64_t need = 0;  // pages, in the high half; copies
-  for_pages([&](int b, const RowRange& r, int k, int32_t* e) {
-    if (!e) return;
-    const int entry = *e;
-    if (entry == -1 || (marked(entry) && !keeps(b, entry)))
-      need += (1ull << 32) + (marked(entry) && k == r.first && r.rows > 0 ? 1ull : 0ull);
-  });
-  uint64_t totals, n_free;
-  uint64_t place = cluster_scan(need, sm, 1, rank, ctas, &totals);
   // a group's lanes share the place of its first
   place = __shfl_sync(kAll, place, lane & ~(lanes - 1));
-  const Slice slice = warp_slice(pg.n_pages, rank, ctas);
-  const int mine = free_pages(pg.counts, slice);
-  uint64_t at = cluster_scan(lane == 0 ? static_cast<uint64_t>(mine) : 0ull, sm, 0, rank, ctas, &n_free);
-  at = __shfl_sync(kAll, at, 0);
   const uint64_t wanted = totals >> 32;
   const bool enough = wanted <= n_free;
   if (rank == 0 && threadIdx.x == 0) {
@@ -282,31 +353,32 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   if (!enough) {
     // as it was: the keepers' numbers out of the counts, then everybody back
     if (sharing) {
-      for_pages([&](int b, const RowRange&, int, int32_t* e) {
-        if (e && marked(*e) && keeps(b, *e)) pg.counts[marked_page(*e)] = 0;
+      for_pages(One{}, [&](int b, const RowRange&, int, int32_t* e, int entry) {
+        if (e && marked(entry) && keeps(b, entry)) pg.counts[marked_page(entry)] = 0;
       });
       cluster_sync();
-      for_pages([&](int, const RowRange&, int, int32_t* e) {
-        if (!e || !marked(*e)) return;
-        atomicAdd(pg.counts + marked_page(*e), 1);
-        *e = marked_page(*e);
+      for_pages(One{}, [&](int, const RowRange&, int, int32_t* e, int entry) {
+        if (!e || !marked(entry)) return;
+        atomicAdd(pg.counts + marked_page(entry), 1);
+        *e = marked_page(entry);
       });
     }
     return;
   }
 
-  // the lowest free pages, in order
-  for (int i = slice.begin; i < slice.end && at < wanted; i += 32) {
-    const bool free = i + lane < slice.end && __ldcg(pg.counts + i + lane) == 0;
-    const uint32_t vote = __ballot_sync(kAll, free);
-    const uint64_t to = at + __popc(vote & ((1u << lane) - 1u));
-    if (free && to < wanted) p.free_ids[to] = i + lane;
-    at += __popc(vote);
-  }
+  // the lowest free pages, in order. (While pages are shared, a count that was
+  // taken to 0 has its keeper's number.)
+  if (free_here > 0 && at < wanted)
+    for_slice(pg.counts, slice, [&](int page, int count, bool in) {
+      const uint32_t vote = __ballot_sync(kAll, in && count == 0);
+      const uint64_t to = at + __popc(vote & ((1u << lane) - 1u));
+      if (in && count == 0 && to < wanted) p.free_ids[to] = page;
+      at += __popc(vote);
+      return at < wanted;
+    });
   cluster_sync();
 
-  for_pages([&](int b, const RowRange& r, int k, int32_t* e) {
-    const int entry = e ? *e : 0;
+  for_pages(Four{}, [&](int b, const RowRange& r, int k, int32_t* e, int entry) {
     const bool shared = e && marked(entry);
     const bool kept = shared && keeps(b, entry);
     const bool wants = e && (entry == -1 || (shared && !kept));
@@ -346,33 +418,32 @@ __global__ void __launch_bounds__(kClusterThreads) cache_compact_kernel(const Co
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
   const int n = slice.end - slice.begin;
   const int mine = n - free_pages(pg.counts, slice);
-  uint64_t total;
-  uint64_t at = cluster_scan(lane == 0 ? static_cast<uint64_t>(mine) : 0ull, sm, 0, rank, ctas, &total);
+  uint64_t total, unused, unused_before;
+  uint64_t at = cluster_scan(lane == 0 ? static_cast<uint64_t>(mine) : 0ull, sm, 0, rank, ctas, &total, 0ull, 1, &unused,
+                             &unused_before);
   at = __shfl_sync(kAll, at, 0);
   const int used = static_cast<int>(total);
   const bool apart = p.counts_out != pg.counts;
   int movers = 0;
-  for (int i = slice.begin; i < slice.end; i += 32) {
-    const int page = i + lane;
-    const bool in = page < slice.end;
-    const int count = in ? __ldcg(pg.counts + page) : 0;
+  for_slice(pg.counts, slice, [&](int page, int count, bool in) {
     const uint32_t vote = __ballot_sync(kAll, in && count != 0);
     const int before = static_cast<int>(at) + __popc(vote & ((1u << lane) - 1u));  // used pages before this
     at += __popc(vote);
-    if (!in) continue;
+    if (!in) return true;
     const bool high = page >= used;
     const bool moves = high && count != 0, hole = !high && count == 0;
     const int k = moves ? used - 1 - before : page - before;
     movers += moves;
     if ((moves || hole) && k < p.max_copies) {
       p.moves[2 * k + hole] = page;
-      continue;  // its count and its place in the map are the move's
+      return true;  // its count and its place in the map are the move's
     }
     if (high) p.map[page] = page;
     if (apart) p.counts_out[page] = count;
-  }
+    return true;
+  });
   uint64_t n_moves;
-  cluster_scan(static_cast<uint64_t>(movers), sm, 1, rank, ctas, &n_moves);
+  cluster_scan(static_cast<uint64_t>(movers), sm, 2, rank, ctas, &n_moves, 0ull, 3, &unused, &unused_before);
   const int moved = static_cast<int>(n_moves) < p.max_copies ? static_cast<int>(n_moves) : p.max_copies;
   for (int k = static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x); k < moved;
        k += static_cast<int>(ctas) * kClusterThreads) {
@@ -421,11 +492,11 @@ int sm_count() {
   return n;
 }
 
-// One cluster for `work` pages or threads.
+// One cluster, of a block for each 8192 pages, 256 to a warp, and at most eight.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t work, cudaStream_t stream, Args&&... args) {
   unsigned ctas = 1;
-  while (ctas < kMaxCtas && work > static_cast<int64_t>(ctas) * 4 * kClusterThreads) ctas *= 2;
+  while (ctas < kMaxCtas && work > static_cast<int64_t>(ctas) * 8 * kClusterThreads) ctas *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kClusterThreads);
@@ -468,13 +539,15 @@ cudaError_t launch_cache_release(const PagesProblem& p, const int32_t* keep_lens
 }
 
 cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
-  // lanes to a row: for the most pages that its new tokens can touch
-  const int64_t pages = ((static_cast<int64_t>(p.n_new) - 1) >> p.pages.page_shift) + 2;
+  // lanes to a unit: for the most pages that a row's new tokens can touch
+  int64_t pages = ((static_cast<int64_t>(p.n_new) - 1) >> p.pages.page_shift) + 2;
+  if (pages > p.pages.max_pages) pages = p.pages.max_pages;
   int lanes_log2 = 0;
   while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
-  const int64_t threads = static_cast<int64_t>(p.pages.B) << lanes_log2;
+  const int units = static_cast<int>((pages + (1 << lanes_log2) - 1) >> lanes_log2);
+  const int64_t threads = (static_cast<int64_t>(p.pages.B) * units) << lanes_log2;
   return launch_cluster(cache_reserve_kernel, threads * 4 > p.pages.n_pages ? threads * 4 : p.pages.n_pages, stream, p,
-                        lanes_log2);
+                        lanes_log2, units);
 }
 
 cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream) {
