@@ -106,68 +106,78 @@ constexpr int kClusterThreads = 1024;
 constexpr int kMaxCtas = 8;  // of the cluster (the portable size)
 constexpr int kWarps = kClusterThreads / 32;
 
+// Two sums, over threads.
+struct Sums {
+  uint64_t v, w;
+};
 struct ClusterSmem {
-  uint64_t warp_sum[2][kWarps];
-  uint64_t cta_sum[4][kMaxCtas];  // written by the cluster's CTAs, each row once
+  Sums warp[kWarps];      // of a warp, then of those before it
+  Sums cta[2][kMaxCtas];  // written by the cluster's CTAs, each row once
+  Sums before, all;
 };
 
-// The sums of `v` and `w` over the threads before this one, CTAs in order of
-// rank (returned, and in *w_before), and over all. Threads of every CTA call it
-// together; row_v and row_w of cta_sum belong to this call.
-__device__ __forceinline__ uint64_t cluster_scan(uint64_t v, ClusterSmem& sm, int row_v, uint32_t rank, uint32_t ctas,
-                                                 uint64_t* v_total, uint64_t w, int row_w, uint64_t* w_total,
-                                                 uint64_t* w_before) {
+// The sums of v and w over the threads before this one, the CTAs in order of
+// rank; *all of them over all. A warp adds `more` to its w. Threads of every CTA
+// call it together; `row` of sm.cta belongs to this call. LANES: which of the
+// two differ within a warp (1: v, 2: both). One warp joins the warps' sums:
+// 32 warps at once take an SM eight times as long for it.
+template <int LANES>
+__device__ __forceinline__ Sums cluster_scan(uint32_t v, uint32_t w, uint64_t more, ClusterSmem& sm, int row, uint32_t rank,
+                                             uint32_t ctas, Sums* all) {
   const int lane = static_cast<int>(lane_id()), warp = warp_id();
-  uint64_t sum_v = v, sum_w = w;
+  uint32_t sum_v = v, sum_w = w;
+  if constexpr (LANES > 0) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t other_v = __shfl_up_sync(kAll, sum_v, o), other_w = __shfl_up_sync(kAll, sum_w, o);
-    if (lane >= o) {
-      sum_v += other_v;
-      sum_w += other_w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t other_v = __shfl_up_sync(kAll, sum_v, o);
+      if (lane >= o) sum_v += other_v;
+      if constexpr (LANES > 1) {
+        const uint32_t other_w = __shfl_up_sync(kAll, sum_w, o);
+        if (lane >= o) sum_w += other_w;
+      }
     }
   }
-  __syncthreads();  // warp_sum's previous use is over
-  if (lane == 31) {
-    sm.warp_sum[0][warp] = sum_v;
-    sm.warp_sum[1][warp] = sum_w;
-  }
+  if (lane == 31) sm.warp[warp] = {sum_v, sum_w + more};
   __syncthreads();
-  uint64_t warp_v = sm.warp_sum[0][lane], warp_w = sm.warp_sum[1][lane];
+  if (warp == 0) {
+    const Sums mine = sm.warp[lane];
+    Sums sum = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t other_v = __shfl_up_sync(kAll, warp_v, o), other_w = __shfl_up_sync(kAll, warp_w, o);
-    if (lane >= o) {
-      warp_v += other_v;
-      warp_w += other_w;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t other_v = __shfl_up_sync(kAll, sum.v, o), other_w = __shfl_up_sync(kAll, sum.w, o);
+      if (lane >= o) {
+        sum.v += other_v;
+        sum.w += other_w;
+      }
     }
-  }
-  uint64_t before_v = sum_v - v, before_w = sum_w - w;
-  const uint64_t cta_v = __shfl_sync(kAll, warp_v, 31), cta_w = __shfl_sync(kAll, warp_w, 31);
-  const uint64_t warps_v = __shfl_sync(kAll, warp_v, (warp + 31) & 31), warps_w = __shfl_sync(kAll, warp_w, (warp + 31) & 31);
-  if (warp > 0) {
-    before_v += warps_v;
-    before_w += warps_w;
-  }
-  if (threadIdx.x < ctas) {
-    st_cluster_u64(cluster_map(&sm.cta_sum[row_v][rank], threadIdx.x), cta_v);
-    st_cluster_u64(cluster_map(&sm.cta_sum[row_w][rank], threadIdx.x), cta_w);
+    sm.warp[lane] = {sum.v - mine.v, sum.w - mine.w};
+    const uint64_t cta_v = __shfl_sync(kAll, sum.v, 31), cta_w = __shfl_sync(kAll, sum.w, 31);
+    if (lane < static_cast<int>(ctas)) {
+      const uint32_t to = cluster_map(&sm.cta[row][rank], static_cast<uint32_t>(lane));
+      st_cluster_u64(to, cta_v);
+      st_cluster_u64(to + 8, cta_w);
+    }
   }
   cluster_sync();
-  uint64_t all_v = 0, all_w = 0;
-  for (uint32_t c = 0; c < ctas; ++c) {
-    const uint64_t t_v = sm.cta_sum[row_v][c], t_w = sm.cta_sum[row_w][c];
-    if (c < rank) {
-      before_v += t_v;
-      before_w += t_w;
+  if (warp == 0) {
+    Sums mine = {0, 0};
+    if (lane < static_cast<int>(ctas)) mine = sm.cta[row][lane];
+    Sums sum = mine;
+#pragma unroll
+    for (int o = 1; o < kMaxCtas; o <<= 1) {
+      const uint64_t other_v = __shfl_up_sync(kAll, sum.v, o), other_w = __shfl_up_sync(kAll, sum.w, o);
+      if (lane >= o) {
+        sum.v += other_v;
+        sum.w += other_w;
+      }
     }
-    all_v += t_v;
-    all_w += t_w;
+    if (lane == static_cast<int>(rank)) sm.before = {sum.v - mine.v, sum.w - mine.w};
+    if (lane == kMaxCtas - 1) sm.all = sum;
   }
-  *v_total = all_v;
-  *w_total = all_w;
-  *w_before = before_w;
-  return before_v;
+  __syncthreads();
+  *all = sm.all;
+  const Sums warps = sm.warp[warp], ctas_before = sm.before;
+  return {ctas_before.v + warps.v + (LANES > 0 ? sum_v - v : 0u), ctas_before.w + warps.w + (LANES > 1 ? sum_w - w : 0u)};
 }
 
 // Pages of one warp: [begin, end), in steps of 256: eight counts to a lane are
@@ -184,13 +194,12 @@ __device__ __forceinline__ Slice warp_slice(int n_pages, uint32_t rank, uint32_t
           static_cast<int>(begin + len < n_pages ? begin + len : n_pages)};
 }
 // f(page, its count, whether it is one) for a warp's pages 32 at a time, while
-// f returns true; all lanes call it together.
-template <typename F>
-__device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, F f) {
+// go() holds ahead of a batch; all lanes call it together.
+template <typename F, typename G>
+__device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, F f, G go) {
   const int lane = static_cast<int>(lane_id());
-  bool go = true;
 #pragma unroll 1
-  for (int i = s.begin; go && i < s.end; i += 32 * kBatch) {
+  for (int i = s.begin; i < s.end && go(); i += 32 * kBatch) {
     int c[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -198,19 +207,13 @@ __device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s,
       c[j] = page < s.end ? __ldcg(counts + page) : 0;
     }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int page = i + 32 * j + lane;
-      go = go && f(page, c[j], page < s.end);
-    }
+    for (int j = 0; j < kBatch; ++j) f(i + 32 * j + lane, c[j], i + 32 * j + lane < s.end);
   }
 }
 // How many of a warp's pages are free, in every lane.
 __device__ __forceinline__ int free_pages(const int32_t* counts, const Slice& s) {
   int n = 0;
-  for_slice(counts, s, [&](int, int count, bool in) {
-    n += in && count == 0;
-    return true;
-  });
+  for_slice(counts, s, [&](int, int count, bool in) { n += in && count == 0; }, [] { return true; });
   return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
 }
 
@@ -245,12 +248,12 @@ __device__ __forceinline__ int marked_page(int entry) { return -2 - entry; }
 
 // The pages of a row are cut into units of 2^lanes_log2, `units` of them to a row; a
 // group of lanes takes consecutive units, so that the groups' order is the rows'
-// and pages'. A call without shared pages, as most are, has two barriers: one
-// that adds up what the rows need, with the free pages, and one after the free
-// pages' numbers are written down. Pages that several rows name take three more.
-// 256 rows of a token, 65536 pages: 5 us; 64 prompts of up to 8192 tokens, 33000
-// pages of 262144: 10 us (with a row to a group, its pages one after the other,
-// and the counts read 32 at a time: 11 and 38).
+// and pages'. ONE: a group has one unit at most, and its entries stay in registers
+// from phase to phase. A call without shared pages, as most are, has two
+// barriers: one that adds up what the rows need, with the free pages, and one
+// after the free pages' numbers are written down. Pages that several rows name
+// take three more.
+template <bool ONE>
 __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const ReserveProblem p, int lanes_log2, int units) {
   __shared__ ClusterSmem sm;
   griddep_wait();
@@ -259,147 +262,188 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
   const int lane = static_cast<int>(lane_id());
   const int lanes = 1 << lanes_log2;
-  const int groups = static_cast<int>(ctas) * (kClusterThreads >> lanes_log2);
   const int group = (static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x)) >> lanes_log2;
   const int64_t all_units = static_cast<int64_t>(pg.B) * units;
-  const int64_t per = (all_units + groups - 1) / groups;
+  const int groups = static_cast<int>(ctas) * (kClusterThreads >> lanes_log2);
+  const int64_t per = ONE ? 1 : (all_units + groups - 1) / groups;
   const int sub = lane & (lanes - 1);
   const uint32_t group_mask = (lanes == 32 ? kAll : ((1u << lanes) - 1u) << (lane & ~(lanes - 1)));
   const uint32_t before_mask = group_mask & ((1u << lane) - 1u);
 
-  // f(row, its range, page number in the row, address of the entry or null, the
-  // entry) for every page of the group's units, U of them loaded at a time; all
-  // lanes of a warp call f together, so that it may vote
+  // a lane's page of a unit
+  struct Place {
+    int row, rows;  // rows: of earlier tokens in the page, if it is the first to be written
+    int entry;
+    int32_t* at;    // the entry's address; null: no page
+  };
+  auto look_up = [&](int64_t u, bool is) {
+    Place q = {0, 0, 0, nullptr};
+    if (!is) return q;
+    q.row = units == 1 ? static_cast<int>(u) : static_cast<int>(u / units);
+    const RowRange r = row_range(p, q.row);
+    const int k = r.first + ((static_cast<int>(u - static_cast<int64_t>(q.row) * units) << lanes_log2) | sub);
+    q.rows = k == r.first ? r.rows : 0;
+    if (k < r.last) q.at = pg.table + static_cast<int64_t>(q.row) * pg.max_pages + k;
+    return q;
+  };
+  Place own = {0, 0, 0, nullptr};
+  if constexpr (ONE) {
+    own = look_up(group, group < all_units);
+    if (own.at) own.entry = __ldcg(own.at);
+  }
+  // f(places, how many) for the group's units, U at a time; all lanes of a warp
+  // call it together, so that it may vote
   auto for_pages = [&](auto unroll, auto f) {
-    constexpr int U = decltype(unroll)::value;
+    if constexpr (ONE) {
+      f(&own, std::integral_constant<int, 1>{});
+    } else {
+      constexpr int U = decltype(unroll)::value;
 #pragma unroll 1
-    for (int64_t i = 0; i < per; i += U) {
-      int row[U], k[U], entry[U];
-      RowRange r[U];
+      for (int64_t i = 0; i < per; i += U) {
+        Place q[U];
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int64_t u = group * per + i + j;
-        const bool is = i + j < per && u < all_units;
-        row[j] = is ? units == 1 ? static_cast<int>(u) : static_cast<int>(u / units) : 0;
-        r[j] = is ? row_range(p, row[j]) : RowRange{0, 0, 0};
-        k[j] = is ? r[j].first + ((static_cast<int>(u - static_cast<int64_t>(row[j]) * units) << lanes_log2) | sub) : 0;
+        for (int j = 0; j < U; ++j) q[j] = look_up(group * per + i + j, i + j < per && group * per + i + j < all_units);
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+          if (q[j].at) q[j].entry = __ldcg(q[j].at);
+        f(q, unroll);
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        entry[j] = k[j] < r[j].last ? __ldcg(pg.table + static_cast<int64_t>(row[j]) * pg.max_pages + k[j]) : 0;
-#pragma unroll
-      for (int j = 0; j < U; ++j)
-        f(row[j], r[j], k[j], k[j] < r[j].last ? pg.table + static_cast<int64_t>(row[j]) * pg.max_pages + k[j] : nullptr,
-          entry[j]);
     }
   };
-  using One = std::integral_constant<int, 1>;
+  using Single = std::integral_constant<int, 1>;
   using Four = std::integral_constant<int, 4>;
 
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
   const int free_here = free_pages(pg.counts, slice);
 
-  // what the rows need: pages, in the high half, and copies; and which entries
-  // name shared pages
-  uint64_t need = 0;
+  // what the rows need, and which entries name shared pages
+  uint32_t need = 0;
   bool any = false;
-  for_pages(Four{}, [&](int, const RowRange&, int, int32_t* e, int page) {
-    if (!e) return;
-    if (page >= pg.n_pages) atomicOr(&g_device_error, kErrIndex);
-    if (page < 0 || page >= pg.n_pages) {
-      if (page != -1) *e = -1;
-      need += 1ull << 32;
-    } else if (__ldcg(pg.counts + page) > 1) {
-      *e = -2 - page;
-      any = true;
+  for_pages(Four{}, [&](Place* q, auto n) {
+    constexpr int U = decltype(n)::value;
+    int count[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      count[j] = q[j].at && q[j].entry >= 0 && q[j].entry < pg.n_pages ? __ldcg(pg.counts + q[j].entry) : 0;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (!q[j].at) continue;
+      const bool names = q[j].entry >= 0 && q[j].entry < pg.n_pages;
+      if (q[j].entry >= pg.n_pages) atomicOr(&g_device_error, kErrIndex);
+      if (!names) ++need;
+      if ((names && count[j] > 1) || (!names && q[j].entry != -1)) {
+        any |= names;
+        q[j].entry = names ? -2 - q[j].entry : -1;
+        *q[j].at = q[j].entry;
+      }
     }
   });
-  uint64_t totals, more;  // more: free pages in the low half, threads with shared ones
-  uint64_t at = cluster_scan((any ? 1ull << 32 : 0ull) + (lane == 0 ? static_cast<uint64_t>(free_here) : 0ull), sm, 1, rank,
-                             ctas, &more, need, 0, &totals, &need);
-  at = __shfl_sync(kAll, at & kAll, 0);
-  const uint64_t n_free = more & kAll;
-  const bool sharing = (more >> 32) != 0;
-  uint64_t place = need;  // of this lane's group among the pages and copies
-  auto keeps = [&](int b, int entry) { return __ldcg(pg.counts + marked_page(entry)) == INT32_MIN + b; };
+  any = __any_sync(kAll, any);
+  Sums all;  // pages needed; free pages, and above 32 bits the warps with shared ones
+  const Sums first = cluster_scan<1>(need, 0u, static_cast<uint64_t>(free_here) + (any ? 1ull << 32 : 0ull), sm, 0, rank, ctas, &all);
+  const uint32_t n_free = static_cast<uint32_t>(all.w);
+  uint32_t free_at = static_cast<uint32_t>(first.w);  // free pages before this warp's
+  const bool sharing = all.w >> 32 != 0;
+  uint64_t page_at = first.v, copy_at = 0, wanted = all.v, n_copies = 0;
+  auto keeps = [&](const Place& q) { return __ldcg(pg.counts + marked_page(q.entry)) == INT32_MIN + q.row; };
+  bool kept = false;  // ONE: the lane's page is shared, and its row keeps it
   if (sharing) {
     // Every row leaves the shared pages that it writes. Where that takes a
     // page's count to 0, the first of them keeps it after all: its number is
     // left in the count.
-    for_pages(One{}, [&](int, const RowRange&, int, int32_t* e, int entry) {
-      if (e && marked(entry)) atomicSub(pg.counts + marked_page(entry), 1);
+    for_pages(Single{}, [&](Place* q, auto) {
+      if (q->at && marked(q->entry)) atomicSub(pg.counts + marked_page(q->entry), 1);
     });
     cluster_sync();
-    for_pages(One{}, [&](int b, const RowRange&, int, int32_t* e, int entry) {
-      if (e && marked(entry) && __ldcg(pg.counts + marked_page(entry)) <= 0)
-        atomicMin(pg.counts + marked_page(entry), INT32_MIN + b);
+    for_pages(Single{}, [&](Place* q, auto) {
+      if (q->at && marked(q->entry) && __ldcg(pg.counts + marked_page(q->entry)) <= 0)
+        atomicMin(pg.counts + marked_page(q->entry), INT32_MIN + q->row);
     });
     cluster_sync();
-    uint64_t now = 0, unused;
-    for_pages(One{}, [&](int b, const RowRange& r, int k, int32_t* e, int entry) {
-      if (e && (entry == -1 || (marked(entry) && !keeps(b, entry))))
-        now += (1ull << 32) + (marked(entry) && k == r.first && r.rows > 0 ? 1ull : 0ull);
+    need = 0;
+    uint32_t copies = 0;
+    for_pages(Single{}, [&](Place* q, auto) {
+      if (!q->at) return;
+      const bool shared = marked(q->entry);
+      kept = shared && keeps(*q);
+      if (q->entry != -1 && (!shared || kept)) return;
+      ++need;
+      copies += shared && q->rows > 0;
     });
-    cluster_scan(0ull, sm, 3, rank, ctas, &unused, now, 2, &totals, &place);
+    const Sums second = cluster_scan<2>(need, copies, 0ull, sm, 1, rank, ctas, &all);
+    page_at = second.v;
+    copy_at = second.w;
+    wanted = all.v;
+    n_copies = all.w;
   }
-  // a group's lanes share the place of its first
-  place = __shfl_sync(kAll, place, lane & ~(lanes - 1));
-  const uint64_t wanted = totals >> 32;
+  // a group's lanes share the places of its first
+  page_at = __shfl_sync(kAll, page_at, lane & ~(lanes - 1));
+  copy_at = __shfl_sync(kAll, copy_at, lane & ~(lanes - 1));
   const bool enough = wanted <= n_free;
   if (rank == 0 && threadIdx.x == 0) {
-    *p.n_copies = enough ? static_cast<int32_t>(totals & kAll) : 0;
+    *p.n_copies = enough ? static_cast<int32_t>(n_copies) : 0;
     *p.n_missing = enough ? 0 : static_cast<int32_t>(wanted - n_free < INT32_MAX ? wanted - n_free : INT32_MAX);
   }
   if (!enough) {
     // as it was: the keepers' numbers out of the counts, then everybody back
     if (sharing) {
-      for_pages(One{}, [&](int b, const RowRange&, int, int32_t* e, int entry) {
-        if (e && marked(entry) && keeps(b, entry)) pg.counts[marked_page(entry)] = 0;
+      for_pages(Single{}, [&](Place* q, auto) {
+        if (q->at && marked(q->entry) && keeps(*q)) pg.counts[marked_page(q->entry)] = 0;
       });
       cluster_sync();
-      for_pages(One{}, [&](int, const RowRange&, int, int32_t* e, int entry) {
-        if (!e || !marked(entry)) return;
-        atomicAdd(pg.counts + marked_page(entry), 1);
-        *e = marked_page(entry);
+      for_pages(Single{}, [&](Place* q, auto) {
+        if (!q->at || !marked(q->entry)) return;
+        atomicAdd(pg.counts + marked_page(q->entry), 1);
+        *q->at = marked_page(q->entry);
       });
     }
     return;
   }
 
-  // the lowest free pages, in order. (While pages are shared, a count that was
-  // taken to 0 has its keeper's number.)
-  if (free_here > 0 && at < wanted)
-    for_slice(pg.counts, slice, [&](int page, int count, bool in) {
-      const uint32_t vote = __ballot_sync(kAll, in && count == 0);
-      const uint64_t to = at + __popc(vote & ((1u << lane) - 1u));
-      if (in && count == 0 && to < wanted) p.free_ids[to] = page;
-      at += __popc(vote);
-      return at < wanted;
-    });
+  // the lowest free pages, in order. (A shared page's count that was taken to 0
+  // has its keeper's number.)
+  if (free_here > 0)
+    for_slice(
+        pg.counts, slice,
+        [&](int page, int count, bool in) {
+          const bool free = in && count == 0;
+          const uint32_t vote = __ballot_sync(kAll, free);
+          const uint32_t to = free_at + __popc(vote & ((1u << lane) - 1u));
+          if (free && to < wanted) p.free_ids[to] = page;
+          free_at += __popc(vote);
+        },
+        [&] { return free_at < wanted; });
   cluster_sync();
 
-  for_pages(Four{}, [&](int b, const RowRange& r, int k, int32_t* e, int entry) {
-    const bool shared = e && marked(entry);
-    const bool kept = shared && keeps(b, entry);
-    const bool wants = e && (entry == -1 || (shared && !kept));
-    const bool copies = wants && shared && k == r.first && r.rows > 0;
-    const uint32_t want_vote = __ballot_sync(kAll, wants), copy_vote = __ballot_sync(kAll, copies);
-    if (kept) {
-      *e = marked_page(entry);
-      pg.counts[marked_page(entry)] = 1;
+  for_pages(Four{}, [&](Place* q, auto n) {
+    constexpr int U = decltype(n)::value;
+    int page[U];
+    int32_t* copy[U];
+    bool keeper[U], wants[U];
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      const bool shared = q[j].at && marked(q[j].entry);
+      keeper[j] = shared && (ONE ? kept : keeps(q[j]));
+      wants[j] = q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
+      const bool copies = wants[j] && shared && q[j].rows > 0;
+      const uint32_t want_vote = __ballot_sync(kAll, wants[j]), copy_vote = __ballot_sync(kAll, copies);
+      page[j] = wants[j] ? __ldcg(p.free_ids + page_at + __popc(want_vote & before_mask)) : 0;
+      copy[j] = copies ? p.copies + 3 * (copy_at + __popc(copy_vote & before_mask)) : nullptr;
+      page_at += __popc(want_vote & group_mask);
+      copy_at += __popc(copy_vote & group_mask);
     }
-    if (wants) {
-      const int page = __ldcg(p.free_ids + (place >> 32) + __popc(want_vote & before_mask));
-      *e = page;
-      pg.counts[page] = 1;
-      if (copies) {
-        int32_t* c = p.copies + 3 * ((place & kAll) + __popc(copy_vote & before_mask));
-        c[0] = marked_page(entry);
-        c[1] = page;
-        c[2] = r.rows;
+#pragma unroll
+    for (int j = 0; j < U; ++j) {
+      if (!wants[j] && !keeper[j]) continue;
+      const int was = marked_page(q[j].entry), now = keeper[j] ? was : page[j];
+      *q[j].at = now;
+      pg.counts[now] = 1;
+      if (copy[j]) {
+        copy[j][0] = was;
+        copy[j][1] = now;
+        copy[j][2] = q[j].rows;
       }
     }
-    place += (static_cast<uint64_t>(__popc(want_vote & group_mask)) << 32) + __popc(copy_vote & group_mask);
   });
 }
 
@@ -418,33 +462,30 @@ __global__ void __launch_bounds__(kClusterThreads) cache_compact_kernel(const Co
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
   const int n = slice.end - slice.begin;
   const int mine = n - free_pages(pg.counts, slice);
-  uint64_t total, unused, unused_before;
-  uint64_t at = cluster_scan(lane == 0 ? static_cast<uint64_t>(mine) : 0ull, sm, 0, rank, ctas, &total, 0ull, 1, &unused,
-                             &unused_before);
-  at = __shfl_sync(kAll, at, 0);
-  const int used = static_cast<int>(total);
+  Sums all;
+  int at = static_cast<int>(cluster_scan<0>(0u, 0u, static_cast<uint64_t>(mine), sm, 0, rank, ctas, &all).w);  // before this warp's
+  const int used = static_cast<int>(all.w);
   const bool apart = p.counts_out != pg.counts;
   int movers = 0;
   for_slice(pg.counts, slice, [&](int page, int count, bool in) {
     const uint32_t vote = __ballot_sync(kAll, in && count != 0);
-    const int before = static_cast<int>(at) + __popc(vote & ((1u << lane) - 1u));  // used pages before this
+    const int before = at + __popc(vote & ((1u << lane) - 1u));  // used pages before this
     at += __popc(vote);
-    if (!in) return true;
+    if (!in) return;
     const bool high = page >= used;
     const bool moves = high && count != 0, hole = !high && count == 0;
     const int k = moves ? used - 1 - before : page - before;
     movers += moves;
     if ((moves || hole) && k < p.max_copies) {
       p.moves[2 * k + hole] = page;
-      return true;  // its count and its place in the map are the move's
+      return;  // its count and its place in the map are the move's
     }
     if (high) p.map[page] = page;
     if (apart) p.counts_out[page] = count;
-    return true;
-  });
-  uint64_t n_moves;
-  cluster_scan(static_cast<uint64_t>(movers), sm, 2, rank, ctas, &n_moves, 0ull, 3, &unused, &unused_before);
-  const int moved = static_cast<int>(n_moves) < p.max_copies ? static_cast<int>(n_moves) : p.max_copies;
+  }, [] { return true; });
+  movers = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(movers)));
+  cluster_scan<0>(0u, 0u, static_cast<uint64_t>(movers), sm, 1, rank, ctas, &all);
+  const int moved = static_cast<int>(all.w) < p.max_copies ? static_cast<int>(all.w) : p.max_copies;
   for (int k = static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x); k < moved;
        k += static_cast<int>(ctas) * kClusterThreads) {
     const int from = __ldcg(p.moves + 2 * k), to = __ldcg(p.moves + 2 * k + 1);
@@ -546,8 +587,9 @@ cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
   while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
   const int units = static_cast<int>((pages + (1 << lanes_log2) - 1) >> lanes_log2);
   const int64_t threads = (static_cast<int64_t>(p.pages.B) * units) << lanes_log2;
-  return launch_cluster(cache_reserve_kernel, threads * 4 > p.pages.n_pages ? threads * 4 : p.pages.n_pages, stream, p,
-                        lanes_log2, units);
+  const int64_t work = threads * 8 > p.pages.n_pages ? threads * 8 : p.pages.n_pages;
+  return threads <= kMaxCtas * kClusterThreads ? launch_cluster(cache_reserve_kernel<true>, work, stream, p, lanes_log2, units)
+                                               : launch_cluster(cache_reserve_kernel<false>, work, stream, p, lanes_log2, units);
 }
 
 cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream) {
