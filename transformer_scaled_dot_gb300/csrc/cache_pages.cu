@@ -110,10 +110,12 @@ constexpr int kWarps = kClusterThreads / 32;
 struct Sums {
   uint64_t v, w;
 };
+constexpr int kNear = 1024;
 struct ClusterSmem {
   Sums warp[kWarps];      // of a warp, then of those before it
   Sums cta[2][kMaxCtas];  // written by the cluster's CTAs, each row once
   Sums before, all;
+  int32_t free_ids[kNear];
 };
 
 // The sums of v and w over the threads before this one, the CTAs in order of
@@ -193,27 +195,35 @@ __device__ __forceinline__ Slice warp_slice(int n_pages, uint32_t rank, uint32_t
   return {static_cast<int>(begin < n_pages ? begin : n_pages),
           static_cast<int>(begin + len < n_pages ? begin + len : n_pages)};
 }
-// f(page, its count, whether it is one) for a warp's pages 32 at a time, while
-// go() holds ahead of a batch; all lanes call it together.
+// A batch of a warp's counts; a page past the slice counts as used.
+struct Batch {
+  int32_t c[kBatch];
+};
+__device__ __forceinline__ Batch load_batch(const int32_t* counts, const Slice& s, int begin, int lane) {
+  Batch b;
+#pragma unroll
+  for (int j = 0; j < kBatch; ++j) {
+    const int page = begin + 32 * j + lane;
+    b.c[j] = page < s.end ? __ldcg(counts + page) : 1;
+  }
+  return b;
+}
+// f(page, its count) for a warp's pages 32 at a time, while go() holds ahead of
+// a batch; all lanes call it together. `batch`: the slice's first.
 template <typename F, typename G>
-__device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, F f, G go) {
-  const int lane = static_cast<int>(lane_id());
+__device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, Batch batch, int lane, F f, G go) {
 #pragma unroll 1
-  for (int i = s.begin; i < s.end && go(); i += 32 * kBatch) {
-    int c[kBatch];
+  for (int i = s.begin; i < s.end && go();) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int page = i + 32 * j + lane;
-      c[j] = page < s.end ? __ldcg(counts + page) : 0;
-    }
-#pragma unroll
-    for (int j = 0; j < kBatch; ++j) f(i + 32 * j + lane, c[j], i + 32 * j + lane < s.end);
+    for (int j = 0; j < kBatch; ++j) f(i + 32 * j + lane, batch.c[j]);
+    i += 32 * kBatch;
+    if (i < s.end) batch = load_batch(counts, s, i, lane);
   }
 }
 // How many of a warp's pages are free, in every lane.
-__device__ __forceinline__ int free_pages(const int32_t* counts, const Slice& s) {
+__device__ __forceinline__ int free_pages(const int32_t* counts, const Slice& s, const Batch& first, int lane) {
   int n = 0;
-  for_slice(counts, s, [&](int, int count, bool in) { n += in && count == 0; }, [] { return true; });
+  for_slice(counts, s, first, lane, [&](int, int count) { n += count == 0; }, [] { return true; });
   return static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(n)));
 }
 
@@ -276,19 +286,23 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     int entry;
     int32_t* at;    // the entry's address; null: no page
   };
-  auto look_up = [&](int64_t u, bool is) {
+  auto look_up = [&](int row, int unit, bool is) {
     Place q = {0, 0, 0, nullptr};
     if (!is) return q;
-    q.row = units == 1 ? static_cast<int>(u) : static_cast<int>(u / units);
-    const RowRange r = row_range(p, q.row);
-    const int k = r.first + ((static_cast<int>(u - static_cast<int64_t>(q.row) * units) << lanes_log2) | sub);
+    q.row = row;
+    const RowRange r = row_range(p, row);
+    const int k = r.first + (unit << lanes_log2 | sub);
     q.rows = k == r.first ? r.rows : 0;
     if (k < r.last) q.at = pg.table + static_cast<int64_t>(q.row) * pg.max_pages + k;
     return q;
   };
+  const Slice slice = warp_slice(pg.n_pages, rank, ctas);
+  const Batch first_batch = load_batch(pg.counts, slice, slice.begin, lane);
+  const int row0 = ONE && units == 1 ? group : static_cast<int>(group * per / units);
+  const int unit0 = static_cast<int>(group * per - static_cast<int64_t>(row0) * units);
   Place own = {0, 0, 0, nullptr};
   if constexpr (ONE) {
-    own = look_up(group, group < all_units);
+    own = look_up(row0, unit0, row0 < pg.B);
     if (own.at) own.entry = __ldcg(own.at);
   }
   // f(places, how many) for the group's units, U at a time; all lanes of a warp
@@ -298,11 +312,18 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
       f(&own, std::integral_constant<int, 1>{});
     } else {
       constexpr int U = decltype(unroll)::value;
+      int row = row0, unit = unit0;
 #pragma unroll 1
       for (int64_t i = 0; i < per; i += U) {
         Place q[U];
 #pragma unroll
-        for (int j = 0; j < U; ++j) q[j] = look_up(group * per + i + j, i + j < per && group * per + i + j < all_units);
+        for (int j = 0; j < U; ++j) {
+          q[j] = look_up(row, unit, i + j < per && row < pg.B);
+          if (++unit == units) {
+            unit = 0;
+            ++row;
+          }
+        }
 #pragma unroll
         for (int j = 0; j < U; ++j)
           if (q[j].at) q[j].entry = __ldcg(q[j].at);
@@ -313,8 +334,7 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   using Single = std::integral_constant<int, 1>;
   using Four = std::integral_constant<int, 4>;
 
-  const Slice slice = warp_slice(pg.n_pages, rank, ctas);
-  const int free_here = free_pages(pg.counts, slice);
+  const int free_here = free_pages(pg.counts, slice, first_batch, lane);
 
   // what the rows need, and which entries name shared pages
   uint32_t need = 0;
@@ -400,20 +420,23 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     return;
   }
 
-  // the lowest free pages, in order. (A shared page's count that was taken to 0
-  // has its keeper's number.)
+  // the lowest free pages, in order: of one block's few in shared memory. (The
+  // shared pages' counts were above 0 when this warp's first batch was read,
+  // and are not 0 now: one that was taken there has its keeper's number.)
+  const bool near = ctas == 1 && wanted <= kNear;
+  const uint32_t most = static_cast<uint32_t>(wanted);  // n_free at most
   if (free_here > 0)
     for_slice(
-        pg.counts, slice,
-        [&](int page, int count, bool in) {
-          const bool free = in && count == 0;
-          const uint32_t vote = __ballot_sync(kAll, free);
+        pg.counts, slice, first_batch, lane,
+        [&](int page, int count) {
+          const uint32_t vote = __ballot_sync(kAll, count == 0);
           const uint32_t to = free_at + __popc(vote & ((1u << lane) - 1u));
-          if (free && to < wanted) p.free_ids[to] = page;
+          if (count == 0 && to < most) (near ? sm.free_ids : p.free_ids)[to] = page;
           free_at += __popc(vote);
         },
-        [&] { return free_at < wanted; });
-  cluster_sync();
+        [&] { return free_at < most; });
+  if (near) __syncthreads();
+  else cluster_sync();
 
   for_pages(Four{}, [&](Place* q, auto n) {
     constexpr int U = decltype(n)::value;
@@ -427,7 +450,8 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
       wants[j] = q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
       const bool copies = wants[j] && shared && q[j].rows > 0;
       const uint32_t want_vote = __ballot_sync(kAll, wants[j]), copy_vote = __ballot_sync(kAll, copies);
-      page[j] = wants[j] ? __ldcg(p.free_ids + page_at + __popc(want_vote & before_mask)) : 0;
+      const uint64_t at = page_at + __popc(want_vote & before_mask);
+      page[j] = !wants[j] ? 0 : near ? sm.free_ids[at] : __ldcg(p.free_ids + at);
       copy[j] = copies ? p.copies + 3 * (copy_at + __popc(copy_vote & before_mask)) : nullptr;
       page_at += __popc(want_vote & group_mask);
       copy_at += __popc(copy_vote & group_mask);
@@ -461,13 +485,15 @@ __global__ void __launch_bounds__(kClusterThreads) cache_compact_kernel(const Co
   const int lane = static_cast<int>(lane_id());
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
   const int n = slice.end - slice.begin;
-  const int mine = n - free_pages(pg.counts, slice);
+  const Batch first_batch = load_batch(pg.counts, slice, slice.begin, lane);
+  const int mine = n - free_pages(pg.counts, slice, first_batch, lane);
   Sums all;
   int at = static_cast<int>(cluster_scan<0>(0u, 0u, static_cast<uint64_t>(mine), sm, 0, rank, ctas, &all).w);  // before this warp's
   const int used = static_cast<int>(all.w);
   const bool apart = p.counts_out != pg.counts;
   int movers = 0;
-  for_slice(pg.counts, slice, [&](int page, int count, bool in) {
+  for_slice(pg.counts, slice, first_batch, lane, [&](int page, int count) {
+    const bool in = page < slice.end;
     const uint32_t vote = __ballot_sync(kAll, in && count != 0);
     const int before = at + __popc(vote & ((1u << lane) - 1u));  // used pages before this
     at += __popc(vote);
