@@ -28,43 +28,51 @@ constexpr uint32_t kAll = 0xffffffffu;
 
 // ---------------------------------------------------------------- fork
 
-// Row r becomes row parents[r], all rows at once. A block takes kCols columns
+// Row r becomes row parents[r], all rows at once. A block takes some columns
 // of every row through shared memory, which is what makes it safe in place:
 // no other block reads or writes them. A count changes only where an entry
 // does, so that the pages that a row shares with its parent already cost
 // nothing.
 constexpr int kForkThreads = 512;
-constexpr int kForkEntries = kForkMaxRows;  // of a block: 128 KB of shared memory
+constexpr int kForkEntries = kForkMaxRows;  // of a block at most
+constexpr int kForkFew = 1024;              // where there are blocks enough
+constexpr int kForkStaged = 16384;          // rows whose parents fit beside their entries
+constexpr int kForkBytes = 4 * (kForkEntries + kForkStaged);
+static_assert(kForkBytes <= 227 * 1024, "shared memory of a block");
 
 __global__ void __launch_bounds__(kForkThreads)
     cache_fork_kernel(const PagesProblem p, int32_t* lens, const int32_t* parents, int cols_log2) {
-  extern __shared__ int32_t old[];  // [B][cols]
+  extern __shared__ int32_t old[];  // [B][cols], then the parents where both fit
   griddep_wait();
   griddep_launch_dependents();
-  const int cols = 1 << cols_log2;
   const bool for_lens = lens != nullptr && blockIdx.x == gridDim.x - 1;
-  const int n = for_lens ? p.B : p.B << cols_log2;
-  const int col0 = static_cast<int>(blockIdx.x) << cols_log2;
+  const int shift = for_lens ? 0 : cols_log2, mask = (1 << shift) - 1;
+  const int n = p.B << shift;
+  const int col0 = static_cast<int>(blockIdx.x) << shift;
+  const bool staged = p.B <= kForkStaged;
+  int32_t* parent_of = old + (p.B << cols_log2);
   auto entry = [&](int i) -> int32_t* {
     if (for_lens) return lens + i;
-    const int col = col0 + (i & (cols - 1));
-    return col < p.max_pages ? p.table + static_cast<int64_t>(i >> cols_log2) * p.max_pages + col : nullptr;
+    const int col = col0 + (i & mask);
+    return col < p.max_pages ? p.table + static_cast<int64_t>(i >> shift) * p.max_pages + col : nullptr;
   };
+#pragma unroll 2
+  for (int i = threadIdx.x; staged && i < p.B; i += kForkThreads) parent_of[i] = __ldg(parents + i);
+#pragma unroll 4
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
     const int32_t* e = entry(i);
     old[i] = e ? *e : -1;
   }
   __syncthreads();
-  const int shift = for_lens ? 0 : cols_log2;
+#pragma unroll 2
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
-    const int r = i >> shift;
-    const int parent = __ldg(parents + r);
+    const int parent = staged ? parent_of[i >> shift] : __ldg(parents + (i >> shift));
     if (parent < -1 || parent >= p.B) {
       if (for_lens || blockIdx.x == 0) atomicOr(&g_device_error, kErrIndex);
       continue;
     }
     const int32_t was = old[i];
-    const int32_t now = parent < 0 ? (for_lens ? 0 : -1) : old[(parent << shift) | (i & ((1 << shift) - 1))];
+    const int32_t now = parent < 0 ? (for_lens ? 0 : -1) : old[(parent << shift) | (i & mask)];
     if (now == was) continue;
     int32_t* e = entry(i);
     if (e == nullptr) continue;
@@ -105,6 +113,13 @@ __global__ void __launch_bounds__(kReleaseThreads)
 constexpr int kClusterThreads = 1024;
 constexpr int kMaxCtas = 8;  // of the cluster (the portable size)
 constexpr int kWarps = kClusterThreads / 32;
+
+// A barrier of the cluster: of its one block where it has no more (a third of the
+// time), which orders the block's accesses to global memory too.
+__device__ __forceinline__ void sync_all(uint32_t ctas) {
+  if (ctas == 1) __syncthreads();
+  else cluster_sync();
+}
 
 // Two sums, over threads.
 struct Sums {
@@ -153,15 +168,19 @@ __device__ __forceinline__ Sums cluster_scan(uint32_t v, uint32_t w, uint64_t mo
       }
     }
     sm.warp[lane] = {sum.v - mine.v, sum.w - mine.w};
+    if (ctas == 1 && lane == 31) {
+      sm.before = {0, 0};
+      sm.all = sum;
+    }
     const uint64_t cta_v = __shfl_sync(kAll, sum.v, 31), cta_w = __shfl_sync(kAll, sum.w, 31);
-    if (lane < static_cast<int>(ctas)) {
+    if (ctas > 1 && lane < static_cast<int>(ctas)) {
       const uint32_t to = cluster_map(&sm.cta[row][rank], static_cast<uint32_t>(lane));
       st_cluster_u64(to, cta_v);
       st_cluster_u64(to + 8, cta_w);
     }
   }
-  cluster_sync();
-  if (warp == 0) {
+  if (ctas > 1) cluster_sync();
+  if (ctas > 1 && warp == 0) {
     Sums mine = {0, 0};
     if (lane < static_cast<int>(ctas)) mine = sm.cta[row][lane];
     Sums sum = mine;
@@ -374,12 +393,12 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     for_pages(Single{}, [&](Place* q, auto) {
       if (q->at && marked(q->entry)) atomicSub(pg.counts + marked_page(q->entry), 1);
     });
-    cluster_sync();
+    sync_all(ctas);
     for_pages(Single{}, [&](Place* q, auto) {
       if (q->at && marked(q->entry) && __ldcg(pg.counts + marked_page(q->entry)) <= 0)
         atomicMin(pg.counts + marked_page(q->entry), INT32_MIN + q->row);
     });
-    cluster_sync();
+    sync_all(ctas);
     need = 0;
     uint32_t copies = 0;
     for_pages(Single{}, [&](Place* q, auto) {
@@ -410,7 +429,7 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
       for_pages(Single{}, [&](Place* q, auto) {
         if (q->at && marked(q->entry) && keeps(*q)) pg.counts[marked_page(q->entry)] = 0;
       });
-      cluster_sync();
+      sync_all(ctas);
       for_pages(Single{}, [&](Place* q, auto) {
         if (!q->at || !marked(q->entry)) return;
         atomicAdd(pg.counts + marked_page(q->entry), 1);
@@ -436,7 +455,7 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
         },
         [&] { return free_at < most; });
   if (near) __syncthreads();
-  else cluster_sync();
+  else sync_all(ctas);
 
   for_pages(Four{}, [&](Place* q, auto n) {
     constexpr int U = decltype(n)::value;
@@ -584,17 +603,18 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), int64_t work, cudaStream_t 
 
 cudaError_t launch_cache_fork(const PagesProblem& p, int32_t* lens, const int32_t* parents,
                               cudaStream_t stream) {
-  // columns to a block: as many as fit, but no fewer blocks than SMs for it
-  // (8 columns are a sector of memory)
-  int cols_log2 = 5;
-  while (cols_log2 > 0 && (static_cast<int64_t>(p.B) << cols_log2) > kForkEntries) --cols_log2;
-  while (cols_log2 > 3 && (p.max_pages >> cols_log2) < sm_count()) --cols_log2;
+  // columns to a block: two entries to a thread, or up to 32 columns (a line of
+  // memory) where that leaves four blocks to an SM
+  int cols_log2 = 0;
+  while (cols_log2 < 5 && (static_cast<int64_t>(p.B) << (cols_log2 + 1)) <= kForkEntries &&
+         ((p.B << (cols_log2 + 1)) <= kForkFew || (p.max_pages >> (cols_log2 + 1)) >= 4 * sm_count()))
+    ++cols_log2;
   static unsigned long long configured = 0;
-  cudaError_t e = set_smem_once(cache_fork_kernel, kForkEntries * 4, &configured);
+  cudaError_t e = set_smem_once(cache_fork_kernel, kForkBytes, &configured);
   if (e != cudaSuccess) return e;
   const int64_t blocks = ((static_cast<int64_t>(p.max_pages) - 1) >> cols_log2) + 1 + (lens ? 1 : 0);
   return launch_pdl(cache_fork_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kForkThreads),
-                    (static_cast<size_t>(p.B) << cols_log2) * 4, stream, p, lens, parents, cols_log2);
+                    ((static_cast<size_t>(p.B) << cols_log2) + (p.B <= kForkStaged ? p.B : 0)) * 4, stream, p, lens, parents, cols_log2);
 }
 
 cudaError_t launch_cache_release(const PagesProblem& p, const int32_t* keep_lens, cudaStream_t stream) {
