@@ -20,6 +20,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kInFlight = 8;
+constexpr int kBlocksPerSm = 3;
 constexpr int kPiece = 32 * kInFlight * 16;  // bytes
 
 struct Pieces {
@@ -27,31 +28,7 @@ struct Pieces {
   int in_layer;
 };
 
-// Bytes [begin, begin + kPiece) of `runs` runs of run_bytes, `stride` apart, in
-// vectors of `Vec` (a divisor of run_bytes).
-template <typename Vec>
-__device__ __forceinline__ void copy_runs(uint8_t* to, const uint8_t* from, int begin, int runs, int run_bytes, int stride,
-                                          int lane) {
-  constexpr int kBytes = static_cast<int>(sizeof(Vec));
-  const int per = run_bytes / kBytes;
-  const int n = min(runs * per, (begin + kPiece) / kBytes);
-  for (int e0 = begin / kBytes + lane; e0 - lane < n; e0 += 32 * kInFlight) {
-    Vec v[kInFlight];
-    int64_t at[kInFlight];
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i) {
-      const int e = e0 + i * 32;
-      const int run = e / per;
-      at[i] = static_cast<int64_t>(run) * stride + (e - run * per) * kBytes;
-      if (e < n) v[i] = __ldcs(reinterpret_cast<const Vec*>(from + at[i]));
-    }
-#pragma unroll
-    for (int i = 0; i < kInFlight; ++i)
-      if (e0 + i * 32 < n) *reinterpret_cast<Vec*>(to + at[i]) = v[i];
-  }
-}
-
-__global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyProblem p, const Pieces pieces) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(const CopyProblem p, const Pieces pieces) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(lane_id());
@@ -96,23 +73,62 @@ __global__ void __launch_bounds__(kThreads) cache_copy_kernel(const CopyProblem 
     base += layer * p.layer_rows * row;
     const uint8_t* src = base + static_cast<int64_t>(from) * page_bytes;
     uint8_t* dst = base + static_cast<int64_t>(to) * page_bytes;
-    const int begin = piece * kPiece;
-    const int run_bytes = rows * row;
-    if (rows == page_size) {  // one run
-      const int last = min(begin + kPiece, page_bytes) - begin;
-      src += begin;
-      dst += begin;
-      uint4 v[kInFlight];
+    // 16 bytes at a time; a run's last ones may be 4, 8 or 12: scales of a part
+    // of a page, where a row has 4 bytes (64 columns) or 8
+    const bool whole = rows == page_size;  // one run
+    const int run_bytes = whole ? page_bytes : rows * row;
+    const int per = (run_bytes + 15) / 16, rest_bytes = run_bytes & 15;
+    const int n = whole ? per : p.h_kv * per;
+    const int begin = piece * (kPiece / 16);
+    if (begin >= n) continue;
+    int at[kInFlight];  // where this lane's lie in the page; -1: none
+    uint32_t cut = 0u;  // bit i: the i-th is a run's last and short
+    const float inverse = 1.f / static_cast<float>(per);
+#pragma unroll
+    for (int i = 0; i < kInFlight; ++i) {
+      const int e = begin + i * 32 + lane;
+      at[i] = e * 16;
+      if (!whole) {
+        // the product is 1 / (2 per) off a whole number at least, and below 2^20 off by a quarter of that
+        const int run = n < 1 << 20 ? static_cast<int>((static_cast<float>(e) + 0.5f) * inverse) : e / per;
+        at[i] = run * (row << p.page_shift) + (e - run * per) * 16;
+        if (rest_bytes != 0 && e - run * per == per - 1) cut |= 1u << i;
+      }
+      if (e >= n) at[i] = -1;
+    }
+    uint4 v[kInFlight];
+    if (rest_bytes == 0) {
 #pragma unroll
       for (int i = 0; i < kInFlight; ++i)
-        if ((i * 32 + lane) * 16 < last) v[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i * 32 + lane);
+        if (at[i] >= 0) v[i] = __ldcs(reinterpret_cast<const uint4*>(src + at[i]));
 #pragma unroll
       for (int i = 0; i < kInFlight; ++i)
-        if ((i * 32 + lane) * 16 < last) reinterpret_cast<uint4*>(dst)[i * 32 + lane] = v[i];
-    } else if (begin < p.h_kv * run_bytes) {
-      // scales of a row: 4 bytes for 64 columns, 8 for 128
-      if (run_bytes % 16 == 0) copy_runs<uint4>(dst, src, begin, p.h_kv, run_bytes, row << p.page_shift, lane);
-      else copy_runs<uint32_t>(dst, src, begin, p.h_kv, run_bytes, row << p.page_shift, lane);
+        if (at[i] >= 0) *reinterpret_cast<uint4*>(dst + at[i]) = v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        if (at[i] < 0) continue;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(src + at[i]);
+        if (cut >> i & 1u) {
+          v[i].x = __ldcs(w);
+          if (rest_bytes > 4) v[i].y = __ldcs(w + 1);
+          if (rest_bytes > 8) v[i].z = __ldcs(w + 2);
+        } else {
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(w));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kInFlight; ++i) {
+        if (at[i] < 0) continue;
+        uint32_t* w = reinterpret_cast<uint32_t*>(dst + at[i]);
+        if (cut >> i & 1u) {
+          w[0] = v[i].x;
+          if (rest_bytes > 4) w[1] = v[i].y;
+          if (rest_bytes > 8) w[2] = v[i].z;
+        } else {
+          *reinterpret_cast<uint4*>(w) = v[i];
+        }
+      }
     }
   }
 }
@@ -130,9 +146,15 @@ cudaError_t launch_cache_copy(const CopyProblem& p, cudaStream_t stream) {
     pieces.in_layer += static_cast<int>(((static_cast<int64_t>(p.h_kv) * p.row_bytes[i] << p.page_shift) + kPiece - 1) / kPiece);
   }
   const int64_t units = static_cast<int64_t>(p.max_copies) * p.n_layers * pieces.in_layer;
-  const int64_t blocks = (units + kWarps - 1) / kWarps, grid = static_cast<int64_t>(sms) * 8;
-  return launch_pdl(cache_copy_kernel, dim3(static_cast<unsigned>(blocks < grid ? blocks : grid)), dim3(kThreads), 0, stream, p,
-                    pieces);
+  // A long list is shared out among more blocks than are resident, so that SMs
+  // which are done sooner take more of them; a short one goes to the resident
+  // ones, as a block more costs more than a second round (in us, 8 and 3 blocks
+  // to an SM: 2500 whole pages of 64 KB in 4 layers 176 and 184, 240 of 32 KB in 6
+  // layers 17.7 and 18.4 with the plan; parts of 120 4-bit pages in 4 layers, 1152
+  // blocks' pieces, 15.6 and 14.4 with the step).
+  const int64_t blocks = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 8, resident = sms * kBlocksPerSm;
+  const int64_t grid = blocks > most ? most : blocks > resident ? resident : blocks;
+  return launch_pdl(cache_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, p, pieces);
 }
 
 TSD_DEFINE_ERROR_READER(take_device_error_copy)
