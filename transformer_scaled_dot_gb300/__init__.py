@@ -173,23 +173,31 @@ def library():
 
 def _ptr(x):
     """Address of a torch tensor (device or host), a numpy array (host), or an int."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
     data_ptr = getattr(x, "data_ptr", None)
-    return x.ctypes.data if data_ptr is None else data_ptr()
+    if data_ptr is not None:
+        return data_ptr()
+    return x if isinstance(x, int) else x.ctypes.data
+
+
+_raw_stream = _device = None  # torch's, from the first call that finds CUDA up
 
 
 def _current_stream():
     """torch's current stream, as a raw cudaStream_t. torch.cuda.current_stream() makes a Stream
     object first (2.9 us against 0.2 us on the Grace host, more than a short kernel's launch),
     so its raw form is asked where torch has it and CUDA is up."""
+    global _raw_stream, _device
+    if _raw_stream is not None:
+        return _raw_stream(_device())
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     if raw is None or not torch.cuda.is_initialized():
         return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = raw
+    return raw(_device())
 
 
 def _stream(s):

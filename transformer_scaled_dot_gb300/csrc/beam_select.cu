@@ -655,15 +655,23 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
     if (more) __syncthreads();  // all have seen the count before it grows
   }
 
-  // their pairs, a warp to a tile
+  // their pairs, a warp to a tile, the next one's logits on their way
   const int listed = sm.n_tiles;
+  auto row_of = [&](int k) {
+    return static_cast<const uint8_t*>(p.logits) + (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
+  };
+  Tile<F32, ALIGNED> next;
+  auto load = [&](int i) {
+    const int tile = sm.tile[i], k = tile / tiles;
+    next.load(row_of(k), tile - k * tiles, p.vocab, lane);
+  };
+  if (warp < listed) load(warp);
 #pragma unroll 1
   for (int i = warp; i < listed; i += kPickWarps) {
-    const int tile = sm.tile[i], k = tile / tiles, t = tile % tiles;
-    const uint8_t* row = static_cast<const uint8_t*>(p.logits) +
-                         (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
-    Tile<F32, ALIGNED> x;
-    x.load(row, t, p.vocab, lane);
+    const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
+    const uint8_t* row = row_of(k);
+    const Tile<F32, ALIGNED> x = next;
+    if (i + kPickWarps < listed) load(i + kPickWarps);
     const Beam beam = sm.beam[k];
     // Logits below `least` are not among the best: the logit at which the last
     // group's total is reached, less what this sum of 32 bits may be off.

@@ -136,10 +136,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(cons
 }  // namespace
 
 cudaError_t launch_cache_copy(const CopyProblem& p, cudaStream_t stream) {
-  int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
+  static int cached = 0;  // atomic accesses: launches may come from several host threads
+  int sms = __atomic_load_n(&cached, __ATOMIC_RELAXED);
+  if (sms == 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    __atomic_store_n(&cached, sms, __ATOMIC_RELAXED);
+  }
   Pieces pieces = {};
   for (int i = 0; i < p.n_pools; ++i) {
     pieces.before[i] = pieces.in_layer;

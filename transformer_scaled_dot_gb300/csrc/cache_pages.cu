@@ -232,11 +232,11 @@ __device__ __forceinline__ Batch load_batch(const int32_t* counts, const Slice& 
 template <typename F, typename G>
 __device__ __forceinline__ void for_slice(const int32_t* counts, const Slice& s, Batch batch, int lane, F f, G go) {
 #pragma unroll 1
-  for (int i = s.begin; i < s.end && go();) {
+  for (int i = s.begin; i < s.end && go(); i += 32 * kBatch) {
+    const Batch now = batch;
+    if (i + 32 * kBatch < s.end) batch = load_batch(counts, s, i + 32 * kBatch, lane);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) f(i + 32 * j + lane, batch.c[j]);
-    i += 32 * kBatch;
-    if (i < s.end) batch = load_batch(counts, s, i, lane);
+    for (int j = 0; j < kBatch; ++j) f(i + 32 * j + lane, now.c[j]);
   }
 }
 // How many of a warp's pages are free, in every lane.
@@ -256,18 +256,17 @@ struct RowRange {
 };
 
 __device__ __forceinline__ RowRange row_range(const ReserveProblem& p, int b) {
-  const int64_t room = static_cast<int64_t>(p.pages.max_pages) << p.pages.page_shift;
-  int64_t len = __ldg(p.lens + b);
+  const int room = p.pages.max_pages << p.pages.page_shift;  // 2^30 at most
+  int len = __ldg(p.lens + b);
   const int m = p.new_lens ? min(max(__ldg(p.new_lens + b), 0), p.n_new) : p.n_new;
-  const int64_t start = len - m > 0 ? len - m : 0;
+  const int start = len > m ? len - m : 0;
   if (len > room) {
     atomicOr(&g_device_error, kErrIndex);
     len = room;
   }
   if (m == 0 || len <= start) return {0, 0, 0};
   const int page = 1 << p.pages.page_shift;
-  return {static_cast<int>(start >> p.pages.page_shift), static_cast<int>((len + page - 1) >> p.pages.page_shift),
-          static_cast<int>(start & (page - 1))};
+  return {start >> p.pages.page_shift, (len + page - 1) >> p.pages.page_shift, start & (page - 1)};
 }
 
 // A table entry that names a page which other entries name too is marked
@@ -337,7 +336,9 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
         Place q[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          q[j] = look_up(row, unit, i + j < per && row < pg.B);
+          q[j] = {0, 0, 0, nullptr};
+          if (i + j >= per) continue;
+          q[j] = look_up(row, unit, row < pg.B);
           if (++unit == units) {
             unit = 0;
             ++row;
@@ -351,14 +352,14 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     }
   };
   using Single = std::integral_constant<int, 1>;
-  using Four = std::integral_constant<int, 4>;
+  using Two = std::integral_constant<int, 2>;
 
   const int free_here = free_pages(pg.counts, slice, first_batch, lane);
 
   // what the rows need, and which entries name shared pages
   uint32_t need = 0;
   bool any = false;
-  for_pages(Four{}, [&](Place* q, auto n) {
+  for_pages(Two{}, [&](Place* q, auto n) {
     constexpr int U = decltype(n)::value;
     int count[U];
 #pragma unroll
@@ -443,6 +444,7 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   // shared pages' counts were above 0 when this warp's first batch was read,
   // and are not 0 now: one that was taken there has its keeper's number.)
   const bool near = ctas == 1 && wanted <= kNear;
+  int32_t* free_ids = near ? sm.free_ids : p.free_ids;
   const uint32_t most = static_cast<uint32_t>(wanted);  // n_free at most
   if (free_here > 0)
     for_slice(
@@ -450,14 +452,15 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
         [&](int page, int count) {
           const uint32_t vote = __ballot_sync(kAll, count == 0);
           const uint32_t to = free_at + __popc(vote & ((1u << lane) - 1u));
-          if (count == 0 && to < most) (near ? sm.free_ids : p.free_ids)[to] = page;
+          if (count == 0 && to < most) free_ids[to] = page;
           free_at += __popc(vote);
         },
         [&] { return free_at < most; });
   if (near) __syncthreads();
   else sync_all(ctas);
 
-  for_pages(Four{}, [&](Place* q, auto n) {
+  uint32_t page_to = static_cast<uint32_t>(page_at), copy_to = static_cast<uint32_t>(copy_at);
+  for_pages(Two{}, [&](Place* q, auto n) {
     constexpr int U = decltype(n)::value;
     int page[U];
     int32_t* copy[U];
@@ -469,11 +472,11 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
       wants[j] = q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
       const bool copies = wants[j] && shared && q[j].rows > 0;
       const uint32_t want_vote = __ballot_sync(kAll, wants[j]), copy_vote = __ballot_sync(kAll, copies);
-      const uint64_t at = page_at + __popc(want_vote & before_mask);
+      const uint32_t at = page_to + __popc(want_vote & before_mask);
       page[j] = !wants[j] ? 0 : near ? sm.free_ids[at] : __ldcg(p.free_ids + at);
-      copy[j] = copies ? p.copies + 3 * (copy_at + __popc(copy_vote & before_mask)) : nullptr;
-      page_at += __popc(want_vote & group_mask);
-      copy_at += __popc(copy_vote & group_mask);
+      copy[j] = copies ? p.copies + 3 * (copy_to + __popc(copy_vote & before_mask)) : nullptr;
+      page_to += __popc(want_vote & group_mask);
+      copy_to += __popc(copy_vote & group_mask);
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
