@@ -771,6 +771,7 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  *               are). At a sentence's start: 0, and -infinity for the others
  *   lengths     int32[B]: tokens of the hypotheses, the one chosen now among
  *               them (less than 1 counts as 1)
+ *   alpha       finite (a double: 0.6 is no number of 32 bits)
  *   end         the end token, or -1: none; then lengths, alpha and the ended_*
  *               arrays are ignored
  *   tokens, parents  int32[B, beams], written: the token, and the row b * beams
@@ -790,11 +791,12 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  * score hold a NaN or +infinity has no candidates, and attn_get_device_status
  * answers ATTN_ERR_DEVICE_VALUE once. Totals are formed and compared in 48 bits
  * from exponentials and partial sums in 32. beams = 1 is greedy decoding.
- * Errors as attn_forward. Two launches.
+ * Errors as attn_forward. Two launches, or one where sentences and vocabulary are
+ * small.
  */
 size_t beam_select_workspace_bytes(int B, int beams, int vocab);
 attn_status beam_select(const void *logits, int64_t row_stride, const float *scores,
-                        const int32_t *lengths, int B, int beams, int vocab, int end, float alpha,
+                        const int32_t *lengths, int B, int beams, int vocab, int end, double alpha,
                         int32_t *tokens, int32_t *parents, float *new_scores, float *ended_scores,
                         int32_t *ended_rows, int32_t *ended_lengths, void *workspace,
                         size_t workspace_bytes, tsd_stream_t stream);
@@ -802,7 +804,7 @@ attn_status beam_select(const void *logits, int64_t row_stride, const float *sco
 /* beam_select_f32 -- beam_select of fp32 logits (4-byte aligned). */
 attn_status beam_select_f32(const float *logits, int64_t row_stride, const float *scores,
                             const int32_t *lengths, int B, int beams, int vocab, int end,
-                            float alpha, int32_t *tokens, int32_t *parents, float *new_scores,
+                            double alpha, int32_t *tokens, int32_t *parents, float *new_scores,
                             float *ended_scores, int32_t *ended_rows, int32_t *ended_lengths,
                             void *workspace, size_t workspace_bytes, tsd_stream_t stream);
 

@@ -153,7 +153,7 @@ def library():
     lib.beam_select_workspace_bytes.argtypes = [i] * 3
     lib.beam_select_workspace_bytes.restype = sz
     for name in ("beam_select", "beam_select_f32"):
-        getattr(lib, name).argtypes = [vp, i64, vp, vp, i, i, i, i, f] + [vp] * 7 + [sz, st]
+        getattr(lib, name).argtypes = [vp, i64, vp, vp, i, i, i, i, ctypes.c_double] + [vp] * 7 + [sz, st]
         getattr(lib, name).restype = ctypes.c_int
     for name in ("attn_cache_fork", "attn_cache_release", "attn_cache_reserve",
                  "attn_cache_compact", "attn_cache_copy", "attn_cache_copy_q4",

@@ -799,13 +799,14 @@ attn_status beam_size_check(int B, int beams, int vocab) {
 
 attn_status run_beam_select(const void* logits, bool f32, int64_t row_stride, const float* scores,
                             const int32_t* lengths, int B, int beams, int vocab, int end,
-                            float alpha, int32_t* tokens, int32_t* parents, float* new_scores,
+                            double alpha, int32_t* tokens, int32_t* parents, float* new_scores,
                             float* ended_scores, int32_t* ended_rows, int32_t* ended_lengths,
                             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   attn_status s = beam_size_check(B, beams, vocab);
   if (s != ATTN_OK) return s;
   if (row_stride < vocab || row_stride > INT64_MAX / 8 / (int64_t(B) * beams + 1)) return ATTN_ERR_INVALID;
-  if (end < -1 || !std::isfinite(alpha)) return ATTN_ERR_INVALID;
+  const float alpha_high = static_cast<float>(alpha);
+  if (end < -1 || !std::isfinite(alpha_high)) return ATTN_ERR_INVALID;
   if (!logits || (reinterpret_cast<uintptr_t>(logits) & (f32 ? 3u : 1u))) return ATTN_ERR_INVALID;
   for (const void* p : {static_cast<const void*>(scores), static_cast<const void*>(tokens),
                         static_cast<const void*>(parents), static_cast<const void*>(new_scores)})
@@ -817,8 +818,8 @@ attn_status run_beam_select(const void* logits, bool f32, int64_t row_stride, co
   if (!workspace || !aligned16(workspace) || workspace_bytes < beam_select_workspace_bytes(B, beams, vocab))
     return ATTN_ERR_INVALID;
   if (B == 0) return ATTN_OK;
-  const tsd::BeamProblem p = {logits, f32, row_stride, scores, lengths, B, beams, vocab, end, alpha,
-                              tokens, parents, new_scores, ended_scores, ended_rows, ended_lengths,
+  const tsd::BeamProblem p = {logits, f32, row_stride, scores, lengths, B, beams, vocab, end, alpha_high,
+                              static_cast<float>(alpha - alpha_high), tokens, parents, new_scores, ended_scores, ended_rows, ended_lengths,
                               workspace};
   cudaError_t e = tsd::launch_beam_select(p, stream);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
@@ -1341,7 +1342,7 @@ size_t beam_select_workspace_bytes(int B, int beams, int vocab) {
 }
 
 attn_status beam_select(const void* logits, int64_t row_stride, const float* scores,
-                        const int32_t* lengths, int B, int beams, int vocab, int end, float alpha,
+                        const int32_t* lengths, int B, int beams, int vocab, int end, double alpha,
                         int32_t* tokens, int32_t* parents, float* new_scores, float* ended_scores,
                         int32_t* ended_rows, int32_t* ended_lengths, void* workspace,
                         size_t workspace_bytes, tsd_stream_t stream) {
@@ -1352,7 +1353,7 @@ attn_status beam_select(const void* logits, int64_t row_stride, const float* sco
 
 attn_status beam_select_f32(const float* logits, int64_t row_stride, const float* scores,
                             const int32_t* lengths, int B, int beams, int vocab, int end,
-                            float alpha, int32_t* tokens, int32_t* parents, float* new_scores,
+                            double alpha, int32_t* tokens, int32_t* parents, float* new_scores,
                             float* ended_scores, int32_t* ended_rows, int32_t* ended_lengths,
                             void* workspace, size_t workspace_bytes, tsd_stream_t stream) {
   return run_beam_select(logits, true, row_stride, scores, lengths, B, beams, vocab, end, alpha,

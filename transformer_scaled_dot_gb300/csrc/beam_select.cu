@@ -16,7 +16,8 @@
 // is enough: a pair among the best M lies in one of the M tiles with the best
 // maxima (each tile ahead of its own holds a pair that beats it). beam_pick, a
 // block to a sentence, joins a row's tiles to its log-sum, picks those M tiles
-// and then the M pairs in them.
+// and then the M pairs in them. Few short rows go through beam_one, which is
+// both in one launch.
 // Totals that lie next to one another decide which token a beam takes: they
 // are formed and compared as pairs of fp32, 48 bits. Exponentials and a tile's
 // sum are in 32, relative to the tile's own maximum, as are the few tiles of a
@@ -405,13 +406,13 @@ __device__ __forceinline__ Pair exp_pair(Pair x, int* exponent) {
 }
 
 // The length penalty ((5 + n) / 6)^alpha as value * 2^exponent.
-__device__ __forceinline__ Pair length_penalty(int n, float alpha, int* exponent) {
+__device__ __forceinline__ Pair length_penalty(int n, Pair alpha, int* exponent) {
   const int64_t top = static_cast<int64_t>(n) + 5;
   const float h = static_cast<float>(top);
   constexpr float kLn6Hi = 0x1.cab0cp+0f, kLn6Lo = -2.1738742e-08f;
   const Pair base = add(log_pair({h, static_cast<float>(top - static_cast<int64_t>(h))}), {-kLn6Hi, -kLn6Lo});
-  float x = alpha * base.h;
-  float rest = __fmaf_rn(alpha, base.h, -x) + alpha * base.l;
+  float x = alpha.h * base.h;
+  float rest = __fmaf_rn(alpha.h, base.h, -x) + (alpha.h * base.l + alpha.l * base.h);
   // e^300 and e^-300 take every score to 0 or beyond fp32 already
   if (!(fabsf(x) < 300.f)) {
     x = copysignf(300.f, x);
@@ -516,20 +517,19 @@ __device__ __forceinline__ Pair warp_sum(float x) {
   return settled(h * 0x1p-6f, static_cast<float>(high & 0xffu) * 0x1p-6f + static_cast<float>(low) * 0x1p-30f);
 }
 
+// The choice of sentence b by a block, given its tiles' records: in `records`,
+// or (null) in sm.key already.
 template <bool F32, bool ALIGNED>
-__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProblem p, int tiles) {
-  extern __shared__ __align__(16) uint8_t smem_raw[];
-  PickSmem& sm = *reinterpret_cast<PickSmem*>(smem_raw);
-  griddep_wait();
-  griddep_launch_dependents();
-  const int b = static_cast<int>(blockIdx.x), K = p.beams;
+__device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, PickSmem& sm, const uint64_t* records) {
+  const int K = p.beams;
   const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = static_cast<int>(lane_id());
   const int M = p.end >= 0 ? 2 * K : K;
   const int n = K * tiles;  // below 2^14
-  const uint64_t* records = static_cast<const uint64_t*>(p.workspace) + static_cast<int64_t>(b) * n;
 
+  if (records != nullptr) {
 #pragma unroll 4
-  for (int i = tid; i < n; i += kPickThreads) sm.key[i] = __ldcg(reinterpret_cast<const unsigned long long*>(records) + i);
+    for (int i = tid; i < n; i += kPickThreads) sm.key[i] = __ldcg(reinterpret_cast<const unsigned long long*>(records) + i);
+  }
   // what the last step needs
   float score = -INFINITY, ended = -INFINITY;
   int end_row = 0, end_length = 0;
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
   if (warp == kPickWarps - 1 && p.end >= 0) {
     int exponent;
     const int length = max(__ldcg(p.lengths + b), 1);
-    const Pair penalty = length_penalty(length, p.alpha, &exponent);
+    const Pair penalty = length_penalty(length, {p.alpha, p.alpha_rest}, &exponent);
     if (lane == 0) {
       sm.length = length;
       sm.penalty = penalty;
@@ -796,6 +796,46 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
 }
 
 template <bool F32, bool ALIGNED>
+__global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProblem p, int tiles) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  griddep_wait();
+  griddep_launch_dependents();
+  pick<F32, ALIGNED>(p, tiles, static_cast<int>(blockIdx.x), *reinterpret_cast<PickSmem*>(smem_raw),
+                     static_cast<const uint64_t*>(p.workspace) + static_cast<int64_t>(blockIdx.x) * p.beams * tiles);
+}
+
+// Few short sentences in one launch: a cluster to a sentence, whose warps take
+// its tiles straight from memory and write their records into the first block's
+// shared memory, which then chooses. For up to a tile to a warp and 8 sentences:
+// 4 beams of 32000 tokens 6.5 us (two launches 6.9, and 2 us more on the host), 8
+// sentences of them 6.65 (7.0), 16 of them 8.1 (7.35: the clusters do not all fit);
+// 8 beams, two tiles to a warp, 10.4 (9.0).
+constexpr int kOneCtas = 8;
+constexpr int kOneSentences = 8, kOneTiles = kOneCtas * kPickWarps;
+template <bool F32, bool ALIGNED>
+__global__ void __launch_bounds__(kPickThreads) beam_one_kernel(const BeamProblem p, int tiles) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  PickSmem& sm = *reinterpret_cast<PickSmem*>(smem_raw);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = static_cast<int>(blockIdx.x) / kOneCtas, rank = static_cast<int>(cluster_ctarank());
+  const int lane = static_cast<int>(lane_id());
+  const int n = p.beams * tiles;
+  for (int i = warp_id() * kOneCtas + rank; i < n; i += kOneCtas * kPickWarps) {
+    const int k = i / tiles, row = b * p.beams + k;
+    Tile<F32, ALIGNED> x;
+    x.load(static_cast<const uint8_t*>(p.logits) + row * (p.row_stride * (F32 ? 4 : 2)), i - k * tiles, p.vocab, lane);
+    if (__ldcg(p.scores + row) == -INFINITY) continue;
+    const float2 record = tile_record(x);
+    if (lane == 0)
+      st_cluster_u64(cluster_map(&sm.key[i], 0),
+                     static_cast<uint64_t>(__float_as_uint(record.y)) << 32 | __float_as_uint(record.x));
+  }
+  cluster_sync();
+  if (rank == 0) pick<F32, ALIGNED>(p, tiles, b, sm, nullptr);
+}
+
+template <bool F32, bool ALIGNED>
 cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   using R = Ring<F32, ALIGNED>;
   constexpr int kRingBytes = kTileWarps * static_cast<int>(sizeof(R));
@@ -803,6 +843,27 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   // the largest call's tiles
   constexpr int kPickMost = static_cast<int>(sizeof(PickSmem)) + kBeamMaxBeams * (kBeamMaxVocab / kTile) * 8;
   static_assert(kPickMost <= 227 * 1024, "shared memory of a block");
+  const size_t pick_bytes = sizeof(PickSmem) + static_cast<size_t>(p.beams) * tiles * sizeof(uint64_t);
+  if (p.B <= kOneSentences && p.beams * tiles <= kOneTiles) {
+    static unsigned long long one_configured = 0;
+    cudaError_t e = set_smem_once(beam_one_kernel<F32, ALIGNED>, kPickMost, &one_configured);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * kOneCtas));
+    cfg.blockDim = dim3(kPickThreads);
+    cfg.dynamicSmemBytes = pick_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kOneCtas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, beam_one_kernel<F32, ALIGNED>, p, tiles);
+  }
   static unsigned long long tiles_configured = 0, pick_configured = 0;
   cudaError_t e = set_smem_once(beam_tiles_kernel<F32, ALIGNED>, kRingBytes, &tiles_configured);
   if (e == cudaSuccess) e = set_smem_once(beam_pick_kernel<F32, ALIGNED>, kPickMost, &pick_configured);
@@ -825,8 +886,8 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   e = launch_pdl(beam_tiles_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(blocks < fit ? blocks : fit)),
                  dim3(32 * kTileWarps), kRingBytes, stream, p, tiles, total);
   if (e != cudaSuccess) return e;
-  return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads),
-                    sizeof(PickSmem) + static_cast<size_t>(p.beams) * tiles * sizeof(uint64_t), stream, p, tiles);
+  return launch_pdl(beam_pick_kernel<F32, ALIGNED>, dim3(static_cast<unsigned>(p.B)), dim3(kPickThreads), pick_bytes,
+                    stream, p, tiles);
 }
 
 }  // namespace

@@ -263,7 +263,7 @@ struct BeamProblem {
   const int32_t* lengths;  // [B], with an end token
   int B, beams, vocab;
   int end;              // the end token, or -1
-  float alpha;
+  float alpha, alpha_rest;  // a number as the sum of two
   int32_t* tokens;      // [B, beams]
   int32_t* parents;
   float* new_scores;
