@@ -452,18 +452,20 @@ __device__ __forceinline__ uint64_t total_key(const Beam& beam, float x) {
   return static_cast<uint64_t>(order_bits(t.h)) << 32 | order_bits(t.l);
 }
 
-constexpr int kGroups = 64;     // of a sentence's tiles
+constexpr int kGroups = 64;     // of a sentence's tiles, or of the lanes of some
 constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
+static_assert(kGroups == 2 * 32, "a group's lane");
 constexpr int kTileList = 64;   // chosen tiles that are looked through
 constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
 
 struct PickSmem {
   Beam beam[kBeamMaxBeams];
   uint64_t group_key[kGroups];
-  int group_tile[kGroups];
-  uint64_t last_key;           // the M-th best group's largest total, and its tile
-  int last_tile;
+  int group_at[kGroups];
+  uint64_t last_key;           // the M-th best group's largest total, and its place
+  int last_at;
   int n_tiles, n_pairs;
+  int crowded;                 // a tile has more than M pairs ahead of the last
   int tile[2 * kPickThreads];  // chosen tiles
   uint64_t tile_key[2 * kPickThreads];
   uint64_t pair_key[kPairList];
@@ -507,6 +509,93 @@ __device__ __noinline__ void keep_best_tiles(PickSmem& sm, int M) {
   __syncthreads();
 }
 
+// Groups of eight threads, each thread with its best (key 0: none), the places
+// all different: the M-th best group's best into sm.last_key and sm.last_at;
+// key 0 if so many groups have none.
+__device__ __noinline__ void last_of_groups(PickSmem& sm, uint64_t key, int at, int M) {
+  const int tid = static_cast<int>(threadIdx.x);
+#pragma unroll
+  for (int o = 1; o < kSubs; o <<= 1) {
+    const uint64_t other_key = __shfl_xor_sync(0xffffffffu, key, o);
+    const int other_at = __shfl_xor_sync(0xffffffffu, at, o);
+    if (ahead(other_key, other_at, key, at)) {
+      key = other_key;
+      at = other_at;
+    }
+  }
+  if (tid % kSubs == 0) {
+    sm.group_key[tid / kSubs] = key;
+    sm.group_at[tid / kSubs] = at;
+  }
+  if (tid == 0) {
+    sm.last_key = 0;
+    sm.last_at = INT32_MAX;
+  }
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int j = 0; j < kGroups / kSubs; ++j) {
+    const int g = j * kSubs + tid % kSubs;
+    before += ahead(sm.group_key[g], sm.group_at[g], key, at);
+  }
+#pragma unroll
+  for (int o = 1; o < kSubs; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (before == M - 1 && key != 0 && tid % kSubs == 0) {
+    sm.last_key = key;
+    sm.last_at = at;
+  }
+  __syncthreads();
+}
+
+// Which of its logits of a tile with at least M a lane has among the best M, the
+// lowest places first among equals: the M-th largest, bit by bit of its place in
+// the numbers' order, then the equal ones from the front. 2 us for any M.
+template <bool F32, bool ALIGNED>
+__device__ __noinline__ uint32_t best_of_tile(const uint8_t* row, int t, int vocab, int M, int lane) {
+  constexpr int kPer = Tile<F32, ALIGNED>::kPer;
+  Tile<F32, ALIGNED> x;
+  x.load(row, t, vocab, lane);
+  auto count = [&](float least) {
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) n += x.at(j) >= least;
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+  };
+  uint32_t order = 0u;
+  int at_least = 0;  // how many are `order` or above
+#pragma unroll 1
+  for (int bit = 31; bit >= 0 && at_least != M; --bit) {
+    const int n = count(from_order_bits(order | 1u << bit));  // none for a NaN
+    if (n < M) continue;
+    order |= 1u << bit;
+    at_least = n;
+  }
+  const float last = from_order_bits(order);
+  uint32_t above = 0u, equal = 0u;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    above |= (x.at(j) > last ? 1u : 0u) << j;
+    equal |= (x.at(j) == last ? 1u : 0u) << j;
+  }
+  int left = M - static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(above))));
+  // places go by vectors of kPer, then by lanes
+#pragma unroll 1
+  for (int j = 0; j < 32 && left > 0; j += kPer) {
+    uint32_t mine = kPer == 32 ? equal : equal >> j & ((1u << kPer) - 1u);
+    const int have = __popc(mine);
+    int sum = have;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int other = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += other;
+    }
+    for (int drop = have - max(min(left - (sum - have), have), 0); drop > 0; --drop) mine &= ~(0x80000000u >> __clz(mine));
+    above |= mine << j;
+    left -= __shfl_sync(0xffffffffu, sum, 31);
+  }
+  return above;
+}
+
 // A sum of numbers of 0 .. 2^20 in all over a warp, off by 2^-25 at most: their parts
 // above and below 2^-6 as whole numbers, for which a warp has an instruction.
 __device__ __forceinline__ Pair warp_sum(float x) {
@@ -540,9 +629,7 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
     end_length = __ldcg(p.ended_lengths + b * K + tid);
   }
   if (tid == 0) {
-    sm.n_tiles = sm.n_pairs = 0;
-    sm.last_key = 0;
-    sm.last_tile = INT32_MAX;
+    sm.n_tiles = sm.n_pairs = sm.crowded = 0;
   }
   if (tid < 2 * kBeamMaxBeams) sm.best_at[tid] = INT32_MAX;
   if (warp == kPickWarps - 1 && p.end >= 0) {
@@ -603,39 +690,11 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
       group_tile = i;
     }
   }
-#pragma unroll
-  for (int o = 1; o < kSubs; o <<= 1) {
-    const uint64_t key = __shfl_xor_sync(0xffffffffu, group_key, o);
-    const int tile = __shfl_xor_sync(0xffffffffu, group_tile, o);
-    if (ahead(key, tile, group_key, group_tile)) {
-      group_key = key;
-      group_tile = tile;
-    }
-  }
-  if (tid % kSubs == 0) {
-    sm.group_key[tid / kSubs] = group_key;
-    sm.group_tile[tid / kSubs] = group_tile;
-  }
-  __syncthreads();
   // The M-th of them: the tiles that are ahead of it, or are it, hold the M best
   // pairs, and no pair behind it is one.
-  {
-    int before = 0;
-#pragma unroll
-    for (int j = 0; j < kGroups / kSubs; ++j) {
-      const int g = j * kSubs + tid % kSubs;
-      before += ahead(sm.group_key[g], sm.group_tile[g], group_key, group_tile);
-    }
-#pragma unroll
-    for (int o = 1; o < kSubs; o <<= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    if (before == M - 1 && group_key != 0 && tid % kSubs == 0) {
-      sm.last_key = group_key;
-      sm.last_tile = group_tile;
-    }
-  }
-  __syncthreads();
+  last_of_groups(sm, group_key, group_tile, M);
   const uint64_t last_key = sm.last_key;
-  const int last_tile = sm.last_tile;
+  const int last_tile = sm.last_at;
 
   // those tiles. More than the list holds (the best ones in few groups): the
   // best M of it are kept and it is filled again.
@@ -655,70 +714,98 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
     if (more) __syncthreads();  // all have seen the count before it grows
   }
 
-  // their pairs, a warp to a tile, the next one's logits on their way
+  // Their pairs, a warp to a tile, the next one's logits on their way. Where a
+  // tile has more than M that are not behind the last (as with fewer tiles than M,
+  // or equal logits), the last is looked for again, among the best of each lane
+  // of each tile, and the tiles once more.
   const int listed = sm.n_tiles;
   auto row_of = [&](int k) {
     return static_cast<const uint8_t*>(p.logits) + (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
   };
-  Tile<F32, ALIGNED> next;
-  auto load = [&](int i) {
-    const int tile = sm.tile[i], k = tile / tiles;
-    next.load(row_of(k), tile - k * tiles, p.vocab, lane);
-  };
-  if (warp < listed) load(warp);
+  uint64_t least_key = last_key;
+  int least_at = INT32_MAX;
 #pragma unroll 1
-  for (int i = warp; i < listed; i += kPickWarps) {
-    const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
-    const uint8_t* row = row_of(k);
-    const Tile<F32, ALIGNED> x = next;
-    if (i + kPickWarps < listed) load(i + kPickWarps);
-    const Beam beam = sm.beam[k];
-    // Logits below `least` are not among the best: the logit at which the last
-    // group's total is reached, less what this sum of 32 bits may be off.
-    const float last = key_total(last_key).h;
-    const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
-    float least = (last - beam.base.h) + beam.top - slack;
-    if (last_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
-    uint32_t in = 0u;  // of this lane's logits
-#pragma unroll
-    for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
-    // more than M, as with many equal logits: the best M one by one
-    const bool crowded = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))) > static_cast<unsigned>(M);
-    if (crowded) {
-      uint32_t best_ones = 0u;
+  for (bool again = false;; again = true) {
+    Tile<F32, ALIGNED> next;
+    auto load = [&](int i) {
+      const int tile = sm.tile[i], k = tile / tiles;
+      next.load(row_of(k), tile - k * tiles, p.vocab, lane);
+    };
+    if (warp < listed) load(warp);
 #pragma unroll 1
-      for (int r = 0; r < M; ++r) {
-        float best = -INFINITY;
-        int best_j = 0, best_v = INT32_MAX;
+    for (int i = warp; i < listed; i += kPickWarps) {
+      const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
+      const uint8_t* row = row_of(k);
+      const Tile<F32, ALIGNED> x = next;
+      if (i + kPickWarps < listed) load(i + kPickWarps);
+      const Beam beam = sm.beam[k];
+      // Logits below `least` are not among the best: the logit at which the
+      // last one's total is reached, less what this sum of 32 bits may be off.
+      const float last = key_total(least_key).h;
+      const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
+      float least = (last - beam.base.h) + beam.top - slack;
+      if (least_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
+      uint32_t in = 0u;  // of this lane's logits
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int v = Tile<F32, ALIGNED>::place(t, j, lane);
-          if ((in >> j & 1u) && (x.at(j) > best || (x.at(j) == best && v < best_v))) {
-            best = x.at(j);
-            best_j = j;
-            best_v = v;
-          }
+      for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
+      if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))) > static_cast<unsigned>(M)) {
+        if (!again) {
+          if (lane == 0) sm.crowded = 1;
+          break;
         }
-        const float top = warp_max_nan(best);
-        const int top_v = static_cast<int>(__reduce_min_sync(0xffffffffu, best == top ? static_cast<unsigned>(best_v) : 0x7fffffffu));
-        if (best_v == top_v) {
-          best_ones |= 1u << best_j;
-          in &= ~(1u << best_j);
-        }
+        in = best_of_tile<F32, ALIGNED>(row, t, p.vocab, M, lane);
       }
-      in = best_ones;
-    }
 #pragma unroll 1
-    for (; in != 0u; in &= in - 1u) {
-      const int v = Tile<F32, ALIGNED>::place(t, __ffs(in) - 1, lane);
-      const uint64_t key = total_key(beam, load_logit<F32>(row, v));
-      if (key == 0) continue;
-      const int at = atomicAdd(&sm.n_pairs, 1);
-      sm.pair_key[at] = key;
-      sm.pair_at[at] = k * p.vocab + v;
+      for (; in != 0u; in &= in - 1u) {
+        const int v = Tile<F32, ALIGNED>::place(t, __ffs(in) - 1, lane);
+        const uint64_t key = total_key(beam, load_logit<F32>(row, v));
+        if (key == 0 || ahead(least_key, least_at, key, k * p.vocab + v)) continue;
+        const int at = atomicAdd(&sm.n_pairs, 1);
+        sm.pair_key[at] = key;
+        sm.pair_at[at] = k * p.vocab + v;
+      }
+    }
+    __syncthreads();
+    if (again || !sm.crowded) break;
+
+    // the best of each lane of each tile
+#pragma unroll 1
+    for (int i = warp; i < listed; i += kPickWarps) {
+      const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
+      Tile<F32, ALIGNED> x;
+      x.load(row_of(k), t, p.vocab, lane);
+      float best = x.at(0);
+#pragma unroll
+      for (int j = 1; j < 32; ++j) best = fmaxf(best, x.at(j));
+      int best_v = INT32_MAX;
+#pragma unroll
+      for (int j = 31; j >= 0; --j) {
+        const int v = Tile<F32, ALIGNED>::place(t, j, lane);
+        if (x.at(j) == best && v < best_v) best_v = v;
+      }
+      const uint64_t key = best > -INFINITY ? total_key(sm.beam[k], best) : 0;
+      sm.pair_key[i * 32 + lane] = key;
+      sm.pair_at[i * 32 + lane] = key != 0 ? k * p.vocab + best_v : INT32_MAX;
+    }
+    if (tid == 0) sm.n_pairs = 0;
+    __syncthreads();
+    uint64_t key = 0;
+    int at = INT32_MAX;
+    // a group: one lane, every other tile (the best may all be in one tile)
+#pragma unroll 1
+    for (int i = tid / kSubs % 2 + 2 * (tid % kSubs); i < listed; i += 2 * kSubs) {
+      const int e = i * 32 + tid / (2 * kSubs);
+      if (ahead(sm.pair_key[e], sm.pair_at[e], key, at)) {
+        key = sm.pair_key[e];
+        at = sm.pair_at[e];
+      }
+    }
+    last_of_groups(sm, key, at, M);
+    if (sm.last_key != 0) {
+      least_key = sm.last_key;
+      least_at = sm.last_at;
     }
   }
-  __syncthreads();
 
   // the best M in order
   const int pairs = sm.n_pairs;
