@@ -903,6 +903,7 @@ template <bool F32, bool ALIGNED>
 __global__ void __launch_bounds__(kPickThreads) beam_one_kernel(const BeamProblem p, int tiles) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   PickSmem& sm = *reinterpret_cast<PickSmem*>(smem_raw);
+  cluster_sync();  // every block has begun: the first one's shared memory may be written
   griddep_wait();
   griddep_launch_dependents();
   const int b = static_cast<int>(blockIdx.x) / kOneCtas, rank = static_cast<int>(cluster_ctarank());

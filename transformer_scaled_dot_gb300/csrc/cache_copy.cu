@@ -7,9 +7,10 @@
 // (copy, layer, pool) end to end are cut into pieces of 4 KB, a warp to a piece,
 // with eight 16-byte loads of every lane in flight before the first store. The
 // list's length is read on the device (the call that made the list has just
-// written it), so the grid is what fits and its warps walk over the pieces;
-// pieces are numbered as if every copy were of whole pages, and those past the
-// end of a shorter one are passed over.
+// written it), so the grid is what fits and its warps walk over the pieces:
+// all copies' first ones, then all second ones, so that the copies that are of
+// whole pages and those of a few rows keep all warps busy. A piece past the end
+// of a copy is passed over.
 #include "kernels.h"
 #include "sm103.cuh"
 
@@ -21,54 +22,71 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kInFlight = 8;
 constexpr int kBlocksPerSm = 3;
+constexpr int kShortList = 512;
 constexpr int kPiece = 32 * kInFlight * 16;  // bytes
 
+// Pieces of a page of rows or codes, and of their scales.
 struct Pieces {
-  int before[4];  // of a copy's pieces in a layer, those of the pools before each
-  int in_layer;
+  int rows, scales;
 };
+// Pieces of so many 16-byte vectors.
+__host__ __device__ __forceinline__ int pieces_of(int vectors) { return (vectors + kPiece / 16 - 1) / (kPiece / 16); }
 
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(const CopyProblem p, const Pieces pieces) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(const CopyProblem p, Pieces pieces) {
   griddep_wait();
   griddep_launch_dependents();
   const int lane = static_cast<int>(lane_id());
   const int page_size = 1 << p.page_shift;
-  const int64_t per_copy = static_cast<int64_t>(p.n_layers) * pieces.in_layer;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
-  int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp_id();
-  int64_t units = static_cast<int64_t>(p.max_copies) * per_copy;
-  bool counted = p.n_copies == nullptr;
-  for (; u < units; u += step) {
-    const int64_t c = units < INT32_MAX ? static_cast<int>(u) / static_cast<int>(per_copy) : u / per_copy;
-    const int64_t rest = u - c * per_copy;
-    const int from = __ldcg(p.copies + 3 * c), to = __ldcg(p.copies + 3 * c + 1), rows = __ldcg(p.copies + 3 * c + 2);
-    if (!counted) {  // the first copy is on its way
-      const int n = __ldcg(p.n_copies);
-      if (n > p.max_copies && u == 0 && lane == 0) atomicOr(&g_device_error, kErrIndex);
-      units = static_cast<int64_t>(min(max(n, 0), p.max_copies)) * per_copy;
-      counted = true;
-      if (u >= units) break;
-    }
+  // The list's length; of a short list (mostly rows' last pages) the most rows of a
+  // copy too, which most pages' later pieces lie past.
+  int n = p.max_copies, most_rows = page_size;
+  if (p.max_copies <= kShortList) {
+    int rows[kShortList / 32];
+#pragma unroll
+    for (int i = 0; i < kShortList / 32; ++i) rows[i] = i * 32 + lane < p.max_copies ? p.copies[3 * (i * 32 + lane) + 2] : 0;
+    if (p.n_copies != nullptr) n = __ldcg(p.n_copies);
+    most_rows = 0;
+#pragma unroll
+    for (int i = 0; i < kShortList / 32; ++i) most_rows = max(most_rows, i * 32 + lane < n ? rows[i] : 0);
+    most_rows = min(__reduce_max_sync(0xffffffffu, most_rows), page_size);
+  } else if (p.n_copies != nullptr) {
+    n = __ldcg(p.n_copies);
+  }
+  if (n > p.max_copies && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(&g_device_error, kErrIndex);
+  n = min(max(n, 0), p.max_copies);
+  if (most_rows < page_size) {
+    pieces.rows = pieces_of((most_rows * p.row_bytes[0] + 15) / 16 * p.h_kv);
+    if (pieces.scales > 0) pieces.scales = pieces_of((most_rows * p.row_bytes[2] + 15) / 16 * p.h_kv);
+  }
+  // units: all copies' and layers' first pieces, then their second ones, and so on;
+  // of all pools while the scales have some
+  const int quads = 4 * pieces.scales, in_layer = 2 * (pieces.rows + pieces.scales);
+  const int64_t per_piece = static_cast<int64_t>(n) * p.n_layers;
+  const int64_t units = per_piece * in_layer;
+  const bool small = units < INT32_MAX;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + warp_id(); u < units; u += step) {
+    const int q = static_cast<int>(small ? static_cast<int>(u) / static_cast<int>(per_piece) : u / per_piece);
+    const int64_t rest = u - q * per_piece;
+    const int c = static_cast<int>(small ? static_cast<int>(rest) / p.n_layers : rest / p.n_layers);
+    const int layer = static_cast<int>(rest - static_cast<int64_t>(c) * p.n_layers);
+    const int32_t* copy = p.copies + 3 * static_cast<int64_t>(c);
+    const int from = copy[0], to = copy[1], rows = copy[2];
     if (from < 0 || from >= p.n_pages || to < 0 || to >= p.n_pages || rows < 0 || rows > page_size) {
       if (lane == 0) atomicOr(&g_device_error, kErrIndex);
       continue;
     }
-    const int layer = units < INT32_MAX ? static_cast<int>(rest) / pieces.in_layer : static_cast<int>(rest / pieces.in_layer);
-    int piece = static_cast<int>(rest - static_cast<int64_t>(layer) * pieces.in_layer);
-    int pool = 0;
-#pragma unroll
-    for (int i = 1; i < 4; ++i)
-      if (i < p.n_pools && piece >= pieces.before[i]) pool = i;
+    // pools 0 and 1 hold rows or codes, 2 and 3 scales
+    const int pool = q < quads ? q & 3 : q & 1;
+    const int piece = q < quads ? q >> 2 : pieces.scales + ((q - quads) >> 1);
     uint8_t* base = static_cast<uint8_t*>(p.pool[0]);
-    int row = p.row_bytes[0], skipped = 0;
+    int row = p.row_bytes[0];
 #pragma unroll
     for (int i = 1; i < 4; ++i) {
       if (pool != i) continue;
       base = static_cast<uint8_t*>(p.pool[i]);
       row = p.row_bytes[i];
-      skipped = pieces.before[i];
     }
-    piece -= skipped;
     const int page_bytes = (p.h_kv * row) << p.page_shift;
     base += layer * p.layer_rows * row;
     const uint8_t* src = base + static_cast<int64_t>(from) * page_bytes;
@@ -145,20 +163,19 @@ cudaError_t launch_cache_copy(const CopyProblem& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     __atomic_store_n(&cached, sms, __ATOMIC_RELAXED);
   }
-  Pieces pieces = {};
-  for (int i = 0; i < p.n_pools; ++i) {
-    pieces.before[i] = pieces.in_layer;
-    pieces.in_layer += static_cast<int>(((static_cast<int64_t>(p.h_kv) * p.row_bytes[i] << p.page_shift) + kPiece - 1) / kPiece);
-  }
-  const int64_t units = static_cast<int64_t>(p.max_copies) * p.n_layers * pieces.in_layer;
+  // a page has 2^26 vectors at most, and its rows a multiple of 16 bytes between heads
+  auto whole = [&](int row_bytes) {
+    return pieces_of(static_cast<int>((static_cast<int64_t>(p.h_kv) * row_bytes << p.page_shift) / 16));
+  };
+  const Pieces pieces = {whole(p.row_bytes[0]), p.n_pools == 4 ? whole(p.row_bytes[2]) : 0};
+  const int64_t units = static_cast<int64_t>(p.max_copies) * p.n_layers * 2 * (pieces.rows + pieces.scales);
   // A long list is shared out among more blocks than are resident, so that SMs
-  // which are done sooner take more of them; a short one goes to the resident
-  // ones, as a block more costs more than a second round (in us, 8 and 3 blocks
-  // to an SM: 2500 whole pages of 64 KB in 4 layers 176 and 184, 240 of 32 KB in 6
-  // layers 17.7 and 18.4 with the plan; parts of 120 4-bit pages in 4 layers, 1152
-  // blocks' pieces, 15.6 and 14.4 with the step).
-  const int64_t blocks = (units + kWarps - 1) / kWarps, most = static_cast<int64_t>(sms) * 8, resident = sms * kBlocksPerSm;
-  const int64_t grid = blocks > most ? most : blocks > resident ? resident : blocks;
+  // which are done sooner take more of them; a short one, which may be shorter
+  // than it says and its pages than whole ones, goes to the resident ones (in us, 8
+  // and 3 blocks to an SM: 2500 whole pages of 64 KB in 4 layers 177 and 192; up to
+  // 384 parts of 64 KB pages in 2 layers 16.1 and 14.8 with the step).
+  const int64_t blocks = (units + kWarps - 1) / kWarps, most = sms * (p.max_copies > kShortList ? 8 : kBlocksPerSm);
+  const int64_t grid = blocks > most ? most : blocks;
   return launch_pdl(cache_copy_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, stream, p, pieces);
 }
 

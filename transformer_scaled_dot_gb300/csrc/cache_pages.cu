@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kReleaseThreads)
 // ---------------------------------------------------------------- one cluster
 
 constexpr int kClusterThreads = 1024;
-constexpr int kMaxCtas = 8;  // of the cluster (the portable size)
+constexpr int kMaxCtas = 16;     // of the cluster (above 8 where the device has room for it)
 constexpr int kWarps = kClusterThreads / 32;
 
 // A barrier of the cluster: of its one block where it has no more (a third of the
@@ -284,10 +284,11 @@ __device__ __forceinline__ int marked_page(int entry) { return -2 - entry; }
 template <bool ONE>
 __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const ReserveProblem p, int lanes_log2, int units) {
   __shared__ ClusterSmem sm;
+  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+  if (ctas > 1) cluster_sync();  // every block has begun: its shared memory may be written
   griddep_wait();
   griddep_launch_dependents();
   const PagesProblem& pg = p.pages;
-  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
   const int lane = static_cast<int>(lane_id());
   const int lanes = 1 << lanes_log2;
   const int group = (static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x)) >> lanes_log2;
@@ -469,10 +470,11 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     for (int j = 0; j < U; ++j) {
       const bool shared = q[j].at && marked(q[j].entry);
       keeper[j] = shared && (ONE ? kept : keeps(q[j]));
-      wants[j] = q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
+      wants[j] = most > 0 && q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
       const bool copies = wants[j] && shared && q[j].rows > 0;
       const uint32_t want_vote = __ballot_sync(kAll, wants[j]), copy_vote = __ballot_sync(kAll, copies);
-      const uint32_t at = page_to + __popc(want_vote & before_mask);
+      // (only a table that its counts do not fit could want more than was counted)
+      const uint32_t at = min(page_to + __popc(want_vote & before_mask), most - 1);
       page[j] = !wants[j] ? 0 : near ? sm.free_ids[at] : __ldcg(p.free_ids + at);
       copy[j] = copies ? p.copies + 3 * (copy_to + __popc(copy_vote & before_mask)) : nullptr;
       page_to += __popc(want_vote & group_mask);
@@ -500,10 +502,11 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
 // lie before it: the holes' from below, the movers' from above.
 __global__ void __launch_bounds__(kClusterThreads) cache_compact_kernel(const CompactProblem p) {
   __shared__ ClusterSmem sm;
+  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
+  if (ctas > 1) cluster_sync();  // every block has begun: its shared memory may be written
   griddep_wait();
   griddep_launch_dependents();
   const PagesProblem& pg = p.pages;
-  const uint32_t rank = cluster_ctarank(), ctas = gridDim.x;
   const int lane = static_cast<int>(lane_id());
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
   const int n = slice.end - slice.begin;
@@ -581,32 +584,59 @@ int sm_count() {
   return n;
 }
 
-// Blocks of the one cluster: enough for `threads` threads and for 512 pages to a
-// warp, or all. (Two blocks in place of one for 13000 pages, in us: a step with
-// shared pages 18.0 and 15.6; one in place of eight for 65536: 7.9 and 6.5, four 7.1.)
-unsigned cluster_blocks(int64_t n_pages, int64_t threads) {
+// Blocks of the one cluster: one up to 16384 pages, else 256 pages to a warp; and
+// enough for `threads` threads; or as many as there can be. (In us: a step with shared
+// pages and 13000 pages in one block 15.6, in two 18.0; a step with 65536 in eight 6.5,
+// in four 7.1, in one 7.9; 64 prompts with 262144 in 16 12.5, in eight 17.6.)
+unsigned cluster_blocks(int64_t n_pages, int64_t threads, unsigned most) {
   unsigned ctas = 1;
-  while (ctas < kMaxCtas && (n_pages > static_cast<int64_t>(ctas) * 512 * kWarps ||
-                             threads > static_cast<int64_t>(ctas) * kClusterThreads))
+  while (ctas < most && ((n_pages > 16384 && n_pages > static_cast<int64_t>(ctas) * 256 * kWarps) ||
+                         threads > static_cast<int64_t>(ctas) * kClusterThreads))
     ctas *= 2;
   return ctas;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned ctas, cudaStream_t stream, Args&&... args) {
+cudaLaunchConfig_t cluster_config(unsigned ctas, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kClusterThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
+  return cfg;
+}
+
+// The largest cluster of `kernel` that the device takes: 16 blocks, or the
+// portable 8. Asked once for each kernel (`known` is its own).
+template <typename Kernel>
+cudaError_t most_blocks(Kernel kernel, unsigned* known, unsigned* most) {
+  *most = __atomic_load_n(known, __ATOMIC_ACQUIRE);
+  if (*most != 0) return cudaSuccess;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = cluster_config(kMaxCtas, nullptr, attr);
+  cfg.numAttrs = 1;
+  int fit = 0;
+  if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    fit = 0;
+  }
+  *most = fit > 0 ? kMaxCtas : 8;
+  __atomic_store_n(known, *most, __ATOMIC_RELEASE);
+  return cudaSuccess;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned ctas, cudaStream_t stream, Args&&... args) {
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = cluster_config(ctas, stream, attr);
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
@@ -644,14 +674,22 @@ cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
   while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
   const int units = static_cast<int>((pages + (1 << lanes_log2) - 1) >> lanes_log2);
   const int64_t threads = (static_cast<int64_t>(p.pages.B) * units) << lanes_log2;
-  const unsigned ctas = cluster_blocks(p.pages.n_pages, threads);
+  static unsigned known_one = 0, known_many = 0;
+  unsigned most_one = 0, most_many = 0;
+  cudaError_t e = most_blocks(cache_reserve_kernel<true>, &known_one, &most_one);
+  if (e == cudaSuccess) e = most_blocks(cache_reserve_kernel<false>, &known_many, &most_many);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = cluster_blocks(p.pages.n_pages, threads, most_one < most_many ? most_one : most_many);
   return threads <= static_cast<int64_t>(ctas) * kClusterThreads
              ? launch_cluster(cache_reserve_kernel<true>, ctas, stream, p, lanes_log2, units)
              : launch_cluster(cache_reserve_kernel<false>, ctas, stream, p, lanes_log2, units);
 }
 
 cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream) {
-  cudaError_t e = launch_cluster(cache_compact_kernel, cluster_blocks(p.pages.n_pages, 0), stream, p);
+  static unsigned known = 0;
+  unsigned most_ctas = 0;
+  cudaError_t e = most_blocks(cache_compact_kernel, &known, &most_ctas);
+  if (e == cudaSuccess) e = launch_cluster(cache_compact_kernel, cluster_blocks(p.pages.n_pages, 0, most_ctas), stream, p);
   if (e != cudaSuccess) return e;
   const int64_t entries = static_cast<int64_t>(p.pages.B) * p.pages.max_pages;
   if (entries == 0) return cudaSuccess;
