@@ -290,6 +290,70 @@ def test_ended_hypotheses(tsd, alpha):
     assert got[3].tolist() == [[-1, -1, -2]] and got[4].tolist() == [[72, 1, 70]] and got[5].tolist() == [[82, 1, 80]]
 
 
+@pytest.mark.parametrize("seed", range(40))
+def test_random_shapes(tsd, seed):
+    """Sizes, alignments, ranges of logits, dead beams and forbidden tokens at random."""
+    rng = np.random.default_rng(500 + seed)
+    B, K = int(rng.integers(1, 24)), int(rng.integers(1, 17))
+    V = int(np.exp(rng.uniform(0, np.log(9000))))
+    f32, end = bool(rng.integers(0, 2)), int(rng.integers(-1, V))
+    s = Step(tsd, B, K, V, f32, end, alpha=float(rng.uniform(-1, 2)), pad=int(rng.choice([0, 0, 1, 5, 8])),
+             offset=int(rng.choice([0, 0, 1, 3, 8])))
+    x = float(rng.choice([0.1, 1, 3, 30, 400])) * logits(rng, B, K, V)
+    x[rng.random(x.shape) < rng.choice([0, 0, 0.3, 0.95])] = -np.inf
+    if end >= 0:
+        x[..., end] = np.where(rng.random((B, K)) < 0.4, x.max(-1), x[..., end])
+    x = s.fill(x)
+    s.scores.copy_(dev_f32(np.where(rng.random((B, K)) < 0.2, -np.inf, -rng.choice([0.5, 20]) * rng.random((B, K)))))
+    s.lengths.copy_(to_dev_i32(rng.integers(0, 400, B)))
+    s.ended[0].copy_(dev_f32(np.where(rng.random((B, K)) < 0.5, -np.inf, -4 * rng.random((B, K)))))
+    check(s, x, seed)
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+
+
+@pytest.mark.parametrize("f32", [False, True])
+def test_few_and_many_sentences_choose_alike(tsd, f32):
+    """A sentence's choice is the same to the bit in a call of its own (one launch), in one of eight, and in one of nine (two)."""
+    rng = np.random.default_rng(8)
+    K, V = 4, 32768
+    x, scores = logits(rng, 9, K, V), -5 * rng.random((9, K))
+    got = []
+    for B, at in ((9, 0), (8, 1), (1, 5)):
+        s = Step(tsd, B, K, V, f32, 2)
+        s.fill(x[at:at + B])
+        s.scores.copy_(dev_f32(scores[at:at + B]))
+        s.run()
+        out = s.get()
+        out[1] = out[1] % K
+        out[4] = np.where(out[3] > -np.inf, out[4] % K, -1)
+        got.append([a[5 - at] for a in out])
+    for other in got[1:]:
+        for a, b in zip(got[0], other):
+            assert np.array_equal(a, b)
+
+
+def test_two_streams_at_once(tsd):
+    """Calls on two streams with workspaces of their own, in turn without waiting, choose as alone."""
+    import torch
+    rng = np.random.default_rng(12)
+    steps, want = [], []
+    for B, V in ((20, 32003), (3, 9000)):
+        s = Step(tsd, B, 4, V, False, -1)
+        s.fill(logits(rng, B, 4, V))
+        s.scores.copy_(dev_f32(-5 * rng.random((B, 4))))
+        s.run()
+        want.append(s.get()[:3])
+        steps.append((s, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream in steps:
+            s.run(stream)
+    torch.cuda.synchronize()
+    for (s, _), w in zip(steps, want):
+        for a, b in zip(s.get()[:3], w):
+            assert np.array_equal(a, b)
+
+
 def test_in_place_and_repeated(tsd):
     """new_scores may be the scores; the same call gives the same bits, on another stream too, and in a graph."""
     import torch

@@ -447,3 +447,138 @@ def test_another_stream_and_a_graph(tsd):
         check_state(plain, t, c)
         for p, w in zip(x, content):
             assert np.array_equal(ints(p), w)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_calls_one_after_the_other(tsd, seed):
+    """Forks, reserves, releases and compactions at random on one state, with their copies: tables and
+    counts as the plain form's after every call, and every row's contents as when they were written."""
+    import torch
+    rng = np.random.default_rng(70 + seed)
+    B, max_pages, page = int(rng.integers(1, 40)), int(rng.integers(1, 12)), int(rng.choice([16, 32, 64]))
+    n_pages, h_kv, d, q4 = int(rng.integers(1, B * max_pages + 5)), int(rng.integers(1, 4)), 64, bool(seed % 2)
+    plain = pu.Pages(np.full((B, max_pages), -1), np.zeros(n_pages), page)
+    t, c = to_dev_i32(plain.table), to_dev_i32(plain.counts)
+    x = pools(rng, q4, 2, n_pages, h_kv, page, d)
+    held = np.zeros(B, int)      # rows of each sequence
+    words = [[] for _ in range(B)]  # what was written into each row, as numbers
+    serial = 1
+
+    def row_of(b, p):
+        return plain.table[b][p // page] * h_kv * page + p % page
+
+    def moved(copies, n):
+        listed = to_dev_i32(np.array([list(e) for e in copies] + [[0, 0, 1]]))
+        run_copy(tsd, q4, x, listed, to_dev_i32([len(copies)]), len(copies) + 1, 2, n_pages * h_kv * page, h_kv, d, n_pages, page)
+
+    for _ in range(30):
+        what = rng.choice(["fork", "reserve", "reserve", "release", "compact"])
+        if what == "fork":
+            parents = rng.integers(-1, B, B) if rng.random() < 0.5 else np.arange(B) // 2 * 2
+            plain.fork(parents)
+            tsd.attn_cache_fork(t, None, c, to_dev_i32(parents), B, n_pages, max_pages)
+            held = np.where(parents >= 0, held[parents], 0)
+            words = [list(words[q]) if q >= 0 else [] for q in parents]
+        elif what == "release":
+            keep = np.where(rng.random(B) < 0.4, rng.integers(0, max_pages * page + 1, B), -1)
+            keep = np.minimum(keep, held)
+            plain.release(keep)
+            tsd.attn_cache_release(t, c, to_dev_i32(keep), B, n_pages, page, max_pages)
+            held = np.where(keep >= 0, keep, held)
+            words = [w[:n] for w, n in zip(words, held)]
+        elif what == "compact":
+            most = int(rng.choice([1, 3, n_pages]))
+            copies, used = plain.compact(most)
+            out, n_copies, n_used = to_dev_i32(np.full((most, 3), GUARD)), ones(), ones()
+            ws, n = workspace(tsd, B, n_pages)
+            tsd.attn_cache_compact(t, c, t, c, out, n_copies, n_used, B, n_pages, page, max_pages, most, ws, n)
+            assert (int(n_copies), int(n_used)) == (len(copies), used)
+            assert ints(out)[:len(copies)].tolist() == [list(e) for e in copies]
+            moved(copies, most)
+        else:
+            most = int(rng.choice([1, 1, 2, 30]))
+            new = np.minimum(rng.integers(0, most + 1, B), max_pages * page - held)
+            copies, missing = plain.reserve((held + new).tolist(), new.tolist())
+            got, n, n_missing = reserve(tsd, t, c, to_dev_i32(held + new), to_dev_i32(new), most, page)
+            assert (n, n_missing) == (len(copies), missing) and got[:n].tolist() == [list(e) for e in copies]
+            if not missing:
+                moved(copies, B)
+                for b in range(B):  # the new tokens' rows, of every head and layer
+                    for p in range(held[b], held[b] + new[b]):
+                        words[b].append(serial % 251)
+                        for pool in x:
+                            pool[:, row_of(b, p):row_of(b, p) + (h_kv - 1) * page + 1:page] = serial % 251
+                        serial += 1
+                held = held + new
+        check_state(plain, t, c)
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+    for pool in x:
+        rows = ints(pool)
+        for b in range(B):
+            for p, word in enumerate(words[b]):
+                at = row_of(b, p)
+                assert (rows[:, at:at + (h_kv - 1) * page + 1:page] == word).all(), (b, p)
+
+
+def test_counts_that_do_not_fit_the_table(tsd):
+    """A page twice in a row, counts too low and too high, negative ones: no access out of range, every
+    entry a page or none, and what lies around the arrays as it was."""
+    rng = np.random.default_rng(3)
+    for seed in range(20):
+        B, max_pages, n_pages = 40, 6, 60
+        big_t, big_c = to_dev_i32(np.full(B * max_pages + 200, GUARD)), to_dev_i32(np.full(n_pages + 200, GUARD))
+        t, c = big_t[100:-100].view(B, max_pages), big_c[100:-100]
+        t.copy_(to_dev_i32(rng.integers(-1, n_pages, (B, max_pages)) if seed % 2 else rng.integers(-1, 8, (B, max_pages))))
+        c.copy_(to_dev_i32(rng.integers(-2, 5, n_pages)))
+        lens = rng.integers(0, max_pages * 16 + 1, B)
+        new = [1, 40][seed % 4 // 2]
+        reserve(tsd, t, c, to_dev_i32(lens), None, new, 16)
+        assert ((ints(t) >= -1) & (ints(t) < n_pages)).all()
+        tsd.attn_cache_fork(t, None, c, to_dev_i32(rng.integers(-1, B, B)), B, n_pages, max_pages)
+        tsd.attn_cache_release(t, c, to_dev_i32(lens // 2), B, n_pages, 16, max_pages)
+        assert ((ints(t) >= -1) & (ints(t) < n_pages)).all()
+        for big in (big_t, big_c):
+            assert (ints(big)[:100] == GUARD).all() and (ints(big)[-100:] == GUARD).all()
+    assert tsd.attn_get_device_status() == tsd.ATTN_OK
+
+
+FIRST_CALLS = """
+import numpy as np, torch
+import transformer_scaled_dot_gb300 as tsd
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+n_pages, wsb = {n_pages}, tsd.attn_cache_pages_workspace_bytes(2, {n_pages})
+table, counts, lens, parents = i32([[0, -1], [0, -1]]), torch.zeros(n_pages, dtype=torch.int32, device="cuda"), i32([17, 17]), i32([0, 0])
+counts[0] = 2
+copies, n, missing, ws = i32([[0, 0, 0]] * 4), i32([0]), i32([0]), torch.zeros(wsb, dtype=torch.uint8, device="cuda")
+k, v = torch.randn(n_pages if n_pages < 99 else 99, 1, 16, 64, device="cuda").bfloat16(), torch.randn(99, 1, 16, 64, device="cuda").bfloat16()
+x = torch.randn({B} * 2, 1000, device="cuda").bfloat16()
+scores, tokens, rows = torch.zeros({B}, 2, device="cuda"), i32([[9, 9]] * {B}), i32([[9, 9]] * {B})
+bsb = tsd.beam_select_workspace_bytes({B}, 2, 1000)
+bws = torch.zeros(bsb, dtype=torch.uint8, device="cuda")
+torch.cuda.synchronize()
+with torch.cuda.graph(graph, stream=stream):
+    tsd.attn_cache_fork(table, None, counts, parents, 2, n_pages, 2, stream=stream)
+    tsd.attn_cache_reserve(table, counts, lens, None, copies, n, missing, 2, 1, n_pages, 16, 2, ws, wsb, stream=stream)
+    tsd.attn_cache_copy(k, v, copies, n, 2, 1, 0, 1, 64, 99 if n_pages > 99 else n_pages, 16, stream=stream)
+    tsd.attn_cache_release(table, counts, lens, 2, n_pages, 16, 2, stream=stream)
+    tsd.attn_cache_compact(table, counts, table, counts, copies, n, missing, 2, n_pages, 16, 2, 4, ws, wsb, stream=stream)
+    tsd.beam_select(x, 1000, scores, None, {B}, 2, 1000, -1, 0.0, tokens, rows, scores, None, None, None, bws, bsb, stream=stream)
+assert (tokens == 9).all() and table.tolist() == [[0, -1], [0, -1]]
+graph.replay()
+torch.cuda.synchronize()
+assert table.tolist() == [[0, 1], [0, 2]] and counts[:4].tolist() == [2, 1, 1, 0], (table, counts[:4])
+assert (tokens >= 0).all() and (tokens != 9).any() and torch.isfinite(scores).all()
+assert tsd.attn_get_device_status() == tsd.ATTN_OK
+print("captured first")
+"""
+
+
+@pytest.mark.parametrize("n_pages,B", [(99, 1), (300000, 20)])
+def test_first_calls_inside_a_capture(tsd, n_pages, B):
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(n_pages=n_pages, B=B)], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
