@@ -372,7 +372,7 @@ __device__ __forceinline__ Pair log_pair(Pair x) {
   const int e = (bits - 0x3f3504f3) >> 23;  // sqrt(1/2) is 0x3f3504f3
   const float m = __int_as_float(bits - (e << 23));
   const float f = m - 1.f, d = 1.f + m, d_rest = m - (d - 1.f);
-  const float inverse = __frcp_rn(d);
+  const float inverse = __fdividef(1.f, d);  // what z is off by is in z_rest
   const float z = f * inverse;
   const float z_rest = (__fmaf_rn(-z, d, f) - z * d_rest) * inverse;
   const float z2 = z * z;
@@ -455,6 +455,7 @@ __device__ __forceinline__ uint64_t total_key(const Beam& beam, float x) {
 constexpr int kGroups = 64;     // of a sentence's tiles, or of the lanes of some
 constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
 static_assert(kGroups == 2 * 32, "a group's lane");
+constexpr int kListMost = 2048, kListStep = 3 * kPickThreads;
 constexpr int kTileList = 64;   // chosen tiles that are looked through
 constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
 
@@ -466,8 +467,8 @@ struct PickSmem {
   int last_at;
   int n_tiles, n_pairs;
   int crowded;                 // a tile has more than M pairs ahead of the last
-  int tile[2 * kPickThreads];  // chosen tiles
-  uint64_t tile_key[2 * kPickThreads];
+  int tile[kListMost];         // chosen tiles
+  uint64_t tile_key[kListMost];
   uint64_t pair_key[kPairList];
   int pair_at[kPairList];
   uint64_t best_key[2 * kBeamMaxBeams];
@@ -616,8 +617,16 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
   const int n = K * tiles;  // below 2^14
 
   if (records != nullptr) {
-#pragma unroll 4
-    for (int i = tid; i < n; i += kPickThreads) sm.key[i] = __ldcg(reinterpret_cast<const unsigned long long*>(records) + i);
+#pragma unroll 1
+    for (int i0 = tid; i0 < n; i0 += 4 * kPickThreads) {
+      unsigned long long r[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * kPickThreads < n) r[j] = __ldcg(reinterpret_cast<const unsigned long long*>(records) + i0 + j * kPickThreads);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i0 + j * kPickThreads < n) sm.key[i0 + j * kPickThreads] = r[j];
+    }
   }
   // what the last step needs
   float score = -INFINITY, ended = -INFINITY;
@@ -699,8 +708,9 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
   // those tiles. More than the list holds (the best ones in few groups): the
   // best M of it are kept and it is filled again.
 #pragma unroll 1
-  for (int i = tid, left = n; left > 0; left -= kPickThreads, i += kPickThreads) {
-    if (i < n) {
+  for (int i0 = 0; i0 < n; i0 += kListStep) {
+#pragma unroll 1
+    for (int i = i0 + tid; i < min(n, i0 + kListStep); i += kPickThreads) {
       const uint64_t key = sm.key[i];
       if (key != 0 && !ahead(last_key, last_tile, key, i)) {
         const int at = atomicAdd(&sm.n_tiles, 1);
@@ -709,8 +719,8 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
       }
     }
     __syncthreads();
-    const bool more = left > kPickThreads;
-    if (sm.n_tiles > (more ? kPickThreads : kTileList)) keep_best_tiles(sm, M);
+    const bool more = i0 + kListStep < n;
+    if (sm.n_tiles > (more ? kListMost - kListStep : kTileList)) keep_best_tiles(sm, M);
     if (more) __syncthreads();  // all have seen the count before it grows
   }
 
