@@ -7,8 +7,8 @@
 // how many table entries name each page (0: a free page). There is no list of
 // free pages that one call would leave to the next: the lowest free pages are
 // found in the counts, so that the pages a call takes follow from its
-// arguments alone, and the pool stays dense by itself. The counts of 2^18
-// pages are 1 MB, two microseconds' reading for one cluster.
+// arguments alone, and the pool stays dense by itself. Its price is to read
+// them: 1 MB where there are 2^18 pages.
 //
 // All of it is integer work on a few hundred kilobytes and bound by latency:
 // dependent reads of the L2 and barriers between phases. What needs an order
@@ -157,7 +157,8 @@ __device__ __forceinline__ Sums cluster_scan(uint32_t v, uint32_t w, uint64_t mo
   if (lane == 31) sm.warp[warp] = {sum_v, sum_w + more};
   __syncthreads();
   if (warp == 0) {
-    const Sums mine = sm.warp[lane];
+    Sums mine = {0, 0};
+    if (lane < static_cast<int>(blockDim.x >> 5)) mine = sm.warp[lane];
     Sums sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -208,9 +209,9 @@ struct Slice {
   int begin, end;
 };
 __device__ __forceinline__ Slice warp_slice(int n_pages, uint32_t rank, uint32_t ctas) {
-  const int warps = static_cast<int>(ctas) * kWarps;
+  const int block_warps = static_cast<int>(blockDim.x) / 32, warps = static_cast<int>(ctas) * block_warps;
   const int64_t len = ((static_cast<int64_t>(n_pages) + warps - 1) / warps + 32 * kBatch - 1) / (32 * kBatch) * (32 * kBatch);
-  const int64_t begin = len * (static_cast<int64_t>(rank) * kWarps + warp_id());
+  const int64_t begin = len * (static_cast<int64_t>(rank) * block_warps + warp_id());
   return {static_cast<int>(begin < n_pages ? begin : n_pages),
           static_cast<int>(begin + len < n_pages ? begin + len : n_pages)};
 }
@@ -291,9 +292,9 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   const PagesProblem& pg = p.pages;
   const int lane = static_cast<int>(lane_id());
   const int lanes = 1 << lanes_log2;
-  const int group = (static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x)) >> lanes_log2;
+  const int group = static_cast<int>(rank * blockDim.x + threadIdx.x) >> lanes_log2;
   const int64_t all_units = static_cast<int64_t>(pg.B) * units;
-  const int groups = static_cast<int>(ctas) * (kClusterThreads >> lanes_log2);
+  const int groups = static_cast<int>(ctas * blockDim.x) >> lanes_log2;
   const int64_t per = ONE ? 1 : (all_units + groups - 1) / groups;
   const int sub = lane & (lanes - 1);
   const uint32_t group_mask = (lanes == 32 ? kAll : ((1u << lanes) - 1u) << (lane & ~(lanes - 1)));
@@ -537,8 +538,7 @@ __global__ void __launch_bounds__(kClusterThreads) cache_compact_kernel(const Co
   movers = static_cast<int>(__reduce_add_sync(kAll, static_cast<unsigned>(movers)));
   cluster_scan<0>(0u, 0u, static_cast<uint64_t>(movers), sm, 1, rank, ctas, &all);
   const int moved = static_cast<int>(all.w) < p.max_copies ? static_cast<int>(all.w) : p.max_copies;
-  for (int k = static_cast<int>(rank) * kClusterThreads + static_cast<int>(threadIdx.x); k < moved;
-       k += static_cast<int>(ctas) * kClusterThreads) {
+  for (int k = static_cast<int>(rank * blockDim.x + threadIdx.x); k < moved; k += static_cast<int>(ctas * blockDim.x)) {
     const int from = __ldcg(p.moves + 2 * k), to = __ldcg(p.moves + 2 * k + 1);
     p.copies[3 * k] = from;
     p.copies[3 * k + 1] = to;
@@ -584,25 +584,33 @@ int sm_count() {
   return n;
 }
 
-// Blocks of the one cluster: one up to 16384 pages, else 256 pages to a warp; and
-// enough for `threads` threads; or as many as there can be. (In us: a step with shared
-// pages and 13000 pages in one block 15.6, in two 18.0; a step with 65536 in eight 6.5,
-// in four 7.1, in one 7.9; 64 prompts with 262144 in 16 12.5, in eight 17.6.)
-unsigned cluster_blocks(int64_t n_pages, int64_t threads, unsigned most) {
+// The cluster for so many pages and threads. Blocks: one up to 16384 pages, else
+// 256 pages to a warp; and enough for `threads`; or as many as there can be. (In us: a
+// step with shared pages and 13000 pages in one block 15.6, in two 18.0; a step with
+// 65536 in eight 6.5, in four 7.1, in one 7.9; 64 prompts with 262144 in 16 12.5, in
+// eight 17.6.) One block has no more threads than that takes, as it waits for its
+// barriers: a step of 16 rows with 1000 pages takes 10.0 with its fork and copies,
+// with 1024 threads 11.2.
+struct Shape {
+  unsigned ctas, threads;
+};
+Shape cluster_shape(int64_t n_pages, int64_t threads, unsigned most) {
   unsigned ctas = 1;
   while (ctas < most && ((n_pages > 16384 && n_pages > static_cast<int64_t>(ctas) * 256 * kWarps) ||
                          threads > static_cast<int64_t>(ctas) * kClusterThreads))
     ctas *= 2;
-  return ctas;
+  if (ctas > 1) return {ctas, kClusterThreads};
+  const int64_t wanted = (threads > n_pages / 8 ? threads : n_pages / 8) + 31;
+  return {1, wanted >= kClusterThreads ? kClusterThreads : wanted < 128 ? 128u : static_cast<unsigned>(wanted) & ~31u};
 }
 
-cudaLaunchConfig_t cluster_config(unsigned ctas, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+cudaLaunchConfig_t cluster_config(const Shape& shape, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kClusterThreads);
+  cfg.gridDim = dim3(shape.ctas);
+  cfg.blockDim = dim3(shape.threads);
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.x = shape.ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -621,7 +629,7 @@ cudaError_t most_blocks(Kernel kernel, unsigned* known, unsigned* most) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = cluster_config(kMaxCtas, nullptr, attr);
+  cudaLaunchConfig_t cfg = cluster_config({kMaxCtas, kClusterThreads}, nullptr, attr);
   cfg.numAttrs = 1;
   int fit = 0;
   if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess) {
@@ -634,9 +642,9 @@ cudaError_t most_blocks(Kernel kernel, unsigned* known, unsigned* most) {
 }
 
 template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), unsigned ctas, cudaStream_t stream, Args&&... args) {
+cudaError_t launch_cluster(void (*kernel)(KArgs...), const Shape& shape, cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = cluster_config(ctas, stream, attr);
+  const cudaLaunchConfig_t cfg = cluster_config(shape, stream, attr);
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
@@ -679,17 +687,19 @@ cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
   cudaError_t e = most_blocks(cache_reserve_kernel<true>, &known_one, &most_one);
   if (e == cudaSuccess) e = most_blocks(cache_reserve_kernel<false>, &known_many, &most_many);
   if (e != cudaSuccess) return e;
-  const unsigned ctas = cluster_blocks(p.pages.n_pages, threads, most_one < most_many ? most_one : most_many);
-  return threads <= static_cast<int64_t>(ctas) * kClusterThreads
-             ? launch_cluster(cache_reserve_kernel<true>, ctas, stream, p, lanes_log2, units)
-             : launch_cluster(cache_reserve_kernel<false>, ctas, stream, p, lanes_log2, units);
+  const Shape shape = cluster_shape(p.pages.n_pages, threads, most_one < most_many ? most_one : most_many);
+  return threads <= static_cast<int64_t>(shape.ctas) * shape.threads
+             ? launch_cluster(cache_reserve_kernel<true>, shape, stream, p, lanes_log2, units)
+             : launch_cluster(cache_reserve_kernel<false>, shape, stream, p, lanes_log2, units);
 }
 
 cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream) {
   static unsigned known = 0;
   unsigned most_ctas = 0;
   cudaError_t e = most_blocks(cache_compact_kernel, &known, &most_ctas);
-  if (e == cudaSuccess) e = launch_cluster(cache_compact_kernel, cluster_blocks(p.pages.n_pages, 0, most_ctas), stream, p);
+  if (e != cudaSuccess) return e;
+  // (a pool of 700 pages: 18.0 to 18.6 us for the whole call with 128, 352 or 1024 threads)
+  e = launch_cluster(cache_compact_kernel, cluster_shape(p.pages.n_pages, kClusterThreads, most_ctas), stream, p);
   if (e != cudaSuccess) return e;
   const int64_t entries = static_cast<int64_t>(p.pages.B) * p.pages.max_pages;
   if (entries == 0) return cudaSuccess;
