@@ -620,13 +620,18 @@ cudaLaunchConfig_t cluster_config(const Shape& shape, cudaStream_t stream, cudaL
   return cfg;
 }
 
-// The largest cluster of `kernel` that the device takes: 16 blocks, or the
-// portable 8. Asked once for each kernel (`known` is its own).
+// The largest cluster of a kernel that the current device takes: 16 blocks, or the
+// portable 8. Asked once for each kernel and device (`known` is the kernel's own).
+constexpr int kDevices = 64;
 template <typename Kernel>
-cudaError_t most_blocks(Kernel kernel, unsigned* known, unsigned* most) {
-  *most = __atomic_load_n(known, __ATOMIC_ACQUIRE);
+cudaError_t most_blocks(Kernel kernel, unsigned (&known)[kDevices], unsigned* most) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  unsigned* mine = dev >= 0 && dev < kDevices ? &known[dev] : nullptr;
+  *most = mine ? __atomic_load_n(mine, __ATOMIC_ACQUIRE) : 0;
   if (*most != 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = cluster_config({kMaxCtas, kClusterThreads}, nullptr, attr);
@@ -637,7 +642,7 @@ cudaError_t most_blocks(Kernel kernel, unsigned* known, unsigned* most) {
     fit = 0;
   }
   *most = fit > 0 ? kMaxCtas : 8;
-  __atomic_store_n(known, *most, __ATOMIC_RELEASE);
+  if (mine) __atomic_store_n(mine, *most, __ATOMIC_RELEASE);
   return cudaSuccess;
 }
 
@@ -682,10 +687,10 @@ cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
   while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
   const int units = static_cast<int>((pages + (1 << lanes_log2) - 1) >> lanes_log2);
   const int64_t threads = (static_cast<int64_t>(p.pages.B) * units) << lanes_log2;
-  static unsigned known_one = 0, known_many = 0;
+  static unsigned known_one[kDevices], known_many[kDevices];
   unsigned most_one = 0, most_many = 0;
-  cudaError_t e = most_blocks(cache_reserve_kernel<true>, &known_one, &most_one);
-  if (e == cudaSuccess) e = most_blocks(cache_reserve_kernel<false>, &known_many, &most_many);
+  cudaError_t e = most_blocks(cache_reserve_kernel<true>, known_one, &most_one);
+  if (e == cudaSuccess) e = most_blocks(cache_reserve_kernel<false>, known_many, &most_many);
   if (e != cudaSuccess) return e;
   const Shape shape = cluster_shape(p.pages.n_pages, threads, most_one < most_many ? most_one : most_many);
   return threads <= static_cast<int64_t>(shape.ctas) * shape.threads
@@ -694,9 +699,9 @@ cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_compact(const CompactProblem& p, cudaStream_t stream) {
-  static unsigned known = 0;
+  static unsigned known[kDevices];
   unsigned most_ctas = 0;
-  cudaError_t e = most_blocks(cache_compact_kernel, &known, &most_ctas);
+  cudaError_t e = most_blocks(cache_compact_kernel, known, &most_ctas);
   if (e != cudaSuccess) return e;
   // (a pool of 700 pages: 18.0 to 18.6 us for the whole call with 128, 352 or 1024 threads)
   e = launch_cluster(cache_compact_kernel, cluster_shape(p.pages.n_pages, kClusterThreads, most_ctas), stream, p);
