@@ -358,6 +358,19 @@ def test_copy_lists(tsd, q4):
             assert np.array_equal(ints(p), w)
 
 
+@pytest.mark.parametrize("copy", [(0, 1, -1), (0, 1, -2 ** 31), (-1, 1, 0), (0, 8, 0), (0, 8, 16)])
+@pytest.mark.parametrize("n", [1, 600])
+def test_copy_lists_of_nothing_to_copy(tsd, copy, n):
+    """A number out of range is reported where no copy of the list has a row, too."""
+    rng = np.random.default_rng(1)
+    x = pools(rng, False, 1, 8, 3, 16, 64)
+    want = [ints(p) for p in x]
+    run_copy(tsd, False, x, to_dev_i32(np.array([(2, 3, 0)] * (n - 1) + [copy])), None, n, 1, 0, 3, 64, 8, 16)
+    assert tsd.attn_get_device_status() == tsd.ATTN_ERR_DEVICE_INDEX
+    for p, w in zip(x, want):
+        assert np.array_equal(ints(p), w)
+
+
 def test_copy_past_32_bit_offsets(tsd):
     """Pages on either side of 2^31 elements and 2^32 bytes of a pool, and a layer beyond them."""
     import torch

@@ -39,17 +39,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(cons
   const int page_size = 1 << p.page_shift;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps;
   // The list's length; of a short list (mostly rows' last pages) the most rows of a
-  // copy too, which most pages' later pieces lie past.
+  // copy too, which most pages' later pieces lie past. One at least, and a whole page
+  // where a number is negative: a unit of each copy checks its numbers.
   int n = p.max_copies, most_rows = page_size;
   if (p.max_copies <= kShortList) {
     int rows[kShortList / 32];
 #pragma unroll
     for (int i = 0; i < kShortList / 32; ++i) rows[i] = i * 32 + lane < p.max_copies ? p.copies[3 * (i * 32 + lane) + 2] : 0;
     if (p.n_copies != nullptr) n = __ldcg(p.n_copies);
-    most_rows = 0;
+    unsigned most = 1u;
 #pragma unroll
-    for (int i = 0; i < kShortList / 32; ++i) most_rows = max(most_rows, i * 32 + lane < n ? rows[i] : 0);
-    most_rows = min(__reduce_max_sync(0xffffffffu, most_rows), page_size);
+    for (int i = 0; i < kShortList / 32; ++i) most = max(most, i * 32 + lane < n ? static_cast<unsigned>(rows[i]) : 0u);
+    most_rows = static_cast<int>(min(__reduce_max_sync(0xffffffffu, most), static_cast<unsigned>(page_size)));
   } else if (p.n_copies != nullptr) {
     n = __ldcg(p.n_copies);
   }
@@ -96,9 +97,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(cons
     const bool whole = rows == page_size;  // one run
     const int run_bytes = whole ? page_bytes : rows * row;
     const int per = (run_bytes + 15) / 16, rest_bytes = run_bytes & 15;
-    const int n = whole ? per : p.h_kv * per;
+    const int vectors = whole ? per : p.h_kv * per;
     const int begin = piece * (kPiece / 16);
-    if (begin >= n) continue;
+    if (begin >= vectors) continue;
     int at[kInFlight];  // where this lane's lie in the page; -1: none
     uint32_t cut = 0u;  // bit i: the i-th is a run's last and short
     const float inverse = 1.f / static_cast<float>(per);
@@ -108,11 +109,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) cache_copy_kernel(cons
       at[i] = e * 16;
       if (!whole) {
         // the product is 1 / (2 per) off a whole number at least, and below 2^20 off by a quarter of that
-        const int run = n < 1 << 20 ? static_cast<int>((static_cast<float>(e) + 0.5f) * inverse) : e / per;
+        const int run = vectors < 1 << 20 ? static_cast<int>((static_cast<float>(e) + 0.5f) * inverse) : e / per;
         at[i] = run * (row << p.page_shift) + (e - run * per) * 16;
         if (rest_bytes != 0 && e - run * per == per - 1) cut |= 1u << i;
       }
-      if (e >= n) at[i] = -1;
+      if (e >= vectors) at[i] = -1;
     }
     uint4 v[kInFlight];
     if (rest_bytes == 0) {
