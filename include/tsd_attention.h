@@ -690,7 +690,8 @@ attn_status attn_cache_release(int32_t *page_table, int32_t *ref_counts, const i
  *               attn_cache_copy carries them out: no page is both from and to
  *   n_copies    int32[1], written
  *   n_missing   int32[1], written: 0, or how many pages are wanting. Then
- *               nothing is changed and nothing listed
+ *               nothing is changed and nothing listed (but that an entry which
+ *               names no page may be -1 afterwards)
  *   workspace   device, 16-byte aligned, >= attn_cache_pages_workspace_bytes(B,
  *               n_pages) bytes of scratch (0 for sizes that the calls refuse)
  * Positions past max_pages * page_size get no page. One launch.
@@ -753,9 +754,9 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  * beam_select -- one step of beam search ("[논문 리뷰]Attention Is All You
  * Need" (kimjiil.github.io) and "Attention Is All You Need 해부" (sj-techlog)
  * decode with beams of 4 and a length penalty alpha = 0.6; how a step handles
- * ended hypotheses is this library's choice). Row b * beams + k of the logits is what beam k of sentence b says of
- * its next token. With s the beams' scores (their tokens' summed log
- * probabilities),
+ * ended hypotheses is this library's choice). Row b * beams + k of the logits is
+ * what beam k of sentence b says of its next token. With s the beams' scores
+ * (their tokens' summed log probabilities),
  *   total(k, v) = s_k + x_kv - log sum_u exp x_ku,
  * the 2 * beams best pairs of a sentence (`beams` without an end token; fewer
  * where fewer are above -infinity), by total and then by lowest k * vocab + v,

@@ -290,6 +290,21 @@ def test_ended_hypotheses(tsd, alpha):
     assert got[3].tolist() == [[-1, -1, -2]] and got[4].tolist() == [[72, 1, 70]] and got[5].tolist() == [[82, 1, 80]]
 
 
+@pytest.mark.parametrize("alpha", [1e6, -1e12, 3e38])
+def test_one_token_has_no_penalty(tsd, alpha):
+    """(6 / 6)^alpha is 1 whatever alpha is; with more tokens the score is 0 or is none."""
+    s = Step(tsd, 2, 2, 8, True, 0, alpha=alpha)
+    x = np.full((2, 2, 8), -np.inf)
+    x[..., 0] = 0  # each beam ends for certain: its total is its score
+    s.fill(x)
+    s.scores.copy_(dev_f32([[-3, -1.5], [-2, -4]]))
+    s.lengths.copy_(to_dev_i32([1, 2]))
+    s.run()
+    got = s.get()
+    assert got[3].tolist() == [[-1.5, -3], [0, 0] if alpha > 0 else [-np.inf, -np.inf]]
+    assert got[4].tolist() == [[1, 0], [2, 3] if alpha > 0 else [-7, -7]]
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_random_shapes(tsd, seed):
     """Sizes, alignments, ranges of logits, dead beams and forbidden tokens at random."""

@@ -410,7 +410,8 @@ __device__ __forceinline__ Pair length_penalty(int n, Pair alpha, int* exponent)
   const int64_t top = static_cast<int64_t>(n) + 5;
   const float h = static_cast<float>(top);
   constexpr float kLn6Hi = 0x1.cab0cp+0f, kLn6Lo = -2.1738742e-08f;
-  const Pair base = add(log_pair({h, static_cast<float>(top - static_cast<int64_t>(h))}), {-kLn6Hi, -kLn6Lo});
+  Pair base = add(log_pair({h, static_cast<float>(top - static_cast<int64_t>(h))}), {-kLn6Hi, -kLn6Lo});
+  if (n == 1) base = {0.f, 0.f};  // exactly, whatever alpha is
   float x = alpha.h * base.h;
   float rest = __fmaf_rn(alpha.h, base.h, -x) + (alpha.h * base.l + alpha.l * base.h);
   // e^300 and e^-300 take every score to 0 or beyond fp32 already
