@@ -681,7 +681,7 @@ cudaError_t launch_cache_release(const PagesProblem& p, const int32_t* keep_lens
 
 cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
   // lanes to a unit: for the most pages that a row's new tokens can touch
-  int64_t pages = ((static_cast<int64_t>(p.n_new) - 1) >> p.pages.page_shift) + 2;
+  int64_t pages = ((static_cast<int64_t>(p.n_new) - 2 + (1 << p.pages.page_shift)) >> p.pages.page_shift) + 1;
   if (pages > p.pages.max_pages) pages = p.pages.max_pages;
   int lanes_log2 = 0;
   while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
