@@ -792,8 +792,8 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  * score hold a NaN or +infinity has no candidates, and attn_get_device_status
  * answers ATTN_ERR_DEVICE_VALUE once. Totals are formed and compared in 48 bits
  * from exponentials and partial sums in 32. beams = 1 is greedy decoding.
- * Errors as attn_forward. Two launches, or one where sentences and vocabulary are
- * small.
+ * Errors as attn_forward. Two launches, or one where beams * ceil(vocab / 1024)
+ * is small (16 for hundreds of sentences, 64 for a hundred, 128 for eight).
  */
 size_t beam_select_workspace_bytes(int B, int beams, int vocab);
 attn_status beam_select(const void *logits, int64_t row_stride, const float *scores,

@@ -305,6 +305,25 @@ def test_one_token_has_no_penalty(tsd, alpha):
     assert got[4].tolist() == [[1, 0], [2, 3] if alpha > 0 else [-7, -7]]
 
 
+@pytest.mark.parametrize("B,V", [(1, v) for v in (17, 33, 96, 120, 128, 129, 300, 1000, 1024, 2000, 4100)]
+                         + [(30, v) for v in (33, 96, 128, 129, 1000, 2000, 4100)]
+                         + [(60, v) for v in (40, 129, 300, 2000, 4000)] + [(170, 96), (170, 1100), (310, 128), (310, 200)])
+@pytest.mark.parametrize("K", [7, 16])
+def test_few_tiles(tsd, B, K, V):
+    """One block, two, four and eight to a sentence, and two launches; fewer tiles than candidates: beams
+    alike, one far ahead of the others (all candidates in its row), equal rows."""
+    rng = np.random.default_rng(100 * B + 10 * K + V)
+    s = Step(tsd, B, K, V, bool((B + V) % 2), 2, pad=V % 3)
+    x = logits(rng, B, K, V)
+    x[B // 2:, :, :] = np.round(x[B // 2:, :1, :])  # equal rows, many equal logits
+    x = s.fill(x)
+    kind = np.arange(B)[:, None] % 3
+    scores = np.where(kind == 0, -rng.random((B, K)), np.where(kind == 1, -40.0 * np.arange(K), -0.137 * np.arange(K)))
+    s.scores.copy_(dev_f32(scores))
+    s.lengths.copy_(to_dev_i32(rng.integers(1, 30, B)))
+    check(s, x)
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_random_shapes(tsd, seed):
     """Sizes, alignments, ranges of logits, dead beams and forbidden tokens at random."""

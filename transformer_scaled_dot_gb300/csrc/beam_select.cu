@@ -16,8 +16,8 @@
 // is enough: a pair among the best M lies in one of the M tiles with the best
 // maxima (each tile ahead of its own holds a pair that beats it). beam_pick, a
 // block to a sentence, joins a row's tiles to its log-sum, picks those M tiles
-// and then the M pairs in them. Few short rows go through beam_one, which is
-// both in one launch.
+// and then the M pairs in them. Sentences of few tiles go through beam_one, which
+// is both in one launch.
 // Totals that lie next to one another decide which token a beam takes: they
 // are formed and compared as pairs of fp32, 48 bits. Exponentials and a tile's
 // sum are in 32, relative to the tile's own maximum, as are the few tiles of a
@@ -79,29 +79,35 @@ struct Tile {
       else word = past ? (word & 0xffff0000u) | 0xff80u : word;
     }
   }
+  // logit i, straight from memory
+  __device__ __forceinline__ void load_one(const void* row, int t, int i, int vocab, int lane) {
+    const int v = place(t, i, lane);
+    const uint32_t x = v < vocab ? one(row, v) : F32 ? 0xff800000u : 0xff80u;
+    if constexpr (F32) w[i] = x;
+    else w[i / 2 % kWords] = i & 1 ? w[i / 2 % kWords] | x << 16 : x;
+  }
   // straight from memory
   __device__ __forceinline__ void load(const void* row, int t, int vocab, int lane) {
     if constexpr (ALIGNED) {
-      if ((t + 1) * kTile <= vocab) {
 #pragma unroll
-        for (int j = 0; j < kWords / 4; ++j) {
-          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) +
-                                                          static_cast<int64_t>(place(t, j * kPer, lane)) * kSize);
+      for (int j = 0; j < kWords / 4; ++j) {
+        const int v = place(t, j * kPer, lane);
+        if (v + kPer <= vocab) {
+          const uint4 q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(row) + static_cast<int64_t>(v) * kSize);
           w[4 * j] = q.x;
           w[4 * j + 1] = q.y;
           w[4 * j + 2] = q.z;
           w[4 * j + 3] = q.w;
-        }
-        return;
-      }
-    }
-    constexpr uint32_t kNone = F32 ? 0xff800000u : 0xff80u;
+        } else if (v >= vocab) {
+          w[4 * j] = w[4 * j + 1] = w[4 * j + 2] = w[4 * j + 3] = F32 ? 0xff800000u : 0xff80ff80u;
+        } else {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const int v = place(t, i, lane);
-      const uint32_t x = v < vocab ? one(row, v) : kNone;
-      if constexpr (F32) w[i] = x;
-      else w[i / 2 % kWords] = i & 1 ? w[i / 2 % kWords] | x << 16 : x;
+          for (int e = 0; e < kPer; ++e) load_one(row, t, j * kPer + e, vocab, lane);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) load_one(row, t, i, vocab, lane);
     }
   }
 };
@@ -456,9 +462,19 @@ __device__ __forceinline__ uint64_t total_key(const Beam& beam, float x) {
 constexpr int kGroups = 64;     // of a sentence's tiles, or of the lanes of some
 constexpr int kSubs = kPickThreads / kGroups;  // threads of a group
 static_assert(kGroups == 2 * 32, "a group's lane");
+// Where a thread's entries of a list lie, every 512th from here: those of a group at
+// every 64th place or a few off, so that neighbours fall into different groups, and a
+// warp's in different banks.
+__device__ __forceinline__ int first_of_thread() {
+  const int sub = static_cast<int>(threadIdx.x) % kSubs, group = static_cast<int>(threadIdx.x) / kSubs;
+  return sub * kGroups + (group + sub * (32 / kSubs)) % kGroups;
+}
 constexpr int kListMost = 2048, kListStep = 3 * kPickThreads;
 constexpr int kTileList = 64;   // chosen tiles that are looked through
-constexpr int kPairList = kTileList * 2 * kBeamMaxBeams;
+constexpr int kPairList = 2 * kTileList * 2 * kBeamMaxBeams;
+constexpr int kSpare = kPairList / 2;  // of it, for tiles with more than M
+constexpr int kTileMost = 128;  // of one tile (a warp takes 6 us for 1024)
+constexpr int kFewPairs = 96;
 
 struct PickSmem {
   Beam beam[kBeamMaxBeams];
@@ -467,7 +483,8 @@ struct PickSmem {
   uint64_t last_key;           // the M-th best group's largest total, and its place
   int last_at;
   int n_tiles, n_pairs;
-  int crowded;                 // a tile has more than M pairs ahead of the last
+  int claimed;                 // pairs of tiles that have more than M not behind the last
+  int crowded;                 // they do not fit
   int tile[kListMost];         // chosen tiles
   uint64_t tile_key[kListMost];
   uint64_t pair_key[kPairList];
@@ -514,7 +531,7 @@ __device__ __noinline__ void keep_best_tiles(PickSmem& sm, int M) {
 // Groups of eight threads, each thread with its best (key 0: none), the places
 // all different: the M-th best group's best into sm.last_key and sm.last_at;
 // key 0 if so many groups have none.
-__device__ __noinline__ void last_of_groups(PickSmem& sm, uint64_t key, int at, int M) {
+__device__ __forceinline__ void last_of_groups(PickSmem& sm, uint64_t key, int at, int M) {
   const int tid = static_cast<int>(threadIdx.x);
 #pragma unroll
   for (int o = 1; o < kSubs; o <<= 1) {
@@ -545,6 +562,38 @@ __device__ __noinline__ void last_of_groups(PickSmem& sm, uint64_t key, int at, 
   if (before == M - 1 && key != 0 && tid % kSubs == 0) {
     sm.last_key = key;
     sm.last_at = at;
+  }
+  __syncthreads();
+}
+
+// Of the pairs those that are not behind the M-th best of 64 groups.
+__device__ __noinline__ void keep_best_pairs(PickSmem& sm, int M) {
+  constexpr int kMost = kPairList / kPickThreads;
+  const int tid = static_cast<int>(threadIdx.x), first = first_of_thread();
+  const int pairs = sm.n_pairs;
+  uint64_t key[kMost], best_key = 0;
+  int at[kMost], best_at = INT32_MAX;
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    key[j] = 0;
+    if (j * kPickThreads >= pairs) continue;
+    const int i = first + j * kPickThreads;
+    key[j] = i < pairs ? sm.pair_key[i] : 0;
+    at[j] = i < pairs ? sm.pair_at[i] : INT32_MAX;
+    if (ahead(key[j], at[j], best_key, best_at)) {
+      best_key = key[j];
+      best_at = at[j];
+    }
+  }
+  __syncthreads();
+  if (tid == 0) sm.n_pairs = 0;
+  last_of_groups(sm, best_key, best_at, M);
+#pragma unroll
+  for (int j = 0; j < kMost; ++j) {
+    if (key[j] == 0 || ahead(sm.last_key, sm.last_at, key[j], at[j])) continue;
+    const int to = atomicAdd(&sm.n_pairs, 1);
+    sm.pair_key[to] = key[j];
+    sm.pair_at[to] = at[j];
   }
   __syncthreads();
 }
@@ -598,6 +647,121 @@ __device__ __noinline__ uint32_t best_of_tile(const uint8_t* row, int t, int voc
   return above;
 }
 
+// i / tiles, given 1 / tiles: i is below 2^14, and (i + 1/2) / tiles at least 2^-11 off
+// a whole number.
+__device__ __forceinline__ int beam_of(int i, float per_tile) {
+  return static_cast<int>((static_cast<float>(i) + 0.5f) * per_tile);
+}
+
+// The logits of a sentence's beam k.
+template <bool F32>
+__device__ __forceinline__ const uint8_t* row_of(const BeamProblem& p, int b, int k) {
+  return static_cast<const uint8_t*>(p.logits) + (static_cast<int64_t>(b) * p.beams + k) * p.row_stride * (F32 ? 4 : 2);
+}
+
+// The pairs of the listed tiles that are not behind the last one, a warp to a tile,
+// the next one's logits on their way. AGAIN: at most M of a tile; else sm.crowded is
+// set where a tile has many or they do not fit in the list.
+template <bool F32, bool ALIGNED, bool AGAIN>
+__device__ __forceinline__ void list_pairs(const BeamProblem& p, int tiles, float per_tile, int b, PickSmem& sm, int M,
+                                           uint64_t least_key, int least_at) {
+  const int warp = warp_id(), lane = static_cast<int>(lane_id());
+  const int listed = sm.n_tiles;
+  Tile<F32, ALIGNED> next;
+  auto load = [&](int i) {
+    const int tile = sm.tile[i], k = beam_of(tile, per_tile);
+    next.load(row_of<F32>(p, b, k), tile - k * tiles, p.vocab, lane);
+  };
+  if (warp < listed) load(warp);
+#pragma unroll 1
+  for (int i = warp; i < listed; i += kPickWarps) {
+    const int tile = sm.tile[i], k = beam_of(tile, per_tile), t = tile - k * tiles;
+    const uint8_t* row = row_of<F32>(p, b, k);
+    const Tile<F32, ALIGNED> x = next;
+    if (i + kPickWarps < listed) load(i + kPickWarps);
+    const Beam beam = sm.beam[k];
+    // Logits below `least` are not among the best: the logit at which the
+    // last one's total is reached, less what this sum of 32 bits may be off.
+    const float last = key_total(least_key).h;
+    const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
+    float least = (last - beam.base.h) + beam.top - slack;
+    if (least_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
+    uint32_t in = 0u;  // of this lane's logits
+#pragma unroll
+    for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
+    const int count = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))));
+    if constexpr (AGAIN) {
+      if (count > kPairList / kTileList) in = best_of_tile<F32, ALIGNED>(row, t, p.vocab, M, lane);
+    } else if (count > M) {
+      int claimed = count > kTileMost ? kSpare + 1 : 0;
+      if (lane == 0 && claimed == 0) claimed = atomicAdd(&sm.claimed, count) + count;
+      if (__shfl_sync(0xffffffffu, claimed, 0) > kSpare) {
+        if (lane == 0) sm.crowded = 1;
+        break;
+      }
+    }
+#pragma unroll 1
+    for (; in != 0u; in &= in - 1u) {
+      const int v = Tile<F32, ALIGNED>::place(t, __ffs(in) - 1, lane);
+      const uint64_t key = total_key(beam, load_logit<F32>(row, v));
+      if (key == 0 || ahead(least_key, least_at, key, k * p.vocab + v)) continue;
+      const int at = atomicAdd(&sm.n_pairs, 1);
+      sm.pair_key[at] = key;
+      sm.pair_at[at] = k * p.vocab + v;
+    }
+  }
+}
+
+// Where a tile has many pairs (no more tiles than M, equal logits), the last one is
+// looked for again, among the best of each lane of each tile, and the
+// tiles once more.
+template <bool F32, bool ALIGNED>
+__device__ __noinline__ void look_again(const BeamProblem& p, int tiles, float per_tile, int b, PickSmem& sm, int M,
+                                         uint64_t least_key) {
+  const int tid = static_cast<int>(threadIdx.x), warp = warp_id(), lane = static_cast<int>(lane_id());
+  const int listed = sm.n_tiles;
+  int least_at = INT32_MAX;
+#pragma unroll 1
+  for (int i = warp; i < listed; i += kPickWarps) {
+    const int tile = sm.tile[i], k = beam_of(tile, per_tile), t = tile - k * tiles;
+    Tile<F32, ALIGNED> x;
+    x.load(row_of<F32>(p, b, k), t, p.vocab, lane);
+    float best = x.at(0);
+#pragma unroll
+    for (int j = 1; j < 32; ++j) best = fmaxf(best, x.at(j));
+    int best_v = INT32_MAX;
+#pragma unroll
+    for (int j = 31; j >= 0; --j) {
+      const int v = Tile<F32, ALIGNED>::place(t, j, lane);
+      if (x.at(j) == best && v < best_v) best_v = v;
+    }
+    const uint64_t key = best > -INFINITY ? total_key(sm.beam[k], best) : 0;
+    const int e = i * 32 + (lane + i) % 32;  // in a group's order in different banks
+    sm.pair_key[e] = key;
+    sm.pair_at[e] = key != 0 ? k * p.vocab + best_v : INT32_MAX;
+  }
+  if (tid == 0) sm.n_pairs = 0;
+  __syncthreads();
+  uint64_t key = 0;
+  int at = INT32_MAX;
+  // a group: one lane, every other tile (the best may all be in one tile)
+#pragma unroll 1
+  for (int i = tid / kSubs % 2 + 2 * (tid % kSubs); i < listed; i += 2 * kSubs) {
+    const int e = i * 32 + (tid / (2 * kSubs) + i) % 32;
+    if (ahead(sm.pair_key[e], sm.pair_at[e], key, at)) {
+      key = sm.pair_key[e];
+      at = sm.pair_at[e];
+    }
+  }
+  last_of_groups(sm, key, at, M);
+  if (sm.last_key != 0) {
+    least_key = sm.last_key;
+    least_at = sm.last_at;
+  }
+  list_pairs<F32, ALIGNED, true>(p, tiles, per_tile, b, sm, M, least_key, least_at);
+  __syncthreads();
+}
+
 // A sum of numbers of 0 .. 2^20 in all over a warp, off by 2^-25 at most: their parts
 // above and below 2^-6 as whole numbers, for which a warp has an instruction.
 __device__ __forceinline__ Pair warp_sum(float x) {
@@ -633,25 +797,17 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
   float score = -INFINITY, ended = -INFINITY;
   int end_row = 0, end_length = 0;
   if (warp < K) score = __ldcg(p.scores + b * K + warp);
-  if (p.end >= 0 && tid < K) {
-    ended = __ldcg(p.ended_scores + b * K + tid);
-    end_row = __ldcg(p.ended_rows + b * K + tid);
-    end_length = __ldcg(p.ended_lengths + b * K + tid);
+  if (p.end >= 0 && warp == 1 && lane < K) {
+    ended = __ldcg(p.ended_scores + b * K + lane);
+    end_row = __ldcg(p.ended_rows + b * K + lane);
+    end_length = __ldcg(p.ended_lengths + b * K + lane);
   }
   if (tid == 0) {
-    sm.n_tiles = sm.n_pairs = sm.crowded = 0;
+    sm.n_tiles = sm.n_pairs = sm.claimed = sm.crowded = 0;
   }
   if (tid < 2 * kBeamMaxBeams) sm.best_at[tid] = INT32_MAX;
-  if (warp == kPickWarps - 1 && p.end >= 0) {
-    int exponent;
-    const int length = max(__ldcg(p.lengths + b), 1);
-    const Pair penalty = length_penalty(length, {p.alpha, p.alpha_rest}, &exponent);
-    if (lane == 0) {
-      sm.length = length;
-      sm.penalty = penalty;
-      sm.penalty_exponent = exponent;
-    }
-  }
+  int length = 0;
+  if (warp == kPickWarps - 1 && p.end >= 0) length = max(__ldcg(p.lengths + b), 1);
   __syncthreads();
 
   // a row's log-sum, by a warp
@@ -677,18 +833,24 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
     }
     if (lane == 0) sm.beam[warp] = beam;
   }
+  if (warp == kPickWarps - 1 && p.end >= 0) {  // the last warp mostly has no row
+    int exponent;
+    const Pair penalty = length_penalty(length, {p.alpha, p.alpha_rest}, &exponent);
+    if (lane == 0) {
+      sm.length = length;
+      sm.penalty = penalty;
+      sm.penalty_exponent = exponent;
+    }
+  }
   __syncthreads();
 
-  // The tiles' largest totals, and the best of each group's: its eight threads
-  // take every 64th tile, so that likely tokens that lie close together fall into
-  // different groups.
-  // i / tiles: i is below 2^14, and (i + 1/2) / tiles at least 2^-11 off a whole number
+  // The tiles' largest totals, and the best of each group's.
   const float per_tile = __fdividef(1.f, static_cast<float>(tiles));
   uint64_t group_key = 0;
   int group_tile = INT32_MAX;
 #pragma unroll 1
-  for (int i = tid % kSubs * kGroups + tid / kSubs; i < n; i += kPickThreads) {
-    const Beam& beam = sm.beam[static_cast<int>((static_cast<float>(i) + 0.5f) * per_tile)];
+  for (int i = first_of_thread(); i < n; i += kPickThreads) {
+    const Beam& beam = sm.beam[beam_of(i, per_tile)];
     uint64_t key = 0;
     if (beam.base.h > -INFINITY) {
       const float x = reinterpret_cast<const float2*>(sm.key)[i].x;
@@ -725,100 +887,14 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
     if (more) __syncthreads();  // all have seen the count before it grows
   }
 
-  // Their pairs, a warp to a tile, the next one's logits on their way. Where a
-  // tile has more than M that are not behind the last (as with fewer tiles than M,
-  // or equal logits), the last is looked for again, among the best of each lane
-  // of each tile, and the tiles once more.
-  const int listed = sm.n_tiles;
-  auto row_of = [&](int k) {
-    return static_cast<const uint8_t*>(p.logits) + (static_cast<int64_t>(b) * K + k) * p.row_stride * (F32 ? 4 : 2);
-  };
-  uint64_t least_key = last_key;
-  int least_at = INT32_MAX;
-#pragma unroll 1
-  for (bool again = false;; again = true) {
-    Tile<F32, ALIGNED> next;
-    auto load = [&](int i) {
-      const int tile = sm.tile[i], k = tile / tiles;
-      next.load(row_of(k), tile - k * tiles, p.vocab, lane);
-    };
-    if (warp < listed) load(warp);
-#pragma unroll 1
-    for (int i = warp; i < listed; i += kPickWarps) {
-      const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
-      const uint8_t* row = row_of(k);
-      const Tile<F32, ALIGNED> x = next;
-      if (i + kPickWarps < listed) load(i + kPickWarps);
-      const Beam beam = sm.beam[k];
-      // Logits below `least` are not among the best: the logit at which the
-      // last one's total is reached, less what this sum of 32 bits may be off.
-      const float last = key_total(least_key).h;
-      const float slack = 0x1p-21f * (fabsf(last) + fabsf(beam.base.h) + fabsf(beam.top));
-      float least = (last - beam.base.h) + beam.top - slack;
-      if (least_key == 0 || !(least > -FLT_MAX)) least = -FLT_MAX;
-      uint32_t in = 0u;  // of this lane's logits
-#pragma unroll
-      for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
-      if (__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))) > static_cast<unsigned>(M)) {
-        if (!again) {
-          if (lane == 0) sm.crowded = 1;
-          break;
-        }
-        in = best_of_tile<F32, ALIGNED>(row, t, p.vocab, M, lane);
-      }
-#pragma unroll 1
-      for (; in != 0u; in &= in - 1u) {
-        const int v = Tile<F32, ALIGNED>::place(t, __ffs(in) - 1, lane);
-        const uint64_t key = total_key(beam, load_logit<F32>(row, v));
-        if (key == 0 || ahead(least_key, least_at, key, k * p.vocab + v)) continue;
-        const int at = atomicAdd(&sm.n_pairs, 1);
-        sm.pair_key[at] = key;
-        sm.pair_at[at] = k * p.vocab + v;
-      }
-    }
-    __syncthreads();
-    if (again || !sm.crowded) break;
+  // their pairs
+  const bool none = n <= M && p.vocab > kTileMost;  // the last one, if there is one, is the worst tile's best
+  if (!none) list_pairs<F32, ALIGNED, false>(p, tiles, per_tile, b, sm, M, last_key, INT32_MAX);
+  __syncthreads();
+  if (none || sm.crowded) look_again<F32, ALIGNED>(p, tiles, per_tile, b, sm, M, last_key);
 
-    // the best of each lane of each tile
-#pragma unroll 1
-    for (int i = warp; i < listed; i += kPickWarps) {
-      const int tile = sm.tile[i], k = tile / tiles, t = tile - k * tiles;
-      Tile<F32, ALIGNED> x;
-      x.load(row_of(k), t, p.vocab, lane);
-      float best = x.at(0);
-#pragma unroll
-      for (int j = 1; j < 32; ++j) best = fmaxf(best, x.at(j));
-      int best_v = INT32_MAX;
-#pragma unroll
-      for (int j = 31; j >= 0; --j) {
-        const int v = Tile<F32, ALIGNED>::place(t, j, lane);
-        if (x.at(j) == best && v < best_v) best_v = v;
-      }
-      const uint64_t key = best > -INFINITY ? total_key(sm.beam[k], best) : 0;
-      sm.pair_key[i * 32 + lane] = key;
-      sm.pair_at[i * 32 + lane] = key != 0 ? k * p.vocab + best_v : INT32_MAX;
-    }
-    if (tid == 0) sm.n_pairs = 0;
-    __syncthreads();
-    uint64_t key = 0;
-    int at = INT32_MAX;
-    // a group: one lane, every other tile (the best may all be in one tile)
-#pragma unroll 1
-    for (int i = tid / kSubs % 2 + 2 * (tid % kSubs); i < listed; i += 2 * kSubs) {
-      const int e = i * 32 + tid / (2 * kSubs);
-      if (ahead(sm.pair_key[e], sm.pair_at[e], key, at)) {
-        key = sm.pair_key[e];
-        at = sm.pair_at[e];
-      }
-    }
-    last_of_groups(sm, key, at, M);
-    if (sm.last_key != 0) {
-      least_key = sm.last_key;
-      least_at = sm.last_at;
-    }
-  }
-
-  // the best M in order
+  // the best M in order (ranks cost the square of the pairs: of 512 40 us)
+  if (sm.n_pairs > kFewPairs) keep_best_pairs(sm, M);
   const int pairs = sm.n_pairs;
 #pragma unroll 1
   for (int i = warp; i < pairs; i += kPickWarps) {
@@ -829,30 +905,34 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
     }
   }
   __syncthreads();
-  if (warp != 0) return;
+  if (warp > 1) return;
 
-  // a lane to a candidate: the next beams
+  // a lane to a candidate
   const int pair = lane < M ? sm.best_at[lane] : INT32_MAX;
   const bool real = pair != INT32_MAX;
   const Pair total = real ? key_total(sm.best_key[lane]) : Pair{0.f, 0.f};
   const int beam = real ? pair / p.vocab : 0, token = real ? pair - beam * p.vocab : 0;
   const bool ends = real && token == p.end;
   const uint32_t before = (1u << lane) - 1u;
-  const uint32_t going = __ballot_sync(0xffffffffu, real && !ends), ending = __ballot_sync(0xffffffffu, ends);
-  const int rank = __popc(going & before);
-  if (real && !ends && rank < K) {
-    p.tokens[b * K + rank] = token;
-    p.parents[b * K + rank] = b * K + beam;
-    p.new_scores[b * K + rank] = total.h;
-  }
-  if (lane < K && lane >= __popc(going)) {  // no pair for this beam
-    p.tokens[b * K + lane] = p.end >= 0 ? p.end : 0;
-    p.parents[b * K + lane] = b * K + lane;
-    p.new_scores[b * K + lane] = -INFINITY;
+  if (warp == 0) {  // the next beams
+    const uint32_t going = __ballot_sync(0xffffffffu, real && !ends);
+    const int rank = __popc(going & before);
+    if (real && !ends && rank < K) {
+      p.tokens[b * K + rank] = token;
+      p.parents[b * K + rank] = b * K + beam;
+      p.new_scores[b * K + rank] = total.h;
+    }
+    if (lane < K && lane >= __popc(going)) {  // no pair for this beam
+      p.tokens[b * K + lane] = p.end >= 0 ? p.end : 0;
+      p.parents[b * K + lane] = b * K + lane;
+      p.new_scores[b * K + lane] = -INFINITY;
+    }
+    return;
   }
   if (p.end < 0) return;
 
   // the ended hypotheses: lanes below 16 hold the earlier ones, the others this step's
+  const uint32_t ending = __ballot_sync(0xffffffffu, ends);
   if (ends) {
     // the quotient of two pairs, rounded once, and the exponent in four steps
     const Pair by = sm.penalty;
@@ -902,36 +982,60 @@ __global__ void __launch_bounds__(kPickThreads) beam_pick_kernel(const BeamProbl
                      static_cast<const uint64_t*>(p.workspace) + static_cast<int64_t>(blockIdx.x) * p.beams * tiles);
 }
 
-// Few short sentences in one launch: a cluster to a sentence, whose warps take
-// its tiles straight from memory and write their records into the first block's
-// shared memory, which then chooses. For up to a tile to a warp and 8 sentences:
-// 4 beams of 32000 tokens 6.5 us (two launches 6.9, and 2 us more on the host), 8
-// sentences of them 6.65 (7.0), 16 of them 8.1 (7.35: the clusters do not all fit);
-// 8 beams, two tiles to a warp, 10.4 (9.0).
+// Few tiles to a sentence in one launch: a block to a sentence, or a cluster of 2 to 8
+// whose warps have a tile or two each. They take the tiles straight from memory and
+// write their records into the first block's shared memory, which then chooses. In us,
+// by blocks to a sentence, against two launches (and 2 us less on the host):
+//   16 tiles   8 sentences 1: 7.5, two launches 9.0; 300: 15.9, 18.2
+//   32         8 2: 6.3, 1: 6.9, two 7.0; 64 2: 7.6, 1: 7.0, two 7.8; 200 1: 14.0, two 14.1
+//   64         8 4: 6.4, 2: 7.3, two 7.0; 64 4: 13.9, 2: 8.4, two 8.5; 150 1: 9.2, two 10.9
+//   128        8 8: 6.5, 4: 7.3, two 6.9; 16 8: 9.5 (not all clusters fit), 4: 7.5, two 7.4
 constexpr int kOneCtas = 8;
-constexpr int kOneSentences = 8, kOneTiles = kOneCtas * kPickWarps;
 template <bool F32, bool ALIGNED>
-__global__ void __launch_bounds__(kPickThreads) beam_one_kernel(const BeamProblem p, int tiles) {
+__global__ void __launch_bounds__(kPickThreads) beam_one_kernel(const BeamProblem p, int tiles, int ctas) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
   PickSmem& sm = *reinterpret_cast<PickSmem*>(smem_raw);
-  cluster_sync();  // every block has begun: the first one's shared memory may be written
+  if (ctas > 1) cluster_sync();  // every block has begun: the first one's shared memory may be written
   griddep_wait();
   griddep_launch_dependents();
-  const int b = static_cast<int>(blockIdx.x) / kOneCtas, rank = static_cast<int>(cluster_ctarank());
+  const int b = static_cast<int>(blockIdx.x) / ctas, rank = ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int lane = static_cast<int>(lane_id());
   const int n = p.beams * tiles;
-  for (int i = warp_id() * kOneCtas + rank; i < n; i += kOneCtas * kPickWarps) {
+  for (int i = warp_id() * ctas + rank; i < n; i += ctas * kPickWarps) {
     const int k = i / tiles, row = b * p.beams + k;
     Tile<F32, ALIGNED> x;
     x.load(static_cast<const uint8_t*>(p.logits) + row * (p.row_stride * (F32 ? 4 : 2)), i - k * tiles, p.vocab, lane);
     if (__ldcg(p.scores + row) == -INFINITY) continue;
     const float2 record = tile_record(x);
-    if (lane == 0)
-      st_cluster_u64(cluster_map(&sm.key[i], 0),
-                     static_cast<uint64_t>(__float_as_uint(record.y)) << 32 | __float_as_uint(record.x));
+    const uint64_t bits = static_cast<uint64_t>(__float_as_uint(record.y)) << 32 | __float_as_uint(record.x);
+    if (lane == 0) {
+      if (ctas > 1) st_cluster_u64(cluster_map(&sm.key[i], 0), bits);
+      else sm.key[i] = bits;
+    }
   }
-  cluster_sync();
+  if (ctas > 1) cluster_sync();
+  else __syncthreads();
   if (rank == 0) pick<F32, ALIGNED>(p, tiles, b, sm, nullptr);
+}
+
+// Blocks to a sentence of n tiles, or 0: two launches.
+int one_launch_blocks(int B, int n, int sms) {
+  if (n <= 16) return B <= 2 * sms ? 1 : 0;
+  if (n <= 32 && B <= 48) return 2;
+  if (n <= 64) return B <= 24 ? 4 : n > 32 && B <= 64 ? 2 : B <= sms ? 1 : 0;
+  return n <= kOneCtas * kPickWarps && B <= 8 ? kOneCtas : 0;
+}
+
+int sm_count() {
+  static int cached = 0;  // atomic accesses: launches may come from several host threads
+  int n = __atomic_load_n(&cached, __ATOMIC_RELAXED);
+  if (n == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      return 1;
+    __atomic_store_n(&cached, n, __ATOMIC_RELAXED);
+  }
+  return n;
 }
 
 template <bool F32, bool ALIGNED>
@@ -943,12 +1047,13 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   constexpr int kPickMost = static_cast<int>(sizeof(PickSmem)) + kBeamMaxBeams * (kBeamMaxVocab / kTile) * 8;
   static_assert(kPickMost <= 227 * 1024, "shared memory of a block");
   const size_t pick_bytes = sizeof(PickSmem) + static_cast<size_t>(p.beams) * tiles * sizeof(uint64_t);
-  if (p.B <= kOneSentences && p.beams * tiles <= kOneTiles) {
+  const int ctas = one_launch_blocks(p.B, p.beams * tiles, sm_count());
+  if (ctas > 0) {
     static unsigned long long one_configured = 0;
     cudaError_t e = set_smem_once(beam_one_kernel<F32, ALIGNED>, kPickMost, &one_configured);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B * kOneCtas));
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B * ctas));
     cfg.blockDim = dim3(kPickThreads);
     cfg.dynamicSmemBytes = pick_bytes;
     cfg.stream = stream;
@@ -956,12 +1061,12 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kOneCtas;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(ctas);
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, beam_one_kernel<F32, ALIGNED>, p, tiles);
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, beam_one_kernel<F32, ALIGNED>, p, tiles, ctas);
   }
   static unsigned long long tiles_configured = 0, pick_configured = 0;
   cudaError_t e = set_smem_once(beam_tiles_kernel<F32, ALIGNED>, kRingBytes, &tiles_configured);
@@ -970,13 +1075,10 @@ cudaError_t launch_variant(const BeamProblem& p, cudaStream_t stream) {
   static int resident = 0;  // blocks on the device
   int fit = __atomic_load_n(&resident, __ATOMIC_RELAXED);
   if (fit == 0) {
-    int dev = 0, sms = 0, per_sm = 0;
-    e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess)
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, beam_tiles_kernel<F32, ALIGNED>, 32 * kTileWarps, kRingBytes);
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, beam_tiles_kernel<F32, ALIGNED>, 32 * kTileWarps, kRingBytes);
     if (e != cudaSuccess) return e;
-    fit = sms * (per_sm > 0 ? per_sm : 1);
+    fit = sm_count() * (per_sm > 0 ? per_sm : 1);
     __atomic_store_n(&resident, fit, __ATOMIC_RELAXED);
   }
   const int total = p.B * p.beams * ((tiles + R::U - 1) / R::U);
