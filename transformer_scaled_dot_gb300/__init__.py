@@ -171,14 +171,19 @@ def library():
     return lib
 
 
+_tensor_types = set()  # that have had a data_ptr()
+
+
 def _ptr(x):
     """Address of a torch tensor (device or host), a numpy array (host), or an int."""
-    if x is None or type(x) is int:
+    if type(x) in _tensor_types:
+        return x.data_ptr()
+    if x is None or isinstance(x, int):
         return x
-    data_ptr = getattr(x, "data_ptr", None)
-    if data_ptr is not None:
-        return data_ptr()
-    return x if isinstance(x, int) else x.ctypes.data
+    if not hasattr(x, "data_ptr"):
+        return x.ctypes.data
+    _tensor_types.add(type(x))
+    return x.data_ptr()
 
 
 _raw_stream = _device = None  # torch's, from the first call that finds CUDA up
@@ -202,7 +207,7 @@ def _current_stream():
 
 def _stream(s):
     if s is None:
-        return _current_stream()
+        return _current_stream() if _raw_stream is None else _raw_stream(_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
