@@ -717,7 +717,7 @@ attn_status attn_cache_reserve(int32_t *page_table, int32_t *ref_counts, const i
  *   n_copies, n_used  int32[1], written: the moves, and U
  *   workspace   as attn_cache_reserve
  * All entries of tables that name pages of the pool have to be in page_table.
- * Two launches (one for B = 0).
+ * Two launches, or one where the table is small.
  */
 attn_status attn_cache_compact(const int32_t *page_table, const int32_t *ref_counts,
                                int32_t *table_out, int32_t *counts_out, int32_t *copies,
