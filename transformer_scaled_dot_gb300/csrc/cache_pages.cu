@@ -608,7 +608,7 @@ int sm_count() {
 // step with shared pages and 13000 pages in one block 15.6, in two 18.0; a step with
 // 65536 in eight 6.5, in four 7.1, in one 7.9; 64 prompts with 262144 in 16 12.5, in
 // eight 17.6.) One block has no more threads than that takes, as it waits for its
-// barriers: a step of 16 rows with 1000 pages takes 10.0 with its fork and copies,
+// barriers: a step of 128 rows with 973 pages takes 10 with its fork and copies,
 // with 1024 threads 11.2.
 struct Shape {
   unsigned ctas, threads;
