@@ -598,11 +598,12 @@ __device__ __noinline__ void keep_best_pairs(PickSmem& sm, int M) {
   __syncthreads();
 }
 
-// Which of its logits of a tile with at least M a lane has among the best M, the
-// lowest places first among equals: the M-th largest, bit by bit of its place in
-// the numbers' order, then the equal ones from the front. 2 us for any M.
+// Which of its logits of a tile with at least M a lane has among the best M, by total
+// and then by place: the M-th largest logit, bit by bit of its place in the
+// numbers' order; what has a larger total; then of what has the same one (logits that
+// differ by less than its 48 bits are equal) from the front. 2 us for any M.
 template <bool F32, bool ALIGNED>
-__device__ __noinline__ uint32_t best_of_tile(const uint8_t* row, int t, int vocab, int M, int lane) {
+__device__ __noinline__ uint32_t best_of_tile(Beam beam, const uint8_t* row, int t, int vocab, int M, int lane) {
   constexpr int kPer = Tile<F32, ALIGNED>::kPer;
   Tile<F32, ALIGNED> x;
   x.load(row, t, vocab, lane);
@@ -622,11 +623,28 @@ __device__ __noinline__ uint32_t best_of_tile(const uint8_t* row, int t, int voc
     at_least = n;
   }
   const float last = from_order_bits(order);
+  // Equal totals have logits nearer than this: each total is off by less than 3 2^-48 of it.
+  const float near = 0x1p-44f * (fabsf(beam.base.h) + fabsf(beam.top) + fabsf(last));
   uint32_t above = 0u, equal = 0u;
+  bool close = false;
 #pragma unroll
   for (int j = 0; j < 32; ++j) {
     above |= (x.at(j) > last ? 1u : 0u) << j;
     equal |= (x.at(j) == last ? 1u : 0u) << j;
+    close |= x.at(j) != last && fabsf(x.at(j) - last) <= near;
+  }
+  // Then by the totals (3 us). Above are at most M, and with the equal ones M or more,
+  // whatever the totals' last bits are.
+  if (__any_sync(0xffffffffu, close)) {
+    const uint64_t last_key = total_key(beam, last);
+    above = equal = 0u;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const uint64_t key = total_key(beam, x.at(j));
+      const bool over = x.at(j) > last && key > last_key;
+      above |= (over ? 1u : 0u) << j;
+      equal |= (!over && key != 0 && (x.at(j) >= last || key >= last_key) ? 1u : 0u) << j;
+    }
   }
   int left = M - static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(above))));
   // places go by vectors of kPer, then by lanes
@@ -691,7 +709,7 @@ __device__ __forceinline__ void list_pairs(const BeamProblem& p, int tiles, floa
     for (int j = 0; j < 32; ++j) in |= (x.at(j) >= least ? 1u : 0u) << j;
     const int count = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(__popc(in))));
     if constexpr (AGAIN) {
-      if (count > kPairList / kTileList) in = best_of_tile<F32, ALIGNED>(row, t, p.vocab, M, lane);
+      if (count > kPairList / kTileList) in = best_of_tile<F32, ALIGNED>(beam, row, t, p.vocab, M, lane);
     } else if (count > M) {
       int claimed = count > kTileMost ? kSpare + 1 : 0;
       if (lane == 0 && claimed == 0) claimed = atomicAdd(&sm.claimed, count) + count;
