@@ -1,0 +1,20 @@
+"""What the host decides about a beam selection and the cache's pages, and what their sources keep to (CPU only)."""
+import os
+import re
+
+import pytest
+
+import transformer_scaled_dot_gb300 as tsd
+
+CSRC = os.path.join(os.path.dirname(os.path.abspath(tsd.__file__)), "csrc")
+
+
+@pytest.mark.parametrize("name", ["beam_select.cu", "cache_pages.cu", "cache_copy.cu", "cache_append.cu", "attn_paged.cu"])
+def test_no_loads_through_the_read_only_path(name):
+    """These kernels begin while the launch before them, which may write what they read (beam_select the parents,
+    fork the lengths), still runs. The read-only path is for memory that nobody writes in a kernel's life: neither
+    its loads nor pointers that allow the compiler to use them."""
+    with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    assert "griddep_wait" in code
+    assert not re.search(r"\b__ldg\b|ld\.global(\.\w+)*\.nc|\b__restrict__\b", code)
