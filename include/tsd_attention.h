@@ -772,7 +772,8 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  *               are). At a sentence's start: 0, and -infinity for the others
  *   lengths     int32[B]: tokens of the hypotheses, the one chosen now among
  *               them (less than 1 counts as 1)
- *   alpha       finite (a double: 0.6 is no number of 32 bits)
+ *   alpha       within fp32's range, else ATTN_ERR_INVALID (a double: 0.6 is no
+ *               number of 32 bits)
  *   end         the end token, or -1: none; then lengths, alpha and the ended_*
  *               arrays are ignored
  *   tokens, parents  int32[B, beams], written: the token, and the row b * beams

@@ -5,6 +5,7 @@ import re
 import pytest
 
 import transformer_scaled_dot_gb300 as tsd
+from test_cache_pages_abi import BEAM, lib  # noqa: F401 (the fixture)
 
 CSRC = os.path.join(os.path.dirname(os.path.abspath(tsd.__file__)), "csrc")
 
@@ -18,3 +19,11 @@ def test_no_loads_through_the_read_only_path(name):
         code = re.sub(r"//[^\n]*", "", f.read())
     assert "griddep_wait" in code
     assert not re.search(r"\b__ldg\b|ld\.global(\.\w+)*\.nc|\b__restrict__\b", code)
+
+
+@pytest.mark.parametrize("name", ["beam_select", "beam_select_f32"])
+def test_alpha_is_ignored_without_an_end_token(lib, name):  # noqa: F811
+    for alpha in (float("nan"), float("inf"), -float("inf"), 1e300):
+        args = {**BEAM, "B": 0, "end": -1, "alpha": alpha}
+        assert getattr(lib, name)(*args.values()) == tsd.ATTN_OK, alpha
+        assert getattr(lib, name)(*{**args, "end": 2}.values()) == tsd.ATTN_ERR_INVALID, alpha

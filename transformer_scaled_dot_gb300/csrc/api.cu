@@ -806,7 +806,7 @@ attn_status run_beam_select(const void* logits, bool f32, int64_t row_stride, co
   if (s != ATTN_OK) return s;
   if (row_stride < vocab || row_stride > INT64_MAX / 8 / (int64_t(B) * beams + 1)) return ATTN_ERR_INVALID;
   const float alpha_high = static_cast<float>(alpha);
-  if (end < -1 || !std::isfinite(alpha_high)) return ATTN_ERR_INVALID;
+  if (end < -1 || (end >= 0 && !std::isfinite(alpha_high))) return ATTN_ERR_INVALID;
   if (!logits || (reinterpret_cast<uintptr_t>(logits) & (f32 ? 3u : 1u))) return ATTN_ERR_INVALID;
   for (const void* p : {static_cast<const void*>(scores), static_cast<const void*>(tokens),
                         static_cast<const void*>(parents), static_cast<const void*>(new_scores)})
