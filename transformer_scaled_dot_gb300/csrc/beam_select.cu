@@ -952,12 +952,16 @@ __device__ __forceinline__ void pick(const BeamProblem& p, int tiles, int b, Pic
   // the ended hypotheses: lanes below 16 hold the earlier ones, the others this step's
   const uint32_t ending = __ballot_sync(0xffffffffu, ends);
   if (ends) {
-    // the quotient of two pairs, rounded once, and the exponent in four steps
+    // the quotient of two pairs, rounded once, and the exponent in four steps; of a
+    // total near the lowest number (a masked end token's) a quarter is divided, as over a
+    // value below 1 it is infinite where with the exponent it is not
     const Pair by = sm.penalty;
-    const float q = __fdividef(total.h, by.h);
-    const float rest = __fmaf_rn(-q, by.h, total.h) + (total.l - q * by.l);
+    const bool large = fabsf(total.h) > 0x1p100f;
+    const float h = large ? 0.25f * total.h : total.h, l = large ? 0.25f * total.l : total.l;
+    const float q = __fdividef(h, by.h);
+    const float rest = __fmaf_rn(-q, by.h, h) + (l - q * by.l);
     float value = q + __fdividef(rest, by.h);
-    int exponent = -sm.penalty_exponent;  // within 433
+    int exponent = (large ? 2 : 0) - sm.penalty_exponent;  // within 435
 #pragma unroll
     for (int j = 4; j > 0; --j) {
       const int part = exponent / j;
