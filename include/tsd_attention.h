@@ -681,10 +681,11 @@ attn_status attn_cache_release(int32_t *page_table, int32_t *ref_counts, const i
  * and belongs to its row alone. The positions are cache_lens[b] - new_lens[b]
  * .. cache_lens[b] - 1; of the pages that hold them,
  *   a missing one is taken from the free pages;
- *   one that other entries name too is left, and a free page taken in its
- *   place. Where all that name it are rows of this call that write it, the
- *   first of them keeps it. If the page holds earlier rows of the sequence (its
- *   first page can), a copy of them is listed.
+ *   one that other entries name too, of this row or another, is left, and a
+ *   free page taken in its place. Where all that name it are entries that this
+ *   call's tokens are written into, the first of them (by row, then by place)
+ *   keeps it. If the page holds earlier rows of the sequence (its first page
+ *   can), a copy of them is listed.
  *   copies      int32[B, 3], written: (from page, to page, rows), in the order
  *               of the sequences; entries past n_copies[0] are left as they were.
  *               attn_cache_copy carries them out: no page is both from and to
@@ -694,7 +695,9 @@ attn_status attn_cache_release(int32_t *page_table, int32_t *ref_counts, const i
  *               names no page may be -1 afterwards)
  *   workspace   device, 16-byte aligned, >= attn_cache_pages_workspace_bytes(B,
  *               n_pages) bytes of scratch (0 for sizes that the calls refuse)
- * Positions past max_pages * page_size get no page. One launch.
+ * Positions past max_pages * page_size get no page. B times the pages that
+ * n_new tokens of a row can lie in (max_pages at most) is at most 2^31, else
+ * ATTN_ERR_UNSUPPORTED. One launch.
  */
 size_t attn_cache_pages_workspace_bytes(int B, int n_pages);
 attn_status attn_cache_reserve(int32_t *page_table, int32_t *ref_counts, const int32_t *cache_lens,

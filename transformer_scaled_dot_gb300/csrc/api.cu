@@ -1288,9 +1288,11 @@ attn_status attn_cache_reserve(int32_t* page_table, int32_t* ref_counts, const i
     if (!p || !aligned4(p)) return ATTN_ERR_INVALID;
   if (!workspace || !aligned16(workspace) || workspace_bytes < attn_cache_pages_workspace_bytes(B, n_pages))
     return ATTN_ERR_INVALID;
+  const int width = tsd::reserve_width(n_new, log2_int(page_size), max_pages);
+  if (int64_t(B) * width > int64_t(1) << 31) return ATTN_ERR_UNSUPPORTED;
   if (B == 0) return ATTN_OK;
   const tsd::ReserveProblem p = {{page_table, ref_counts, B, n_pages, log2_int(page_size), max_pages},
-                                 cache_lens, new_lens, n_new, copies, n_copies, n_missing,
+                                 cache_lens, new_lens, n_new, width, copies, n_copies, n_missing,
                                  static_cast<int32_t*>(workspace)};
   cudaError_t e = tsd::launch_cache_reserve(p, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);

@@ -308,18 +308,19 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
 
   // a lane's page of a unit
   struct Place {
-    int row, rows;  // rows: of earlier tokens in the page, if it is the first to be written
+    uint32_t id;    // in the order of the rows and of their pages, below 2^31
+    int rows;       // of earlier tokens in the page, if it is the first to be written
     int entry;
     int32_t* at;    // the entry's address; null: no page
   };
   auto look_up = [&](int row, int unit, bool is) {
     Place q = {0, 0, 0, nullptr};
     if (!is) return q;
-    q.row = row;
     const RowRange r = row_range(p, row);
-    const int k = r.first + (unit << lanes_log2 | sub);
-    q.rows = k == r.first ? r.rows : 0;
-    if (k < r.last) q.at = pg.table + static_cast<int64_t>(q.row) * pg.max_pages + k;
+    const int i = unit << lanes_log2 | sub, k = r.first + i;
+    q.id = static_cast<uint32_t>(row) * static_cast<uint32_t>(p.width) + static_cast<uint32_t>(i);
+    q.rows = i == 0 ? r.rows : 0;
+    if (k < r.last) q.at = pg.table + static_cast<int64_t>(row) * pg.max_pages + k;
     return q;
   };
   const Slice slice = warp_slice(pg.n_pages, rank, ctas);
@@ -393,19 +394,20 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
   uint32_t free_at = static_cast<uint32_t>(first.w);  // free pages before this warp's
   const bool sharing = all.w >> 32 != 0;
   uint64_t page_at = first.v, copy_at = 0, wanted = all.v, n_copies = 0;
-  auto keeps = [&](const Place& q) { return __ldcg(pg.counts + marked_page(q.entry)) == INT32_MIN + q.row; };
-  bool kept = false;  // ONE: the lane's page is shared, and its row keeps it
+  auto keeper = [](const Place& q) { return static_cast<int>(0x80000000u + q.id); };  // below 0
+  auto keeps = [&](const Place& q) { return __ldcg(pg.counts + marked_page(q.entry)) == keeper(q); };
+  bool kept = false;  // ONE: the lane's page is shared, and its entry keeps it
   if (sharing) {
-    // Every row leaves the shared pages that it writes. Where that takes a
-    // page's count to 0, the first of them keeps it after all: its number is
-    // left in the count.
+    // Every entry to be written leaves its shared page. Where that takes a page's
+    // count to 0, the first of them keeps it after all: its number is left in the
+    // count. (The entry's, not its row's: a row may name a page more than once.)
     for_pages(Single{}, [&](Place* q, auto) {
       if (q->at && marked(q->entry)) atomicSub(pg.counts + marked_page(q->entry), 1);
     });
     sync_all(ctas);
     for_pages(Single{}, [&](Place* q, auto) {
       if (q->at && marked(q->entry) && __ldcg(pg.counts + marked_page(q->entry)) <= 0)
-        atomicMin(pg.counts + marked_page(q->entry), INT32_MIN + q->row);
+        atomicMin(pg.counts + marked_page(q->entry), keeper(*q));
     });
     sync_all(ctas);
     need = 0;
@@ -472,12 +474,12 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     constexpr int U = decltype(n)::value;
     int page[U];
     int32_t* copy[U];
-    bool keeper[U], wants[U];
+    bool stays[U], wants[U];
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const bool shared = q[j].at && marked(q[j].entry);
-      keeper[j] = shared && (ONE ? kept : keeps(q[j]));
-      wants[j] = most > 0 && q[j].at && (q[j].entry == -1 || (shared && !keeper[j]));
+      stays[j] = shared && (ONE ? kept : keeps(q[j]));
+      wants[j] = most > 0 && q[j].at && (q[j].entry == -1 || (shared && !stays[j]));
       const bool copies = wants[j] && shared && q[j].rows > 0;
       const uint32_t want_vote = __ballot_sync(kAll, wants[j]), copy_vote = __ballot_sync(kAll, copies);
       // (only a table that its counts do not fit could want more than was counted)
@@ -489,8 +491,8 @@ __global__ void __launch_bounds__(kClusterThreads) cache_reserve_kernel(const Re
     }
 #pragma unroll
     for (int j = 0; j < U; ++j) {
-      if (!wants[j] && !keeper[j]) continue;
-      const int was = marked_page(q[j].entry), now = keeper[j] ? was : page[j];
+      if (!wants[j] && !stays[j]) continue;
+      const int was = marked_page(q[j].entry), now = stays[j] ? was : page[j];
       *q[j].at = now;
       pg.counts[now] = 1;
       if (copy[j]) {
@@ -705,12 +707,10 @@ cudaError_t launch_cache_release(const PagesProblem& p, const int32_t* keep_lens
 }
 
 cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream) {
-  // lanes to a unit: for the most pages that a row's new tokens can touch
-  int64_t pages = ((static_cast<int64_t>(p.n_new) - 2 + (1 << p.pages.page_shift)) >> p.pages.page_shift) + 1;
-  if (pages > p.pages.max_pages) pages = p.pages.max_pages;
+  // lanes to a unit: for the most pages that a row's new tokens can lie in
   int lanes_log2 = 0;
-  while (lanes_log2 < 5 && (1 << lanes_log2) < pages) ++lanes_log2;
-  const int units = static_cast<int>((pages + (1 << lanes_log2) - 1) >> lanes_log2);
+  while (lanes_log2 < 5 && (1 << lanes_log2) < p.width) ++lanes_log2;
+  const int units = (p.width + (1 << lanes_log2) - 1) >> lanes_log2;
   const int64_t threads = (static_cast<int64_t>(p.pages.B) * units) << lanes_log2;
   static unsigned known_one[kDevices], known_many[kDevices];
   unsigned most_one = 0, most_many = 0;

@@ -292,11 +292,17 @@ struct ReserveProblem {
   const int32_t* lens;
   const int32_t* new_lens;  // or null: n_new each
   int n_new;
+  int width;          // pages that a row's new tokens can lie in at most; B * width <= 2^31
   int32_t* copies;    // [B, 3]: from page, to page, rows
   int32_t* n_copies;
   int32_t* n_missing;
   int32_t* free_ids;  // workspace [n_pages]
 };
+// The width for so many new tokens.
+inline int reserve_width(int n_new, int page_shift, int max_pages) {
+  const int64_t page = int64_t(1) << page_shift, pages = ((n_new - 2 + page) >> page_shift) + 1;
+  return pages < max_pages ? static_cast<int>(pages) : max_pages;
+}
 cudaError_t launch_cache_reserve(const ReserveProblem& p, cudaStream_t stream);
 struct CompactProblem {
   PagesProblem pages;  // read
