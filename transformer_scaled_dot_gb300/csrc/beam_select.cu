@@ -113,8 +113,8 @@ struct Tile {
 };
 
 // A warp's ring of units of U tiles in shared memory, filled by bulk copies: one
-// thread starts 2 or 4 KB. They move 16-byte blocks of memory; a row that starts
-// `skew` bytes into one has one block more to a unit.
+// thread starts 4 KB, less at a row's end. They move 16-byte blocks of memory; a row
+// that starts `skew` bytes into one has one block more to a unit.
 template <bool F32, bool ALIGNED>
 struct Ring {
   using T = Tile<F32, ALIGNED>;
@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(32 * kTileWarps, 6)
   constexpr int U = R::U;
   using T = Tile<F32, ALIGNED>;
   static_assert(sizeof(R) % 16 == 0 && R::kStageBytes % 16 == 0, "copies into shared memory start on 16 bytes");
+  static_assert(R::kStages == 2, "the first copy ahead of the loop, the second by its first round");
   extern __shared__ __align__(16) uint8_t smem_raw[];
   R& ring = reinterpret_cast<R*>(smem_raw)[warp_id()];
   __shared__ uint32_t abort_word;
@@ -297,8 +298,6 @@ __global__ void __launch_bounds__(32 * kTileWarps, 6)
   uint32_t live = 0u;  // bit i: the unit i after the one at hand has a hypothesis
 #pragma unroll
   for (int i = 0; i < R::kStages; ++i) live |= (scores[i] != -INFINITY ? 1u : 0u) << i;
-#pragma unroll
-  for (int i = 1; i < R::kStages - 1; ++i) copy(i, live >> i & 1u);
   uint32_t parity = 0u;  // bit s: of stage s
   bool ok = true;
   for (int s = 0; id < total; id += step) {
