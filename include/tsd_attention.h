@@ -495,6 +495,7 @@ attn_status attn_decode_host_async(const void *q_host, const void *k_cache,
  *   h_kv        key/value heads, a divisor of h: query head i reads key head
  *               i / (h / h_kv)
  *   d           64 or 128 (else ATTN_ERR_UNSUPPORTED), of keys and values
+ *   B, h        at most 65535, else ATTN_ERR_INVALID
  *
  * A bf16 cache is two pools [n_pages, h_kv, page_size, d] of bf16. A 4-bit
  * cache holds each of keys and values as
@@ -637,10 +638,11 @@ attn_status attn_decode_paged_q4(const void *q, const void *k_codes, const void 
  * access out of range. An entry or a number that is out of range is left out and
  * attn_get_device_status answers ATTN_ERR_DEVICE_INDEX once. Calls that change
  * the same ref_counts have to be ordered by their stream.
- *   page_size, max_pages, B: as above; n_pages <= 2^30, else ATTN_ERR_UNSUPPORTED
+ *   page_size, max_pages: as above; n_pages <= 2^30, else ATTN_ERR_UNSUPPORTED
+ *   B           at most 65535, else ATTN_ERR_INVALID. B = 0 launches nothing and
+ *               writes nothing (but for attn_cache_compact)
  *   every array: device memory, 4-byte aligned; a null or misaligned pointer
- *   or a bad size -> ATTN_ERR_INVALID. B = 0 launches nothing (but for
- *   attn_cache_compact)
+ *   or a bad size -> ATTN_ERR_INVALID
  *
  * A step of beam search over a paged cache is
  *   attn_cache_fork(table, lens, counts, parents, ...)  the rows beam_select chose
@@ -735,10 +737,13 @@ attn_status attn_cache_compact(const int32_t *page_table, const int32_t *ref_cou
  *   k_cache, v_cache  the first layer's pools [n_pages, h_kv, page_size, d]
  *               bf16; layer i's begin layer_rows * i rows of d columns further on
  *   copies      int32[max_copies, 3]; n_copies int32[1], how many of them there
- *               are (clamped to [0, max_copies]), or NULL: all
- *   n_layers    >= 0; layer_rows a multiple of 16, >= n_pages * h_kv * page_size
- *               (ignored for one layer), else ATTN_ERR_INVALID
- *   h_kv * page_size * d <= 2^29, else ATTN_ERR_UNSUPPORTED
+ *               are (clamped to [0, max_copies]; above it is out of range), or
+ *               NULL: all
+ *   n_layers    0 .. 65535; layer_rows a multiple of 16, >= n_pages * h_kv *
+ *               page_size, and times n_layers at most 2^50 (ignored for one
+ *               layer), else ATTN_ERR_INVALID
+ *   h_kv        1 .. 65535, else ATTN_ERR_INVALID; h_kv * page_size * d <= 2^29,
+ *               else ATTN_ERR_UNSUPPORTED
  * No page may be `to` of two copies, or `from` of one and `to` of another. A
  * copy with a number out of range is left out. One launch.
  */
@@ -777,8 +782,8 @@ attn_status attn_cache_copy_q4(void *k_codes, void *k_scales, void *v_codes, voi
  *               them (less than 1 counts as 1)
  *   alpha       within fp32's range, else ATTN_ERR_INVALID (a double: 0.6 is no
  *               number of 32 bits)
- *   end         the end token, or -1: none; then lengths, alpha and the ended_*
- *               arrays are ignored
+ *   end         the end token (one from vocab on is never chosen), or -1: none;
+ *               then lengths, alpha and the ended_* arrays are ignored
  *   tokens, parents  int32[B, beams], written: the token, and the row b * beams
  *               + k that it continues (as attn_cache_fork takes it)
  *   new_scores  fp32[B, beams], written: totals; may be `scores` itself.
